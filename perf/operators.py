@@ -7,7 +7,8 @@ E2M1 (fp4, two to a byte, the even element in the low half) or E4M3 (fp8).
 The scale is the smallest power of two under which the block's largest
 magnitude does not exceed the largest code (6 or 448); codes round to the
 nearest value, ties to the even code.  Rows are padded with zero codes to a
-multiple of 128 elements.
+multiple of 128 elements; the scale bytes of a row's 128 elements lie together,
+those of the next row behind them: scales[column // 128, row, column // 32 % 4].
 
 The operators, in a linear layer's order of use:
 
@@ -215,7 +216,8 @@ def _held(x, fmt):
         man = a * torch.exp2(3.0 - ex.float())
         c = torch.where(man < 8, man, (ex + 6).float() * 8 + man).to(torch.uint8)
         c = c + torch.signbit(v).to(torch.uint8) * 128
-    return {"rows": x.shape[0], "cols": x.shape[1], "fmt": fmt, "codes": c.contiguous(), "scales": e.contiguous()}
+    return {"rows": x.shape[0], "cols": x.shape[1], "fmt": fmt, "codes": c.contiguous(),
+            "scales": e.view(e.shape[0], -1, 4).transpose(0, 1).contiguous()}
 
 
 def _values(h):
@@ -230,7 +232,7 @@ def _values(h):
         ex = (n >> 3).clamp(min=1)
         man = torch.where(n < 8, n, (n & 7) + 8)
         a = man.float() * torch.exp2(ex.float() - 10)
-    s = torch.exp2(h["scales"].float() - 127).repeat_interleave(32, 1)
+    s = torch.exp2(h["scales"].transpose(0, 1).flatten(1).float() - 127).repeat_interleave(32, 1)
     return (torch.where(sign == 1, -a, a) * s)[:, :h["cols"]]
 
 
@@ -341,7 +343,8 @@ def _stored(h):
         wide = torch.empty(raw.shape[0], 2 * raw.shape[1], dtype=torch.long, device=raw.device)
         wide[:, 0::2], wide[:, 1::2] = raw % 16, raw // 16
         raw = wide
-    blocks = table[raw].view(raw.shape[0], -1, 32) * torch.exp2(h["scales"].double() - 127)[:, :, None]
+    power = torch.exp2(h["scales"].double() - 127).permute(1, 0, 2).reshape(raw.shape[0], -1, 1)
+    blocks = table[raw].view(raw.shape[0], -1, 32) * power
     return blocks.reshape(raw.shape[0], -1)[:, :h["cols"]]
 
 
