@@ -19,4 +19,11 @@ from .api import (  # noqa: F401
     RULE_STATE_RTN, RULE_STATE_SR, RULE_UPDATE_RTN, RULE_UPDATE_SR,
     HP_REUSE_TABLE, HP_CHECK_POINTERS, HP_GRAD_STATS, ACC_FIRST, ACC_LAST, ACC_REUSE_TABLE, TF_LM_HEAD,
 )
+from .api import (  # noqa: F401
+    Q4MXMatrix, q4mx_matrix_bytes, q4mx_quantize, q4mx_dequantize, q4mx_linear, q4mx_linear_workspace_bytes,
+    q4mx_linear_bf16, q4mx_linear_bf16_workspace_bytes, q4mx_dgrad, q4mx_dgrad_workspace_bytes, q4mx_wgrad,
+    q4mx_wgrad_workspace_bytes, q4mx_act_forward, q4mx_act_backward, MX_FP4, MX_FP8, MX_F32, MX_BF16, MX_GELU,
+    MX_GELU_ERF, MX_SWIGLU, MX_WGRAD_TRANSPOSED, MX_WGRAD_ADD, MX_FEW_TOKENS,
+)
 from .state import Q4State, RECIPE_BY_NAME  # noqa: F401
+from . import mx  # noqa: F401

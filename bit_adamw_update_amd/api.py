@@ -19,6 +19,11 @@ ACC_FIRST, ACC_LAST, ACC_REUSE_TABLE = 1, 2, 4
 TF_LM_HEAD = 1
 ABI_VERSION = 3
 MAX_NDIM = 8
+MX_FP4, MX_FP8 = range(2)
+MX_F32, MX_BF16 = range(2)
+MX_GELU, MX_GELU_ERF, MX_SWIGLU = range(3)
+MX_WGRAD_TRANSPOSED, MX_WGRAD_ADD = 1, 2
+MX_FEW_TOKENS = 16
 
 STATUS = {0: "Q4_OK", 1: "Q4_ERR_INVALID_ARG", 2: "Q4_ERR_SHAPE", 3: "Q4_ERR_ALIGNMENT", 4: "Q4_ERR_CONFLICT",
           5: "Q4_ERR_STATE_FORMAT", 6: "Q4_ERR_DEVICE", 7: "Q4_ERR_WORKSPACE", 8: "Q4_ERR_HIP"}
@@ -56,6 +61,11 @@ class Q4StateHeader(C.Structure):
                 ("m_rule", C.c_int32), ("v_rule", C.c_int32), ("eden", C.c_int32), ("block", C.c_int32)]
 
 
+class Q4MXMatrix(C.Structure):
+    _fields_ = [("format", C.c_int32), ("reserved", C.c_int32), ("rows", C.c_int64), ("cols", C.c_int64),
+                ("codes", C.c_void_p), ("scales", C.c_void_p)]
+
+
 class Q4Error(RuntimeError):
     def __init__(self, status: int, message: str):
         super().__init__(f"{STATUS.get(status, status)}: {message}")
@@ -91,6 +101,28 @@ _SIGNATURES = {
     "q4adamw_grad_stats": ([C.POINTER(Q4Config), C.POINTER(Q4Tensor), C.c_int32, C.c_void_p, C.c_size_t,
                            C.c_void_p], C.c_int),
     "q4adamw_grad_norm": ([C.c_void_p, C.c_size_t, C.POINTER(C.c_double), C.c_void_p], C.c_int),
+    "q4mx_matrix_bytes": ([C.c_int32, C.c_int64, C.c_int64, C.POINTER(C.c_size_t), C.POINTER(C.c_size_t)], C.c_int),
+    "q4mx_quantize": ([C.c_void_p, C.c_int32, C.c_int64, C.c_int32, C.POINTER(Q4MXMatrix), C.c_void_p], C.c_int),
+    "q4mx_dequantize": ([C.POINTER(Q4MXMatrix), C.c_void_p, C.c_int32, C.c_int64, C.c_void_p], C.c_int),
+    "q4mx_linear": ([C.POINTER(Q4MXMatrix), C.POINTER(Q4MXMatrix), C.c_void_p, C.c_int32, C.c_int64, C.c_void_p,
+                     C.c_size_t, C.c_void_p], C.c_int),
+    "q4mx_linear_workspace_bytes": ([C.POINTER(Q4MXMatrix), C.POINTER(Q4MXMatrix), C.POINTER(C.c_size_t)], C.c_int),
+    "q4mx_linear_bf16": ([C.c_void_p, C.c_int64, C.c_int64, C.POINTER(Q4MXMatrix), C.c_void_p, C.c_int32, C.c_int64,
+                          C.c_void_p, C.c_size_t, C.c_void_p], C.c_int),
+    "q4mx_linear_bf16_workspace_bytes": ([C.c_int64, C.POINTER(Q4MXMatrix), C.POINTER(C.c_size_t)], C.c_int),
+    "q4mx_dgrad": ([C.c_void_p, C.c_int64, C.c_int64, C.POINTER(Q4MXMatrix), C.c_void_p, C.c_int32, C.c_int64,
+                    C.c_void_p, C.c_size_t, C.c_void_p], C.c_int),
+    "q4mx_dgrad_workspace_bytes": ([C.c_void_p, C.c_int64, C.c_int64, C.POINTER(Q4MXMatrix),
+                                    C.POINTER(C.c_size_t)], C.c_int),
+    "q4mx_wgrad": ([C.c_void_p, C.c_int64, C.c_int64, C.POINTER(Q4MXMatrix), C.c_void_p, C.c_int32, C.c_int64,
+                    C.c_int32, C.c_void_p, C.c_size_t, C.c_void_p], C.c_int),
+    "q4mx_wgrad_workspace_bytes": ([C.c_void_p, C.c_int64, C.c_int64, C.POINTER(Q4MXMatrix), C.c_int32,
+                                    C.POINTER(C.c_size_t)], C.c_int),
+    "q4mx_act_forward": ([C.c_int32, C.c_void_p, C.c_int64, C.c_void_p, C.c_int64, C.c_int64, C.c_int64, C.c_void_p,
+                          C.c_int64, C.POINTER(Q4MXMatrix), C.POINTER(Q4MXMatrix), C.POINTER(Q4MXMatrix),
+                          C.c_void_p], C.c_int),
+    "q4mx_act_backward": ([C.c_int32, C.POINTER(Q4MXMatrix), C.POINTER(Q4MXMatrix), C.c_void_p, C.c_int64,
+                           C.c_void_p, C.c_int64, C.c_void_p, C.c_int64, C.c_void_p], C.c_int),
 }
 
 
@@ -258,3 +290,87 @@ def q4adamw_grad_norm(ws, ws_bytes: int | None = None, stream=None) -> float:
     out = C.c_double()
     _check(load_library().q4adamw_grad_norm(_ptr(ws), ws_bytes, C.byref(out), _stream(stream)))
     return out.value
+
+
+# ---- microscaled matrices (dense operands as pointer, row stride) -----------
+
+def _mx(m):
+    return C.byref(m) if m is not None else None
+
+
+def _ws(ws, ws_bytes):
+    return (ws.numel() * ws.element_size() if ws is not None else 0) if ws_bytes is None else ws_bytes
+
+
+def q4mx_matrix_bytes(fmt: int, rows: int, cols: int) -> tuple[int, int]:
+    codes, scales = C.c_size_t(), C.c_size_t()
+    _check(load_library().q4mx_matrix_bytes(fmt, rows, cols, C.byref(codes), C.byref(scales)))
+    return codes.value, scales.value
+
+
+def q4mx_quantize(src, dtype: int, ld: int, transpose: bool, out: Q4MXMatrix, stream=None) -> None:
+    _check(load_library().q4mx_quantize(_ptr(src), dtype, ld, int(transpose), _mx(out), _stream(stream)))
+
+
+def q4mx_dequantize(a: Q4MXMatrix, dst, dtype: int, ld: int, stream=None) -> None:
+    _check(load_library().q4mx_dequantize(_mx(a), _ptr(dst), dtype, ld, _stream(stream)))
+
+
+def q4mx_linear_workspace_bytes(x: Q4MXMatrix, w: Q4MXMatrix) -> int:
+    out = C.c_size_t()
+    _check(load_library().q4mx_linear_workspace_bytes(_mx(x), _mx(w), C.byref(out)))
+    return out.value
+
+
+def q4mx_linear(x: Q4MXMatrix, w: Q4MXMatrix, y, dtype: int, ldy: int, ws=None, ws_bytes: int | None = None,
+                stream=None) -> None:
+    _check(load_library().q4mx_linear(_mx(x), _mx(w), _ptr(y), dtype, ldy, _ptr(ws), _ws(ws, ws_bytes),
+                                      _stream(stream)))
+
+
+def q4mx_linear_bf16_workspace_bytes(tokens: int, w: Q4MXMatrix) -> int:
+    out = C.c_size_t()
+    _check(load_library().q4mx_linear_bf16_workspace_bytes(tokens, _mx(w), C.byref(out)))
+    return out.value
+
+
+def q4mx_linear_bf16(x, ldx: int, tokens: int, w: Q4MXMatrix, y, dtype: int, ldy: int, ws=None,
+                     ws_bytes: int | None = None, stream=None) -> None:
+    _check(load_library().q4mx_linear_bf16(_ptr(x), ldx, tokens, _mx(w), _ptr(y), dtype, ldy, _ptr(ws),
+                                           _ws(ws, ws_bytes), _stream(stream)))
+
+
+def q4mx_dgrad_workspace_bytes(dy, lddy: int, tokens: int, w: Q4MXMatrix) -> int:
+    out = C.c_size_t()
+    _check(load_library().q4mx_dgrad_workspace_bytes(_ptr(dy), lddy, tokens, _mx(w), C.byref(out)))
+    return out.value
+
+
+def q4mx_dgrad(dy, lddy: int, tokens: int, w: Q4MXMatrix, dx, dtype: int, lddx: int, ws=None,
+               ws_bytes: int | None = None, stream=None) -> None:
+    _check(load_library().q4mx_dgrad(_ptr(dy), lddy, tokens, _mx(w), _ptr(dx), dtype, lddx, _ptr(ws),
+                                     _ws(ws, ws_bytes), _stream(stream)))
+
+
+def q4mx_wgrad_workspace_bytes(dy, lddy: int, n: int, x: Q4MXMatrix, flags: int = 0) -> int:
+    out = C.c_size_t()
+    _check(load_library().q4mx_wgrad_workspace_bytes(_ptr(dy), lddy, n, _mx(x), flags, C.byref(out)))
+    return out.value
+
+
+def q4mx_wgrad(dy, lddy: int, n: int, x: Q4MXMatrix, dw, dtype: int, lddw: int, flags: int = 0, ws=None,
+               ws_bytes: int | None = None, stream=None) -> None:
+    _check(load_library().q4mx_wgrad(_ptr(dy), lddy, n, _mx(x), _ptr(dw), dtype, lddw, flags, _ptr(ws),
+                                     _ws(ws, ws_bytes), _stream(stream)))
+
+
+def q4mx_act_forward(act: int, x, ldx: int, up, ldup: int, rows: int, cols: int, y, ldy: int, y_mx=None, kept_x=None,
+                     kept_up=None, stream=None) -> None:
+    _check(load_library().q4mx_act_forward(act, _ptr(x), ldx, _ptr(up), ldup, rows, cols, _ptr(y), ldy, _mx(y_mx),
+                                           _mx(kept_x), _mx(kept_up), _stream(stream)))
+
+
+def q4mx_act_backward(act: int, kept_x: Q4MXMatrix, kept_up, dy, lddy: int, dx, lddx: int, dup=None, lddup: int = 0,
+                      stream=None) -> None:
+    _check(load_library().q4mx_act_backward(act, _mx(kept_x), _mx(kept_up), _ptr(dy), lddy, _ptr(dx), lddx,
+                                            _ptr(dup), lddup, _stream(stream)))

@@ -439,6 +439,17 @@ q4_status prepare(const q4_config* cfg, const q4_tensor* t, int32_t n, bool need
 
 }  // namespace
 
+namespace q4 {
+
+int report(int status, const char* message) {
+    if (!message) return ok();
+    return fail((q4_status)status, "%s", message);
+}
+
+int current_device(int* dev) { return check_device(dev); }
+
+}  // namespace q4
+
 extern "C" {
 
 uint32_t q4adamw_abi_version(void) { return Q4ADAMW_ABI_VERSION; }

@@ -155,4 +155,11 @@ constexpr size_t kScratchBytes = size_t(32) << 20;
 hipError_t scratch_address(void** ptr);
 void codebook_table(int cb, float* out);  // 16 entries, 256 for the 8-bit maps
 
+// The ABI's error state, for entry points in other files (a q4_status in an
+// int): stores the message of this thread's last call (NULL: none) and
+// returns `status`.
+int report(int status, const char* message);
+// Q4_OK and the current device's index if a gfx950 device is current.
+int current_device(int* dev);
+
 }  // namespace q4

@@ -1,0 +1,46 @@
+// q4_mx.h -- shared by the host entry points (q4_mx_abi.cpp) and the kernels
+// (q4_mx_elem.hip, q4_mx_gemm.hip) of the microscaled linear layer.  Not
+// part of the public C ABI.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "../../include/q4adamw.h"
+
+namespace q4 {
+
+constexpr int64_t kMxPad = 128;  // columns of a row are padded to this many
+
+// An MX matrix as the kernels see it.
+struct MxMat {
+    uint8_t* codes;
+    uint8_t* scales;
+    int64_t rows, cols;
+    int64_t slices;  // P / 128
+    int fmt;         // q4mx_format
+};
+
+// A dense row-major matrix: element (r, c) at p[r * ld + c].
+struct Dense {
+    void* p;
+    int64_t ld;
+    int dtype;  // q4mx_dtype
+};
+
+hipError_t launch_mx_quantize(const Dense& src, bool transpose, const MxMat& out, hipStream_t st);
+hipError_t launch_mx_dequantize(const MxMat& a, const Dense& dst, hipStream_t st);
+// y, y_mx, kx, ku: absent where their pointer (codes) is NULL.
+hipError_t launch_act_forward(int act, const Dense& x, const Dense& up, int64_t rows, int64_t cols, const Dense& y,
+                              const MxMat& y_mx, const MxMat& kx, const MxMat& ku, hipStream_t st);
+hipError_t launch_act_backward(int act, const MxMat& kx, const MxMat& ku, const Dense& dy, const Dense& dx,
+                               const Dense& dup, hipStream_t st);
+
+// The three products.  add: the result is added to what out holds.
+hipError_t launch_linear(const MxMat& x, const MxMat& w, const Dense& y, hipStream_t st);
+hipError_t launch_dgrad(const Dense& dy, int64_t tokens, const MxMat& w, const Dense& dx, hipStream_t st);
+hipError_t launch_wgrad(const Dense& dy, int64_t n, const MxMat& x, const Dense& dw, bool transposed, bool add,
+                        hipStream_t st);
+
+}  // namespace q4

@@ -1,0 +1,274 @@
+"""The microscaled linear layer on torch tensors.
+
+``MXMatrix`` owns the codes and scales of a matrix in a microscaled format
+(see "microscaled matrices" in ``include/q4adamw.h``); the functions allocate
+results and workspaces with torch and forward to the ``q4mx_*`` calls.  They
+compute nothing themselves.
+
+A linear layer beside ``Q4State``, for a master stored [in, out]::
+
+    w = mx.quantize(master, "fp4", transpose=True)       # after every step
+    xq = mx.quantize(x, "fp8")                           # kept for backward
+    y = mx.linear(xq, w)
+    ...
+    dx = mx.linear_dgrad(dy, w)
+    mx.linear_wgrad(dy, xq, out=grad, transposed=True)   # the BF16 gradient
+
+The calls run on ``stream`` (a torch stream), or on the current stream of
+their operands' device.  They are not recorded by autograd: the backward
+calls are the layer's backward pass.
+"""
+from __future__ import annotations
+
+import contextlib
+
+import torch
+
+from . import api
+
+FORMATS = {"fp4": api.MX_FP4, "fp8": api.MX_FP8}
+ACTIVATIONS = {"gelu": api.MX_GELU, "gelu_erf": api.MX_GELU_ERF, "swiglu": api.MX_SWIGLU}
+_DTYPES = {torch.float32: api.MX_F32, torch.bfloat16: api.MX_BF16}
+
+
+class MXMatrix:
+    """rows x cols values in format "fp4" or "fp8".
+
+    codes:  uint8 [rows, P / 2] ("fp4") or [rows, P], P = cols rounded up to
+            a multiple of 128;
+    scales: uint8 [P / 128, rows, 4].
+    """
+    __slots__ = ("rows", "cols", "format", "codes", "scales", "desc")
+
+    def __init__(self, rows: int, cols: int, format: str, codes=None, scales=None, device="cuda"):
+        if format not in FORMATS:
+            raise ValueError(f"unknown format {format!r}; expected one of {sorted(FORMATS)}")
+        api.q4mx_matrix_bytes(FORMATS[format], rows, cols)   # refuses sizes out of range
+        slices = (cols + 127) // 128
+        shapes = ((rows, slices * (64 if format == "fp4" else 128)), (slices, rows, 4))
+        if (codes is None) != (scales is None):
+            raise ValueError("codes and scales come together")
+        if codes is None:
+            codes, scales = (torch.empty(s, dtype=torch.uint8, device=device) for s in shapes)
+        for name, t, shape in (("codes", codes, shapes[0]), ("scales", scales, shapes[1])):
+            if t.dtype != torch.uint8 or tuple(t.shape) != shape or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous uint8 tensor of shape {shape}")
+            if not t.is_cuda:
+                raise ValueError(f"{name} must be on a GPU")
+        if codes.device != scales.device:
+            raise ValueError("codes and scales must be on one device")
+        self.rows, self.cols, self.format, self.codes, self.scales = rows, cols, format, codes, scales
+        self.desc = api.Q4MXMatrix(FORMATS[format], 0, rows, cols, codes.data_ptr(), scales.data_ptr())
+
+    @property
+    def shape(self) -> tuple:
+        return (self.rows, self.cols)
+
+    @property
+    def device(self):
+        return self.codes.device
+
+    def __repr__(self) -> str:
+        return f"MXMatrix({self.rows} x {self.cols}, {self.format!r}, device='{self.device}')"
+
+
+def _dense(name, t, dtypes=(torch.bfloat16,)):
+    """A 2-D GPU tensor with consecutive columns; returns its row stride."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise ValueError(f"{name} must be a 2-D tensor")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, not {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a GPU")
+    rows, cols = t.shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have consecutive columns (stride 1)")
+    # the stride of a single row, or of an empty matrix, means nothing
+    return t.stride(0) if rows > 1 and cols > 0 else max(1, cols)
+
+
+def _matrix(name, m):
+    if not isinstance(m, MXMatrix):
+        raise ValueError(f"{name} must be an MXMatrix")
+    return m
+
+
+def _result(out, shape, dtype, device):
+    if out is None:
+        if dtype not in _DTYPES:
+            raise ValueError(f"dtype must be torch.float32 or torch.bfloat16, not {dtype}")
+        out = torch.empty(shape, dtype=dtype, device=device)
+    ld = _dense("out", out, tuple(_DTYPES))
+    if tuple(out.shape) != tuple(shape):
+        raise ValueError(f"out must have shape {tuple(shape)}, not {tuple(out.shape)}")
+    if out.shape[0] > 1 and ld < out.shape[1]:
+        raise ValueError("out's rows overlap")
+    return out, _DTYPES[out.dtype], ld
+
+
+def _mx_result(out, rows, cols, fmt, device):
+    if out is None:
+        return MXMatrix(rows, cols, fmt, device=device)
+    if _matrix("out", out).shape != (rows, cols) or out.format != fmt:
+        raise ValueError(f"out must be a {rows} x {cols} MXMatrix in {fmt!r}")
+    return out
+
+
+def _same_device(*operands):
+    device = operands[0].device
+    for t in operands:
+        if t is not None and t.device != device:
+            raise ValueError(f"the operands are on different devices ({device} and {t.device})")
+    return device
+
+
+@contextlib.contextmanager
+def _on(device, stream):
+    with torch.cuda.device(device):
+        if stream is None:
+            yield
+        else:
+            with torch.cuda.stream(stream):
+                yield
+
+
+def _workspace(nbytes, device):
+    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+
+
+def quantize(src, format: str, transpose: bool = False, out: MXMatrix | None = None, stream=None) -> MXMatrix:
+    """src (float32 or bfloat16) in a microscaled format, blocks along its
+    columns; transpose: the quantized transpose, blocks along its rows (a
+    weight whose master is stored [in, out])."""
+    ld = _dense("src", src, tuple(_DTYPES))
+    if format not in FORMATS:
+        raise ValueError(f"unknown format {format!r}; expected one of {sorted(FORMATS)}")
+    rows, cols = src.shape[::-1] if transpose else src.shape
+    device = _same_device(src, out)
+    with _on(device, stream):
+        out = _mx_result(out, rows, cols, format, device)
+        api.q4mx_quantize(src, _DTYPES[src.dtype], ld, transpose, out.desc)
+    return out
+
+
+def dequantize(a: MXMatrix, dtype=torch.bfloat16, out=None, stream=None) -> torch.Tensor:
+    """The values of a."""
+    device = _same_device(_matrix("a", a), out)
+    with _on(device, stream):
+        out, code, ld = _result(out, a.shape, dtype, device)
+        api.q4mx_dequantize(a.desc, out, code, ld)
+    return out
+
+
+def linear(x, w: MXMatrix, out=None, dtype=torch.bfloat16, stream=None) -> torch.Tensor:
+    """x w^T: x an MXMatrix [tokens, in] or a bfloat16 tensor (quantized to
+    "fp8" on the way), w an MXMatrix [out, in] in "fp4"."""
+    device = _same_device(x, _matrix("w", w), out)
+    if isinstance(x, MXMatrix):
+        with _on(device, stream):
+            out, code, ld = _result(out, (x.rows, w.rows), dtype, device)
+            ws = _workspace(api.q4mx_linear_workspace_bytes(x.desc, w.desc), device)
+            api.q4mx_linear(x.desc, w.desc, out, code, ld, ws)
+        return out
+    ldx = _dense("x", x)
+    if x.shape[1] != w.cols:
+        raise ValueError(f"x has {x.shape[1]} columns, w has {w.cols}")
+    tokens = x.shape[0]
+    with _on(device, stream):
+        out, code, ld = _result(out, (tokens, w.rows), dtype, device)
+        ws = _workspace(api.q4mx_linear_bf16_workspace_bytes(tokens, w.desc), device)
+        api.q4mx_linear_bf16(x, ldx, tokens, w.desc, out, code, ld, ws)
+    return out
+
+
+def linear_dgrad(dy, w: MXMatrix, out=None, dtype=torch.bfloat16, stream=None) -> torch.Tensor:
+    """dy w: the gradient of linear's x, dy bfloat16 [tokens, out]."""
+    lddy = _dense("dy", dy)
+    device = _same_device(dy, _matrix("w", w), out)
+    if dy.shape[1] != w.rows:
+        raise ValueError(f"dy has {dy.shape[1]} columns, w has {w.rows} rows")
+    tokens = dy.shape[0]
+    with _on(device, stream):
+        out, code, ld = _result(out, (tokens, w.cols), dtype, device)
+        ws = _workspace(api.q4mx_dgrad_workspace_bytes(dy, lddy, tokens, w.desc), device)
+        api.q4mx_dgrad(dy, lddy, tokens, w.desc, out, code, ld, ws)
+    return out
+
+
+def linear_wgrad(dy, x: MXMatrix, out=None, transposed: bool = False, accumulate: bool = False,
+                 dtype=torch.bfloat16, stream=None) -> torch.Tensor:
+    """dy^T x [out, in], or with transposed its transpose [in, out], from the
+    checkpoint x: the gradient of linear's w.  accumulate: added to out."""
+    lddy = _dense("dy", dy)
+    device = _same_device(dy, _matrix("x", x), out)
+    if dy.shape[0] != x.rows:
+        raise ValueError(f"dy has {dy.shape[0]} rows, x has {x.rows}")
+    if accumulate and out is None:
+        raise ValueError("accumulate needs out")
+    n = dy.shape[1]
+    flags = (api.MX_WGRAD_TRANSPOSED if transposed else 0) | (api.MX_WGRAD_ADD if accumulate else 0)
+    with _on(device, stream):
+        out, code, ld = _result(out, (x.cols, n) if transposed else (n, x.cols), dtype, device)
+        ws = _workspace(api.q4mx_wgrad_workspace_bytes(dy, lddy, n, x.desc, flags), device)
+        api.q4mx_wgrad(dy, lddy, n, x.desc, out, code, ld, flags, ws)
+    return out
+
+
+def _activation(kind):
+    if kind not in ACTIVATIONS:
+        raise ValueError(f"unknown activation {kind!r}; expected one of {sorted(ACTIVATIONS)}")
+    return ACTIVATIONS[kind]
+
+
+def act_forward(kind: str, x, up=None, out_format: str | None = None, stream=None):
+    """(y, kept): y = f(x) for "gelu" (tanh form) and "gelu_erf", x / (1 +
+    e^-x) * up for "swiglu", as a bfloat16 tensor or, with out_format, as an
+    MXMatrix (the next linear layer's operand); kept is what act_backward
+    needs, the inputs in 8 bits."""
+    act = _activation(kind)
+    ldx = _dense("x", x)
+    if (up is not None) != (kind == "swiglu"):
+        raise ValueError('"swiglu" takes up, the others do not')
+    ldup = 0
+    if up is not None:
+        ldup = _dense("up", up)
+        if up.shape != x.shape:
+            raise ValueError("x and up must have one shape")
+    if out_format is not None and out_format not in FORMATS:
+        raise ValueError(f"unknown format {out_format!r}; expected one of {sorted(FORMATS)}")
+    device = _same_device(x, up)
+    rows, cols = x.shape
+    with _on(device, stream):
+        y = y_mx = kept_up = None
+        ldy = 0
+        if out_format is None:
+            y = torch.empty((rows, cols), dtype=torch.bfloat16, device=device)
+            ldy = max(1, cols)
+        else:
+            y_mx = MXMatrix(rows, cols, out_format, device=device)
+        kept_x = MXMatrix(rows, cols, "fp8", device=device)
+        if up is not None:
+            kept_up = MXMatrix(rows, cols, "fp8", device=device)
+        api.q4mx_act_forward(act, x, ldx, up, ldup, rows, cols, y, ldy, y_mx.desc if y_mx is not None else None,
+                             kept_x.desc, kept_up.desc if kept_up is not None else None)
+    return (y if y_mx is None else y_mx), (kept_x, kept_up)
+
+
+def act_backward(kind: str, kept, dy, stream=None) -> tuple:
+    """(dx,) or, for "swiglu", (dx, dup), from act_forward's kept."""
+    act = _activation(kind)
+    kept_x, kept_up = kept
+    _matrix("kept[0]", kept_x)
+    if (kept_up is not None) != (kind == "swiglu"):
+        raise ValueError('"swiglu" keeps up, the others do not')
+    lddy = _dense("dy", dy)
+    if tuple(dy.shape) != kept_x.shape:
+        raise ValueError(f"dy must have shape {kept_x.shape}, not {tuple(dy.shape)}")
+    device = _same_device(dy, kept_x, kept_up)
+    ld = max(1, dy.shape[1])
+    with _on(device, stream):
+        dx = torch.empty(dy.shape, dtype=torch.bfloat16, device=device)
+        dup = torch.empty_like(dx) if kept_up is not None else None
+        api.q4mx_act_backward(act, kept_x.desc, kept_up.desc if kept_up is not None else None, dy, lddy, dx, ld, dup,
+                              ld)
+    return (dx,) if dup is None else (dx, dup)

@@ -340,6 +340,135 @@ q4_status q4adamw_grad_norm(const void* ws, size_t ws_bytes, double* norm, void*
 q4_status q4adamw_dequant_state(const q4_config* cfg, const q4_tensor* t, float* m_out, float* v_out,
                                 void* ws, size_t ws_bytes, void* stream);
 
+/* ---- microscaled matrices: the low-bit linear layer --------------------
+ * The step leaves FP32 masters and takes BF16 gradients; these calls are the
+ * linear layer between them.  Its weights are the masters in 4 bits, its
+ * activations are kept in 8 bits from the forward to the backward pass, and
+ * its weight gradient lands in (or is added to) a tensor's BF16 gradient:
+ *
+ *   w  = quantize(master)            4-bit weights, after every step
+ *   xq = quantize(x)                 the 8-bit checkpoint of x, which is also
+ *                                    the forward product's operand
+ *   y  = linear(xq, w)               y  = xq w^T
+ *   dx = dgrad(dy, w)                dx = dy w
+ *   dw = wgrad(dy, xq)               dw = dy^T xq (or its transpose)
+ *
+ * so one copy of x is stored, and the gradients are those of the product
+ * that the forward pass formed (the quantizers pass gradients through).
+ *
+ * A microscaled (MX) matrix is `rows` x `cols` values in blocks of 32
+ * consecutive columns; the last block of a row may be partial.  A block has
+ * one scale byte e, which stands for 2^(e-127), and a code per element:
+ * Q4MX_FP4 is E2M1 (magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6), Q4MX_FP8 is E4M3
+ * (largest magnitude 448, no infinities, 0x7F and 0xFF NaN).  An element's
+ * value is its code's times its block's scale.  Scale byte 255 makes the
+ * whole block NaN.
+ *
+ * Quantization takes, per block, the smallest power of two 2^k, k >= -127,
+ * with absmax / 2^k at most the largest code (6 or 448), and rounds each
+ * element to the nearest value, ties to the even code.  Nothing saturates.
+ * A block that holds a NaN or an infinity gets scale 255 and zero codes.
+ *
+ * Layout.  Let P = cols rounded up to a multiple of 128.
+ *   codes   rows x P codes, row-major: FP8 one byte each, FP4 two to a byte,
+ *           the even column in the low nibble (P or P/2 bytes per row);
+ *   scales  P/128 x rows x 4 bytes: block b of row r is byte
+ *           ((b/4) rows + r) 4 + b%4, so the scales of one 128-column slice
+ *           of neighbouring rows are consecutive.
+ * Codes of columns cols .. P-1 are 0, and so are the scale bytes of blocks
+ * that lie wholly there; the calls that write an MX matrix write these too,
+ * and the calls that read one require it.
+ *
+ * Dense operands are row-major with a row stride `ld` in elements (ld >= the
+ * row's length) and pointers aligned to the element; 16-byte aligned pointers
+ * with rows a multiple of 16 bytes apart are read and written fastest.
+ * Codes, scales and workspaces are 16-byte aligned.  Nothing outside a
+ * dense result's rows x cols elements is written.  A call whose result has
+ * no elements does nothing; a product over no elements is 0.  The calls take
+ * no upload and allocate nothing, so they may be captured in a HIP graph;
+ * the operands' pointers must live on the current device. */
+
+typedef enum { Q4MX_FP4 = 0, Q4MX_FP8 = 1 } q4mx_format;
+typedef enum { Q4MX_F32 = 0, Q4MX_BF16 = 1 } q4mx_dtype;
+
+typedef struct {
+    int32_t format;   /* q4mx_format */
+    int32_t reserved; /* 0 */
+    int64_t rows, cols; /* each in [0, 2^31); rows x P < 2^34 */
+    uint8_t* codes;
+    uint8_t* scales;
+} q4mx_matrix;
+
+/* Bytes of an MX matrix's codes and scales. */
+q4_status q4mx_matrix_bytes(int32_t format, int64_t rows, int64_t cols, size_t* codes, size_t* scales);
+
+/* out <- src (dtype Q4MX_F32 or Q4MX_BF16).  transpose = 0: src is
+ * out->rows x out->cols.  transpose = 1: src is out->cols x out->rows, and
+ * out is the quantized transpose (the blocks run along src's rows axis): the
+ * form of a weight whose master is stored [in, out]. */
+q4_status q4mx_quantize(const void* src, int32_t dtype, int64_t ld, int32_t transpose, const q4mx_matrix* out,
+                        void* stream);
+
+/* dst (a->rows x a->cols, dtype) <- the values of a.  FP32 holds every value
+ * but those past its range (infinity); BF16 also rounds values below 2^-126
+ * (to nearest even). */
+q4_status q4mx_dequantize(const q4mx_matrix* a, void* dst, int32_t dtype, int64_t ld, void* stream);
+
+/* y (x->rows x w->rows, dtype) <- x w^T, x in either format and w in
+ * Q4MX_FP4, x->cols == w->cols.  Sums in FP32, one rounding at the end. */
+q4_status q4mx_linear(const q4mx_matrix* x, const q4mx_matrix* w, void* y, int32_t dtype, int64_t ldy, void* ws,
+                      size_t ws_bytes, void* stream);
+q4_status q4mx_linear_workspace_bytes(const q4mx_matrix* x, const q4mx_matrix* w, size_t* bytes);
+
+/* The same from a dense BF16 x (tokens x w->cols), which is quantized to
+ * Q4MX_FP8 on the way: the same result as q4mx_quantize, then q4mx_linear.
+ * Up to Q4MX_FEW_TOKENS tokens (a decoding step) take one launch and no
+ * workspace. */
+#define Q4MX_FEW_TOKENS 16
+q4_status q4mx_linear_bf16(const uint16_t* x, int64_t ldx, int64_t tokens, const q4mx_matrix* w, void* y,
+                           int32_t dtype, int64_t ldy, void* ws, size_t ws_bytes, void* stream);
+q4_status q4mx_linear_bf16_workspace_bytes(int64_t tokens, const q4mx_matrix* w, size_t* bytes);
+
+/* dx (tokens x w->cols, dtype) <- dy w, dy BF16 (tokens x w->rows), w in
+ * Q4MX_FP4. */
+q4_status q4mx_dgrad(const uint16_t* dy, int64_t lddy, int64_t tokens, const q4mx_matrix* w, void* dx, int32_t dtype,
+                     int64_t lddx, void* ws, size_t ws_bytes, void* stream);
+q4_status q4mx_dgrad_workspace_bytes(const uint16_t* dy, int64_t lddy, int64_t tokens, const q4mx_matrix* w,
+                                     size_t* bytes);
+
+#define Q4MX_WGRAD_TRANSPOSED 1 /* dw <- x^T dy (x->cols x n): the layout of a master stored [in, out] */
+#define Q4MX_WGRAD_ADD 2        /* dw <- dw + the product, summed in FP32 and rounded once */
+
+/* dw (n x x->cols, dtype) <- dy^T x, dy BF16 (x->rows x n), x in Q4MX_FP8 or
+ * Q4MX_FP4: the 8-bit checkpoint used where it is needed.  A tensor's BF16
+ * gradient (q4_tensor.grad) is a dw of dtype Q4MX_BF16. */
+q4_status q4mx_wgrad(const uint16_t* dy, int64_t lddy, int64_t n, const q4mx_matrix* x, void* dw, int32_t dtype,
+                     int64_t lddw, int32_t flags, void* ws, size_t ws_bytes, void* stream);
+q4_status q4mx_wgrad_workspace_bytes(const uint16_t* dy, int64_t lddy, int64_t n, const q4mx_matrix* x,
+                                     int32_t flags, size_t* bytes);
+
+/* Activation functions between two linear layers, the input kept in 8 bits. */
+typedef enum {
+    Q4MX_GELU = 0,     /* 0.5 x (1 + tanh(sqrt(2/pi) (x + 0.044715 x^3))) */
+    Q4MX_GELU_ERF = 1, /* 0.5 x (1 + erf(x / sqrt 2)) */
+    Q4MX_SWIGLU = 2    /* x / (1 + e^-x) * up */
+} q4mx_act;
+
+/* Forward: y = f(x) (or f(x) up), rounded to BF16, for BF16 x and up (rows x
+ * cols; up only for Q4MX_SWIGLU, else NULL).  Writes y if it is not NULL,
+ * the quantized y (of the BF16 values) if y_mx is not NULL, and the
+ * checkpoints kept_x and kept_up (Q4MX_FP8; kept_up only for Q4MX_SWIGLU)
+ * if they are not NULL: each as q4mx_quantize would. */
+q4_status q4mx_act_forward(int32_t act, const uint16_t* x, int64_t ldx, const uint16_t* up, int64_t ldup,
+                           int64_t rows, int64_t cols, uint16_t* y, int64_t ldy, const q4mx_matrix* y_mx,
+                           const q4mx_matrix* kept_x, const q4mx_matrix* kept_up, void* stream);
+
+/* Backward from the checkpoints: dx <- dy f'(x) (times up), and dup <- dy
+ * f(x) for Q4MX_SWIGLU, with x and up the kept values; all BF16, rows x cols
+ * of kept_x.  dx may be dy. */
+q4_status q4mx_act_backward(int32_t act, const q4mx_matrix* kept_x, const q4mx_matrix* kept_up, const uint16_t* dy,
+                            int64_t lddy, uint16_t* dx, int64_t lddx, uint16_t* dup, int64_t lddup, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

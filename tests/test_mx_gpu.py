@@ -1,0 +1,512 @@
+"""The microscaled linear layer on the GPU against plain 64-bit
+implementations (mx_reference.py), at the sizes and values where it can go
+wrong.
+
+Tolerances.  Quantization and restoring have none: they are exact.  A product
+of depth K whose terms have the sum of magnitudes S is a sum of K exact
+products in FP32; each of its at most K additions is off by at most one step
+(2^-23) of a partial sum of at most S, and a join of partial sums by the same:
+|error| <= (K + 16) 2^-23 S, plus half a step of the result's type, 2^-8 |y|
+for BF16 and 2^-24 |y| for FP32.
+"""
+import math
+
+import pytest
+import torch
+
+import mx_reference as ref
+from bit_adamw_update_amd import api, mx
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+HALF_STEP = {torch.bfloat16: 2.0 ** -8, torch.float32: 2.0 ** -24}
+
+
+def _say(*a):
+    print(*a, flush=True)
+
+
+def _gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def _values(rows, cols, seed, dtype=torch.float32, scale=1.0):
+    """Normal values, a few columns twenty times larger, a few exact zeros."""
+    g = _gen(seed)
+    x = torch.randn(rows, cols, generator=g) * scale
+    x = x * torch.where(torch.rand(cols, generator=g) < 0.02, 20.0, 1.0)
+    x[torch.rand(rows, cols, generator=g) < 0.01] = 0
+    return x.to(dtype)
+
+
+def _strided(x, gap=0, shift=0, fill=7.0):
+    """x on the GPU as a view with `gap` elements between rows, starting
+    `shift` elements past an aligned address; (view, whole buffer)."""
+    rows, cols = x.shape
+    ld = cols + gap
+    buf = torch.full((shift + rows * ld + 8,), fill, dtype=x.dtype, device=DEV)
+    view = buf[shift:shift + rows * ld].view(rows, ld)[:, :cols]
+    view.copy_(x)
+    return view, buf
+
+
+def _matrix(x, fmt):
+    return mx.quantize(x.to(DEV).contiguous(), fmt)
+
+
+def _check_product(y, want, terms, depth, dtype):
+    assert y.dtype == dtype
+    y = y.double().cpu()
+    tol = want.abs() * HALF_STEP[dtype] + (depth + 16) * 2.0 ** -23 * terms
+    off = (y - want).abs()
+    assert bool((off <= tol).all()), f"off by {off.max().item()}, {(off / tol.clamp(min=1e-300)).max().item()} of the tolerance"
+
+
+# ---- quantize, dequantize ----------------------------------------------------
+
+QUANT_SIZES = [(1, 1), (1, 31), (3, 32), (2, 33), (5, 127), (17, 128), (33, 129), (64, 300), (31, 1000), (130, 257)]
+
+
+@pytest.mark.parametrize("fmt", ["fp4", "fp8"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("rows,cols", QUANT_SIZES)
+def test_quantize_is_exact(rows, cols, dtype, fmt):
+    _say("quantize", rows, cols, dtype, fmt)
+    x = _values(rows, cols, 1, dtype)
+    codes, scales = ref.quantize(x, fmt)
+    got, gs = ref.unpack(_matrix(x, fmt))
+    assert torch.equal(gs, scales)
+    assert torch.equal(got, codes)
+
+
+@pytest.mark.parametrize("fmt", ["fp4", "fp8"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("rows,cols", QUANT_SIZES)
+def test_quantized_transpose_is_exact(rows, cols, dtype, fmt):
+    _say("quantize transposed", rows, cols, dtype, fmt)
+    x = _values(rows, cols, 2, dtype)
+    codes, scales = ref.quantize(x.t(), fmt)
+    got, gs = ref.unpack(mx.quantize(x.to(DEV), fmt, transpose=True))
+    assert torch.equal(gs, scales)
+    assert torch.equal(got, codes)
+
+
+@pytest.mark.parametrize("transpose", [False, True])
+@pytest.mark.parametrize("gap,shift", [(0, 1), (3, 0), (8, 8), (8, 3)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_quantize_takes_strided_and_misaligned_sources(dtype, gap, shift, transpose):
+    x = _values(37, 200, 3, dtype)
+    view, _ = _strided(x, gap, shift, fill=float("nan"))
+    codes, scales = ref.quantize(x.t() if transpose else x, "fp8")
+    got, gs = ref.unpack(mx.quantize(view, "fp8", transpose=transpose))
+    assert torch.equal(gs, scales) and torch.equal(got, codes)
+
+
+def _edge_blocks():
+    """One block of 32 per line: ties, extremes, subnormals, signed zeros."""
+    tiny, big = 2.0 ** -149, torch.finfo(torch.float32).max
+    lines = [[0.0, -0.0] * 16,
+             [0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 6.0] * 4,            # ties of E2M1
+             [-0.25, -0.75, -1.25, -1.75, -2.5, -3.5, -5.0, -6.0] * 4,
+             [6.0 * (1 + 2.0 ** -23)] + [1.0] * 31,                        # just past the largest code
+             [448.0] + [2.0 ** -10 * i for i in range(31)],                # E4M3 subnormals and their ties
+             [448.0 * (1 + 2.0 ** -23)] + [2.0 ** -9] * 31,
+             [tiny * (i + 1) for i in range(32)],
+             [2.0 ** -126 * (i / 16) for i in range(32)],
+             [big] + [big / 2 ** i for i in range(31)],
+             [-big] * 32,
+             [1.0] + [2.0 ** -i for i in range(31)],
+             [16.5, 17.0, 17.5, 18.0, 19.0, 21.0, 23.0, 25.0] * 4,         # ties of E4M3
+             [7.0, 7.999, 8.0, 3.0] * 8]
+    return torch.tensor(lines, dtype=torch.float32)
+
+
+@pytest.mark.parametrize("transpose", [False, True])
+@pytest.mark.parametrize("fmt", ["fp4", "fp8"])
+def test_quantize_edge_values(fmt, transpose):
+    x = _edge_blocks()
+    codes, scales = ref.quantize(x, fmt)
+    src = x.t().contiguous() if transpose else x
+    m = mx.quantize(src.to(DEV), fmt, transpose=transpose)
+    got, gs = ref.unpack(m)
+    assert torch.equal(gs, scales)
+    assert torch.equal(got, codes)
+    # FP32's range ends at 2^128 - 2^104: a value rounded up to 2^128 is infinite
+    want = ref.values(codes, scales, 32, fmt).float()
+    assert torch.equal(mx.dequantize(m, torch.float32).cpu(), want)
+
+
+@pytest.mark.parametrize("transpose", [False, True])
+@pytest.mark.parametrize("fmt", ["fp4", "fp8"])
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+def test_a_block_with_a_non_finite_value_is_nan(bad, fmt, transpose):
+    x = torch.randn(4, 96, generator=_gen(4))
+    x[1, 40] = bad
+    src = x.t().contiguous() if transpose else x
+    m = mx.quantize(src.to(DEV), fmt, transpose=transpose)
+    codes, scales = ref.quantize(x, fmt)
+    got, gs = ref.unpack(m)
+    assert torch.equal(gs, scales) and torch.equal(got, codes) and gs[1, 1] == 255
+    nan = torch.isnan(mx.dequantize(m, torch.float32).cpu())
+    assert bool(nan[1, 32:64].all()) and int(nan.sum()) == 32
+
+
+@pytest.mark.parametrize("fmt", ["fp4", "fp8"])
+def test_every_code_with_every_scale(fmt):
+    """dequantize of all codes under all scale bytes: exact in FP32 (infinite
+    past its range), rounded to nearest even in BF16."""
+    n = 16 if fmt == "fp4" else 256
+    codes = torch.arange(n, dtype=torch.uint8).repeat(256, 128 // n if n < 128 else 1)
+    scales = torch.arange(256, dtype=torch.uint8)[:, None].repeat(1, codes.shape[1] // 32)
+    packed = codes[:, 0::2] | (codes[:, 1::2] << 4) if fmt == "fp4" else codes
+    m = mx.MXMatrix(256, codes.shape[1], fmt, codes=packed.contiguous().to(DEV),
+                    scales=scales.view(256, -1, 4).transpose(0, 1).contiguous().to(DEV))
+    want = ref.values(codes, scales, codes.shape[1], fmt)
+    for dtype in (torch.float32, torch.bfloat16):
+        got = mx.dequantize(m, dtype).cpu()
+        exp = want.float().to(dtype)   # FP32 holds every finite value exactly, so this rounds once
+        same = (got == exp) | (torch.isnan(got) & torch.isnan(exp))
+        assert bool(same.all()), (dtype, (~same).nonzero()[:5])
+
+
+@pytest.mark.parametrize("gap,shift", [(0, 0), (5, 0), (8, 1)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_dequantize_writes_only_its_elements(dtype, gap, shift):
+    x = _values(19, 77, 5)
+    m = _matrix(x, "fp8")
+    view, buf = _strided(torch.zeros(19, 77, dtype=dtype), gap, shift)
+    before = buf.clone()
+    mx.dequantize(m, out=view)
+    assert torch.equal(view.double().cpu(), ref.values_of(m).to(dtype).double())
+    view.copy_(torch.zeros_like(view))
+    assert torch.equal(buf, before)
+
+
+# ---- products ----------------------------------------------------------------
+
+LINEAR_SIZES = [(1, 1, 1), (1, 128, 16), (1, 2048, 300), (2, 100, 33), (7, 129, 65), (15, 640, 257), (16, 256, 128),
+                (17, 384, 100), (33, 31, 5), (64, 500, 130), (130, 257, 131), (257, 1000, 300), (513, 512, 520)]
+
+
+@pytest.mark.parametrize("xfmt", ["fp8", "fp4", "bf16"])
+@pytest.mark.parametrize("tokens,cin,cout", LINEAR_SIZES)
+def test_linear(tokens, cin, cout, xfmt):
+    _say("linear", tokens, cin, cout, xfmt)
+    w = _matrix(_values(cout, cin, 7, scale=0.02), "fp4")
+    x = _values(tokens, cin, 8, torch.bfloat16)
+    wv = ref.values_of(w)
+    if xfmt == "bf16":
+        xv = ref.values(*ref.quantize(x, "fp8"), cin, "fp8")
+        operand = x.to(DEV)
+    else:
+        operand = _matrix(x, xfmt)
+        xv = ref.values_of(operand)
+    want, terms = xv @ wv.t(), xv.abs() @ wv.abs().t()
+    for dtype in (torch.bfloat16, torch.float32):
+        _check_product(mx.linear(operand, w, dtype=dtype), want, terms, cin, dtype)
+
+
+DGRAD_SIZES = [(1, 1, 1), (1, 256, 512), (3, 129, 31), (16, 128, 128), (65, 33, 127), (100, 300, 1000), (257, 777, 257),
+               (300, 256, 64), (513, 520, 513)]
+
+
+@pytest.mark.parametrize("tokens,cin,cout", DGRAD_SIZES)
+def test_dgrad(tokens, cin, cout):
+    _say("dgrad", tokens, cin, cout)
+    w = _matrix(_values(cout, cin, 9, scale=0.02), "fp4")
+    dy = _values(tokens, cout, 10, torch.bfloat16, 1e-3)
+    wv, d = ref.values_of(w), dy.double()
+    for dtype in (torch.bfloat16, torch.float32):
+        _check_product(mx.linear_dgrad(dy.to(DEV), w, dtype=dtype), d @ wv, d.abs() @ wv.abs(), cout, dtype)
+
+
+WGRAD_SIZES = [(1, 1, 1), (1, 256, 256), (31, 129, 33), (64, 128, 128), (100, 300, 70), (257, 777, 257), (1000, 65, 40),
+               (4097, 128, 64), (513, 520, 513)]
+
+
+@pytest.mark.parametrize("transposed", [False, True])
+@pytest.mark.parametrize("fmt", ["fp8", "fp4"])
+@pytest.mark.parametrize("tokens,cin,cout", WGRAD_SIZES)
+def test_wgrad(tokens, cin, cout, fmt, transposed):
+    _say("wgrad", tokens, cin, cout, fmt, transposed)
+    x = _matrix(_values(tokens, cin, 11, torch.bfloat16), fmt)
+    dy = _values(tokens, cout, 12, torch.bfloat16, 1e-3)
+    xv, d = ref.values_of(x), dy.double()
+    want, terms = d.t() @ xv, d.abs().t() @ xv.abs()
+    if transposed:
+        want, terms = want.t(), terms.t()
+    for dtype in (torch.bfloat16, torch.float32):
+        _check_product(mx.linear_wgrad(dy.to(DEV), x, transposed=transposed, dtype=dtype), want, terms, tokens, dtype)
+        # added to a gradient: its magnitude is one more term, and the sum is rounded once
+        g = _values(*want.shape, 13, dtype, 1e-2)
+        out = g.to(DEV)
+        mx.linear_wgrad(dy.to(DEV), x, out=out, transposed=transposed, accumulate=True)
+        _check_product(out, want + g.double(), terms + g.double().abs(), tokens + 1, dtype)
+
+
+@pytest.mark.parametrize("gap,shift", [(0, 1), (3, 0), (8, 8), (8, 5)])
+def test_products_take_strided_and_misaligned_operands(gap, shift):
+    """Rows with gaps of NaN between them, bases off by one element; results
+    into such views leave the gaps as they were."""
+    tokens, cin, cout = 70, 200, 90
+    w = _matrix(_values(cout, cin, 14, scale=0.02), "fp4")
+    x = _values(tokens, cin, 15, torch.bfloat16)
+    dy = _values(tokens, cout, 16, torch.bfloat16, 1e-3)
+    xs, _ = _strided(x, gap, shift, math.nan)
+    dys, _ = _strided(dy, gap, shift, math.nan)
+    xq = _matrix(x, "fp8")
+    wv, xv, d = ref.values_of(w), ref.values_of(xq), dy.double()
+    for t in (tokens, 5):
+        for shape, call, want, terms, depth in (
+                ((t, cout), lambda o: mx.linear(xs[:t], w, out=o), xv[:t] @ wv.t(), xv[:t].abs() @ wv.abs().t(), cin),
+                ((t, cin), lambda o: mx.linear_dgrad(dys[:t], w, out=o), d[:t] @ wv, d[:t].abs() @ wv.abs(), cout)):
+            view, buf = _strided(torch.zeros(shape, dtype=torch.bfloat16), gap, shift)
+            before = buf.clone()
+            call(view)
+            _check_product(view, want, terms, depth, torch.bfloat16)
+            view.zero_()
+            assert torch.equal(buf, before)
+    for transposed in (False, True):
+        want, terms = d.t() @ xv, d.abs().t() @ xv.abs()
+        if transposed:
+            want, terms = want.t(), terms.t()
+        view, buf = _strided(torch.zeros(want.shape, dtype=torch.bfloat16), gap, shift)
+        before = buf.clone()
+        mx.linear_wgrad(dys, xq, out=view, transposed=transposed)
+        _check_product(view, want, terms, tokens, torch.bfloat16)
+        view.zero_()
+        assert torch.equal(buf, before)
+
+
+@pytest.mark.parametrize("tokens", [1, 16, 40, 300])
+def test_non_finite_values_stay_in_their_rows_and_columns(tokens):
+    """A NaN or infinity of one operand row reaches the results that use it
+    and no others, at the end of the depth too."""
+    cin, cout = 203, 150
+    w0 = _values(cout, cin, 17, scale=0.02) + 0.1
+    w0[cout - 1, cin - 1] = math.inf
+    w = _matrix(w0, "fp4")
+    x = _values(tokens, cin, 18, torch.bfloat16)
+    x[tokens - 1, 3] = math.nan
+    nan = torch.zeros(tokens, cout, dtype=torch.bool)
+    nan[tokens - 1], nan[:, cout - 1] = True, True
+    xq = _matrix(x, "fp8")
+    assert torch.equal(torch.isnan(mx.linear(xq, w)).cpu(), nan)
+    assert torch.equal(torch.isnan(mx.linear(x.to(DEV), w)).cpu(), nan)
+    dy = _values(tokens, cout, 19, torch.bfloat16) + 1
+    dy[0, 2] = math.inf
+    dx = mx.linear_dgrad(dy.to(DEV), w).cpu()
+    # w's last row is NaN in its last block, columns 192 .. 202, and dy[0, 2]
+    # is infinite: its row is infinite where w's row 2 is not 0
+    w2 = ref.values_of(w)[2]
+    assert torch.equal(torch.isnan(dx[1:]), (torch.arange(cin) >= 192).expand(tokens - 1, cin))
+    assert torch.equal(torch.isinf(dx[0, :192]), w2[:192] != 0)
+    dw = mx.linear_wgrad(dy.to(DEV), xq).cpu()
+    # x's last row is NaN in its first block; dy[0, 2] is infinite
+    first = torch.arange(cin) < 32
+    bad = first.expand(cout, cin).clone()
+    assert torch.equal(torch.isnan(dw)[torch.arange(cout) != 2], bad[torch.arange(cout) != 2])
+    assert torch.equal(torch.isinf(dw[2, 32:]), ref.values_of(xq)[0, 32:] != 0)
+
+
+def test_empty_operands():
+    w = _matrix(_values(40, 64, 20), "fp4")
+    x = torch.empty(0, 64, dtype=torch.bfloat16, device=DEV)
+    assert mx.linear(x, w).shape == (0, 40)
+    assert mx.linear(mx.quantize(x, "fp8"), w).shape == (0, 40)
+    dy = torch.empty(0, 40, dtype=torch.bfloat16, device=DEV)
+    assert mx.linear_dgrad(dy, w).shape == (0, 64)
+    xq = mx.quantize(x, "fp8")
+    g = torch.full((40, 64), 3.0, dtype=torch.bfloat16, device=DEV)
+    assert bool((mx.linear_wgrad(dy, xq) == 0).all())            # a sum over no tokens
+    mx.linear_wgrad(dy, xq, out=g, accumulate=True)
+    assert bool((g == 3).all())
+    for tokens in (3, 40):
+        none = mx.MXMatrix(5, 0, "fp4")
+        e = torch.empty(tokens, 0, dtype=torch.bfloat16, device=DEV)
+        assert bool((mx.linear(mx.quantize(e, "fp8"), none) == 0).all())   # over no inputs
+        assert bool((mx.linear(e, none) == 0).all())
+        assert bool((mx.linear_dgrad(e, mx.MXMatrix(0, 7, "fp4")) == 0).all())
+    y, kept = mx.act_forward("gelu", x)
+    assert y.shape == (0, 64) and mx.act_backward("gelu", kept, y)[0].shape == (0, 64)
+    assert mx.dequantize(mx.MXMatrix(4, 0, "fp8")).shape == (4, 0)
+
+
+# ---- activation functions ------------------------------------------------------
+# f and f' in FP32: the exponential's argument (at most 128 before it leaves
+# FP32's range) is off by a few 2^-24 of itself, so the values are off by at
+# most 2^-24 * 256 * (1 + |x|) = 2^-16 (1 + |x|) of the largest term, on top
+# of BF16's half step.
+
+ACT_SIZES = [(1, 1), (3, 33), (17, 128), (40, 300), (33, 1001)]
+
+
+@pytest.mark.parametrize("kind", ["gelu", "gelu_erf", "swiglu"])
+@pytest.mark.parametrize("rows,cols", ACT_SIZES)
+@pytest.mark.parametrize("gap,shift", [(0, 0), (3, 1)])
+def test_activation(rows, cols, kind, gap, shift):
+    _say("act", rows, cols, kind, gap, shift)
+    x = _values(rows, cols, 21, torch.bfloat16, 3.0)
+    up = _values(rows, cols, 22, torch.bfloat16) if kind == "swiglu" else None
+    dy = _values(rows, cols, 23, torch.bfloat16, 1e-2)
+    xs = _strided(x, gap, shift, math.nan)[0]
+    ups = None if up is None else _strided(up, gap, shift, math.nan)[0]
+    dys = _strided(dy, gap, shift, math.nan)[0]
+    y, kept = mx.act_forward(kind, xs, ups)
+    f, _ = ref.act(kind, x.double())
+    u = torch.ones(1).double() if up is None else up.double()
+    tol = (f * u).abs() * 2.0 ** -8 + 2.0 ** -16 * (1 + x.double().abs()) * (f * u).abs() + 2.0 ** -133
+    assert bool(((y.double().cpu() - f * u).abs() <= tol).all())
+    # the checkpoints are those of quantize, and the quantized result is that of y
+    for k, src in zip(kept, (x, up)):
+        if src is not None:
+            codes, scales = ref.quantize(src, "fp8")
+            got, gs = ref.unpack(k)
+            assert torch.equal(got, codes) and torch.equal(gs, scales)
+    for fmt in ("fp8", "fp4"):
+        ymx, kept2 = mx.act_forward(kind, xs, ups, out_format=fmt)
+        again = mx.quantize(y, fmt)
+        assert torch.equal(ymx.codes, again.codes) and torch.equal(ymx.scales, again.scales)
+        assert torch.equal(kept2[0].codes, kept[0].codes)
+    # backward, against the formula at the kept values
+    xv = ref.values_of(kept[0])
+    uv = torch.ones(1).double() if up is None else ref.values_of(kept[1])
+    f, df = ref.act(kind, xv)
+    d = dy.double()
+    grads = mx.act_backward(kind, kept, dys)
+    slack = 2.0 ** -16 * (1 + xv.abs()) * d.abs()
+    want = d * uv * df
+    assert bool(((grads[0].double().cpu() - want).abs() <= want.abs() * 2.0 ** -8 + slack * uv.abs() + 2.0 ** -133).all())
+    if up is not None:
+        want = d * f
+        assert bool(((grads[1].double().cpu() - want).abs() <= want.abs() * 2.0 ** -8 + slack * xv.abs() + 2.0 ** -133).all())
+
+
+@pytest.mark.parametrize("kind", ["gelu", "gelu_erf", "swiglu"])
+def test_activation_gradient_against_differences(kind):
+    """(f(x + h) - f(x - h)) / 2h in 64 bits, h = 2^-10: its own error is at
+    most h^2/6 |f'''| < 2^-20, as |f'''| < 5 for all three."""
+    x = _values(9, 130, 24, torch.bfloat16, 2.0)
+    up = _values(9, 130, 25, torch.bfloat16) if kind == "swiglu" else None
+    _, kept = mx.act_forward(kind, x.to(DEV), None if up is None else up.to(DEV))
+    one = torch.ones(9, 130, dtype=torch.bfloat16, device=DEV)
+    dx = mx.act_backward(kind, kept, one)[0].double().cpu()
+    xv, h = ref.values_of(kept[0]), 2.0 ** -10
+    uv = torch.ones(1).double() if up is None else ref.values_of(kept[1])
+    want = (ref.act(kind, xv + h)[0] - ref.act(kind, xv - h)[0]) / (2 * h) * uv
+    tol = want.abs() * 2.0 ** -8 + (2.0 ** -16 * (1 + xv.abs()) + 2.0 ** -20) * uv.abs()
+    assert bool(((dx - want).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("kind", ["gelu", "gelu_erf", "swiglu"])
+def test_activation_extremes(kind):
+    """Very negative x gives 0 (no overflow of the exponential), very positive
+    x gives x; a NaN block's checkpoint gives NaN gradients, the others do not."""
+    x = torch.tensor([[-3e38, -1e4, -200.0, -100.0, -0.0, 0.0, 100.0, 1e4] + [0.0] * 24 + [math.nan] + [1.0] * 31],
+                     dtype=torch.bfloat16, device=DEV)
+    one = torch.ones_like(x)
+    up = one if kind == "swiglu" else None
+    y, kept = mx.act_forward(kind, x, up)
+    assert torch.equal(y[0, :6].cpu().abs(), torch.zeros(6, dtype=torch.bfloat16))
+    assert torch.equal(y[0, 6:8], x[0, 6:8])
+    dx = mx.act_backward(kind, kept, one)[0]
+    assert torch.equal(torch.isnan(dx[0]).cpu(), torch.arange(64) >= 32)
+
+
+# ---- as a program uses them ----------------------------------------------------
+
+def test_activation_gradient_in_place_of_dy():
+    x = _values(20, 200, 26, torch.bfloat16).to(DEV)
+    dy = _values(20, 200, 27, torch.bfloat16).to(DEV)
+    _, kept = mx.act_forward("gelu", x)
+    want = mx.act_backward("gelu", kept, dy)[0]
+    api.q4mx_act_backward(api.MX_GELU, kept[0].desc, None, dy, 200, dy, 200)
+    assert torch.equal(dy, want)
+
+
+def _mlp(masters, x, dy, ws=None):
+    """A two-layer block, forward and backward; its gradients in the masters' layout."""
+    w1, w2 = (mx.quantize(m, "fp4", transpose=True) for m in masters)
+    xq = mx.quantize(x, "fp8")
+    h = mx.linear(xq, w1)
+    a, kept = mx.act_forward("gelu", h, out_format="fp8")
+    y = mx.linear(a, w2)
+    da = mx.linear_dgrad(dy, w2)
+    dw2 = mx.linear_wgrad(dy, a, transposed=True)
+    dh = mx.act_backward("gelu", kept, da)[0]
+    dw1 = mx.linear_wgrad(dh, xq, transposed=True)
+    return y, mx.linear_dgrad(dh, w1), dw1, dw2
+
+
+def test_layer_on_a_side_stream_and_in_a_graph():
+    """Bit for bit the eager results: on another stream, and in a HIP graph
+    replayed with eager work between the replays (new inputs each time)."""
+    g = _gen(30)
+    masters = [(torch.randn(200, 300, generator=g) * 0.05).to(DEV), (torch.randn(300, 100, generator=g) * 0.05).to(DEV)]
+    x, dy = torch.empty(77, 200, dtype=torch.bfloat16, device=DEV), torch.empty(77, 100, dtype=torch.bfloat16, device=DEV)
+
+    def fill(seed):
+        x.copy_(_values(77, 200, seed, torch.bfloat16))
+        dy.copy_(_values(77, 100, seed + 1, torch.bfloat16, 1e-2))
+
+    fill(31)
+    want = _mlp(masters, x, dy)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = _mlp(masters, x, dy)
+    torch.cuda.current_stream().wait_stream(side)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    got = mx.linear(x, mx.quantize(masters[0], "fp4", transpose=True), stream=None)
+    side.wait_stream(torch.cuda.current_stream())
+    w = mx.quantize(masters[0], "fp4", transpose=True, stream=side)
+    again = mx.linear(x, w, stream=side)
+    side.synchronize()
+    assert torch.equal(got, again)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = _mlp(masters, x, dy)
+    for seed in (40, 50, 60):
+        fill(seed)
+        graph.replay()
+        torch.cuda.synchronize()
+        want = _mlp(masters, x, dy)
+        assert all(torch.equal(a, b) for a, b in zip(held, want)), seed
+        torch.cuda.synchronize()
+
+
+def test_training_steps_with_the_optimizer():
+    """Quantize the masters, forward, backward into the BF16 gradients (two
+    microbatches, the second added), 4-bit AdamW step, three times: the
+    gradients are the formula's for the quantized operands each time, and
+    the masters move."""
+    import bit_adamw_update_amd as q4
+    from bit_adamw_update_amd import inputs
+    g = _gen(70)
+    shapes = [(96, 160), (160, 64)]
+    masters = [(torch.randn(s, generator=g) * 0.05).to(DEV) for s in shapes]
+    grads = [torch.empty(s, dtype=torch.bfloat16, device=DEV) for s in shapes]
+    state = q4.Q4State("zip_sr", [inputs.TensorSpec(f"w{i}", s, i) for i, s in enumerate(shapes)])
+    for step in (1, 2, 3):
+        start = [m.clone() for m in masters]
+        ws = [mx.quantize(m, "fp4", transpose=True) for m in masters]
+        sums = [0.0, 0.0]
+        terms = [0.0, 0.0]
+        for micro in range(2):
+            x = _values(50, 96, 100 * step + micro, torch.bfloat16).to(DEV)
+            dy = _values(50, 64, 100 * step + 10 + micro, torch.bfloat16, 1e-2).to(DEV)
+            xq = mx.quantize(x, "fp8")
+            a, kept = mx.act_forward("gelu", mx.linear(xq, ws[0]), out_format="fp8")
+            da = mx.linear_dgrad(dy, ws[1])
+            dh = mx.act_backward("gelu", kept, da)[0]
+            for i, (d, op) in enumerate(((dh, xq), (dy, a))):
+                mx.linear_wgrad(d, op, out=grads[i], transposed=True, accumulate=micro > 0)
+                ov, dv = ref.values_of(op), d.double().cpu()
+                sums[i], terms[i] = sums[i] + ov.t() @ dv, terms[i] + ov.abs().t() @ dv.abs()
+        for i in range(2):
+            # the first microbatch was rounded to BF16 before the second was added: one more half step
+            off = (grads[i].double().cpu() - sums[i]).abs()
+            assert bool((off <= 2 * 2.0 ** -8 * terms[i]).all())
+        state.step([m.reshape(-1) for m in masters], [d.reshape(-1) for d in grads], step)
+        for m, s in zip(masters, start):
+            assert bool(torch.isfinite(m).all()) and not torch.equal(m, s)
