@@ -37,10 +37,16 @@ hipError_t launch_act_forward(int act, const Dense& x, const Dense& up, int64_t 
 hipError_t launch_act_backward(int act, const MxMat& kx, const MxMat& ku, const Dense& dy, const Dense& dx,
                                const Dense& dup, hipStream_t st);
 
-// The three products.  add: the result is added to what out holds.
+// Whether dy (rows x cols) must be copied into 16-byte aligned rows of whole
+// 8-element pieces first, and the bytes of that copy.
+bool dense_needs_copy(const Dense& d, int64_t rows, int64_t cols);
+size_t dense_copy_bytes(int64_t rows, int64_t cols);
+
+// The three products.  add: the result is added to what out holds.  ws: the
+// copy of dy, if it needs one.
 hipError_t launch_linear(const MxMat& x, const MxMat& w, const Dense& y, hipStream_t st);
-hipError_t launch_dgrad(const Dense& dy, int64_t tokens, const MxMat& w, const Dense& dx, hipStream_t st);
+hipError_t launch_dgrad(const Dense& dy, int64_t tokens, const MxMat& w, const Dense& dx, void* ws, hipStream_t st);
 hipError_t launch_wgrad(const Dense& dy, int64_t n, const MxMat& x, const Dense& dw, bool transposed, bool add,
-                        hipStream_t st);
+                        void* ws, hipStream_t st);
 
 }  // namespace q4

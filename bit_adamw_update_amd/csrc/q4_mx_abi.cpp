@@ -94,6 +94,13 @@ Quantized quantized(int64_t tokens, int64_t cols) {
     return Quantized{round256((size_t)(tokens * padded(cols))), round256((size_t)(tokens * padded(cols) / 32))};
 }
 
+// Workspace of a gradient product: the copy of a dy whose rows are not aligned.
+size_t copy_bytes(const uint16_t* dy, int64_t lddy, int64_t rows, int64_t cols) {
+    if (rows == 0 || cols == 0 || !dense_needs_copy(Dense{const_cast<uint16_t*>(dy), lddy, Q4MX_BF16}, rows, cols))
+        return 0;
+    return round256(dense_copy_bytes(rows, cols));
+}
+
 #define Q4_TRY(x)                        \
     do {                                 \
         const q4_status s_ = (x);        \
@@ -105,10 +112,17 @@ q4_status device() {
     return (q4_status)current_device(&dev);
 }
 
+// The products address a tile's rows with 32-bit byte offsets from its first.
+constexpr int64_t kMaxWidth = int64_t(1) << 23;
+q4_status check_width(const char* name, int64_t n) {
+    if (n >= kMaxWidth) return bad(Q4_ERR_SHAPE, "%s is %lld, a product takes less than 2^23", name, (long long)n);
+    return Q4_OK;
+}
+
 q4_status check_weight(const q4mx_matrix* w) {
     Q4_TRY(check_mx("w", w));
     if (w->format != Q4MX_FP4) return bad(Q4_ERR_CONFLICT, "w must be in Q4MX_FP4");
-    return Q4_OK;
+    return check_width("w->cols", w->cols);
 }
 
 }  // namespace
@@ -203,7 +217,7 @@ q4_status q4mx_dgrad_workspace_bytes(const uint16_t* dy, int64_t lddy, int64_t t
     if (!bytes) return bad(Q4_ERR_INVALID_ARG, "output is NULL");
     Q4_TRY(check_mx_shape("w", w));
     Q4_TRY(check_dense("dy", dy, Q4MX_BF16, tokens, w->rows, lddy));
-    *bytes = 0;
+    *bytes = copy_bytes(dy, lddy, tokens, w->rows);
     return ok();
 }
 
@@ -211,6 +225,7 @@ q4_status q4mx_dgrad(const uint16_t* dy, int64_t lddy, int64_t tokens, const q4m
                      int64_t lddx, void* ws, size_t ws_bytes, void* stream) {
     Q4_TRY(check_weight(w));
     Q4_TRY(check_dense("dy", dy, Q4MX_BF16, tokens, w->rows, lddy));
+    Q4_TRY(check_width("lddy", tokens > 0 && w->rows > 0 ? lddy : 0));
     Q4_TRY(check_dense("dx", dx, dtype, tokens, w->cols, lddx));
     if (tokens == 0 || w->cols == 0) return ok();
     size_t need = 0;
@@ -218,7 +233,7 @@ q4_status q4mx_dgrad(const uint16_t* dy, int64_t lddy, int64_t tokens, const q4m
     Q4_TRY(check_ws(ws, ws_bytes, need));
     Q4_TRY(device());
     return launched(launch_dgrad(Dense{const_cast<uint16_t*>(dy), lddy, Q4MX_BF16}, tokens, mat(w),
-                                 Dense{dx, lddx, dtype}, reinterpret_cast<hipStream_t>(stream)),
+                                 Dense{dx, lddx, dtype}, ws, reinterpret_cast<hipStream_t>(stream)),
                     "dgrad launch");
 }
 
@@ -228,7 +243,7 @@ q4_status q4mx_wgrad_workspace_bytes(const uint16_t* dy, int64_t lddy, int64_t n
     if (flags & ~(Q4MX_WGRAD_TRANSPOSED | Q4MX_WGRAD_ADD)) return bad(Q4_ERR_INVALID_ARG, "unknown flags 0x%x", flags);
     Q4_TRY(check_mx_shape("x", x));
     Q4_TRY(check_dense("dy", dy, Q4MX_BF16, x->rows, n, lddy));
-    *bytes = 0;
+    *bytes = copy_bytes(dy, lddy, x->rows, n);
     return ok();
 }
 
@@ -236,6 +251,8 @@ q4_status q4mx_wgrad(const uint16_t* dy, int64_t lddy, int64_t n, const q4mx_mat
                      int64_t lddw, int32_t flags, void* ws, size_t ws_bytes, void* stream) {
     size_t need = 0;
     Q4_TRY(check_mx("x", x));
+    Q4_TRY(check_width("x->cols", x->cols));
+    Q4_TRY(check_width("lddy", x->rows > 0 && n > 0 ? lddy : 0));
     Q4_TRY(q4mx_wgrad_workspace_bytes(dy, lddy, n, x, flags, &need));
     const bool t = (flags & Q4MX_WGRAD_TRANSPOSED) != 0;
     Q4_TRY(check_dense("dw", dw, dtype, t ? x->cols : n, t ? n : x->cols, lddw));
@@ -244,7 +261,7 @@ q4_status q4mx_wgrad(const uint16_t* dy, int64_t lddy, int64_t n, const q4mx_mat
     Q4_TRY(check_ws(ws, ws_bytes, need));
     Q4_TRY(device());
     return launched(launch_wgrad(Dense{const_cast<uint16_t*>(dy), lddy, Q4MX_BF16}, n, mat(x), Dense{dw, lddw, dtype},
-                                 t, (flags & Q4MX_WGRAD_ADD) != 0, reinterpret_cast<hipStream_t>(stream)),
+                                 t, (flags & Q4MX_WGRAD_ADD) != 0, ws, reinterpret_cast<hipStream_t>(stream)),
                     "wgrad launch");
 }
 

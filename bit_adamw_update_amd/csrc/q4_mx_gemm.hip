@@ -1,9 +1,13 @@
 // q4_mx_gemm.hip -- the three products of the microscaled linear layer
 // (gfx950).
 //
-// Every code value is exact in BF16 (E2M1 has one fraction bit, E4M3 three,
-// and scales are powers of two), so all three products are sums of BF16
-// products in FP32 on the matrix cores.
+// linear multiplies codes by codes: the block-scaled matrix instructions take
+// E4M3 or E2M1 operands with a power of two per row and 32 columns, which is
+// the format itself.  dgrad and wgrad multiply BF16 gradients by codes whose
+// blocks run across the sum, so the codes are decoded to BF16 (exactly: E2M1
+// has one fraction bit, E4M3 three, and scales are powers of two) once per
+// tile on their way into shared memory.  All sums are FP32 in the matrix
+// cores' accumulators.
 
 #include "q4_mx.h"
 #include "q4_mx_dev.h"
@@ -13,106 +17,517 @@ namespace {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
 
-// An operand: element (row, k) of `rows` x `depth`.
-struct Operand {
-    const void* p;  // dense BF16
-    MxMat mx;       // or codes (p == NULL)
-    int64_t rows, depth;
-    int64_t sr, sk;  // dense strides
-    bool turned;     // MX: row is the MX column
-};
+#define Q4_LDS __attribute__((address_space(3)))
 
-__device__ __forceinline__ uint16_t element(const Operand& a, int64_t row, int64_t k) {
-    if (row >= a.rows || k >= a.depth) return 0;
-    if (a.p) return static_cast<const uint16_t*>(a.p)[row * a.sr + k * a.sk];
-    const int64_t r = a.turned ? k : row, c = a.turned ? row : k;
-    const float s = scale_of(a.mx.scales[((c >> 7) * a.mx.rows + r) * 4 + ((c >> 5) & 3)]);
-    float v[8];
-    if (a.mx.fmt == Q4MX_FP4) {
-        dec4x8(a.mx.codes[r * a.mx.slices * 64 + c / 2], s, v);
-        return bf16_bits(v[c & 1]);
-    }
-    dec8x4(a.mx.codes[r * a.mx.slices * 128 + c], s, v);
-    return bf16_bits(v[0]);
+// ---- tiles, buffers, shared memory -------------------------------------------
+
+// Work-group -> tile.  Consecutive work-groups go to the 8 XCDs in turn, each
+// with an L2 of its own; the renumbering gives each XCD one contiguous run of
+// tiles, taken in bands of 4 along the first axis, so that the tiles that run
+// together on an XCD share rows of both operands.
+__device__ __forceinline__ void tile_of(uint32_t bid, uint32_t n0, uint32_t n1, uint32_t& i0, uint32_t& i1) {
+    const uint32_t total = n0 * n1, q = total / 8, r = total % 8, x = bid % 8;
+    const uint32_t id = x * q + min(x, r) + bid / 8;
+    constexpr uint32_t kBand = 4;
+    const uint32_t band = id / (kBand * n1), first = band * kBand, h = min(n0 - first, kBand);
+    const uint32_t in = id - band * (kBand * n1);
+    i0 = first + in % h;
+    i1 = in / h;
 }
 
-struct Result {
+// A raw buffer: loads past `bytes` read as 0 (checked per dword).
+__device__ __forceinline__ i32x4 buffer(const void* p, int64_t bytes) {
+    const uint64_t a = reinterpret_cast<uint64_t>(p);
+    const uint32_t n = bytes < 0 ? 0u : bytes > 0xFFFFFF00ll ? 0xFFFFFF00u : (uint32_t)bytes;
+    i32x4 r;
+    r[0] = __builtin_amdgcn_readfirstlane((int)(uint32_t)a);
+    r[1] = __builtin_amdgcn_readfirstlane((int)(uint32_t)(a >> 32));
+    r[2] = __builtin_amdgcn_readfirstlane((int)n);
+    r[3] = 0x00020000;
+    return r;
+}
+// The same for the compiler's own loads.
+__device__ __forceinline__ auto readable(const void* p, int64_t bytes) {
+    const i32x4 b = buffer(p, bytes);
+    return __builtin_amdgcn_make_buffer_rsrc(
+        reinterpret_cast<void*>((uint64_t)(uint32_t)b[0] | ((uint64_t)(uint32_t)b[1] << 32)), 0, b[2], b[3]);
+}
+constexpr uint32_t kOutside = 0xFFFFFFF0u;  // an offset past every buffer
+
+// A wavefront copies 64 x 16 (or 4) bytes into shared memory from byte `lds`
+// on, lane i's piece at lds + 16 i (4 i), without passing through registers.
+// No register is written, so the only thing to wait for is vmcnt.
+__device__ __forceinline__ void copy16(const i32x4& b, uint32_t off, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(off), "s"(b)
+                 : "memory");
+}
+__device__ __forceinline__ void copy4(const i32x4& b, uint32_t off, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(lds), "v"(off), "s"(b)
+                 : "memory");
+}
+template <int N> __device__ __forceinline__ void wait_copies_and_barrier() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ uint32_t lds_base(const void* p) {
+    return (uint32_t) reinterpret_cast<uintptr_t>((Q4_LDS const char*)p);
+}
+
+// ---- results -------------------------------------------------------------------
+
+// A result whose element (r, c) is p[r * ld + c]; `add`: added to what is there.
+struct Out {
     void* p;
-    int64_t sm, sn;  // element (m, n) at p[m * sm + n * sn]
-    int dtype;
-    bool add;
+    int64_t ld, rows, cols;
+    bool bf16, add, vec;  // vec: 4 consecutive columns from a multiple of 4 are one access
 };
 
-// 64 x 64 results per work-group of four wavefronts, 32 deep per step.
-__global__ __launch_bounds__(256) void k_mx_product(Operand a, Operand b, Result out, int64_t ntiles) {
-    __shared__ __attribute__((aligned(16))) uint16_t la[64][40], lb[64][40];
-    const int64_t m0 = blockIdx.x / ntiles * 64, n0 = blockIdx.x % ntiles * 64;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int sr = threadIdx.x >> 2, sk = (threadIdx.x & 3) * 8;
-    f32x4 acc[4] = {};
-    for (int64_t k0 = 0; k0 < a.depth; k0 += 32) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            la[sr][sk + j] = element(a, m0 + sr, k0 + sk + j);
-            lb[sr][sk + j] = element(b, n0 + sr, k0 + sk + j);
+__device__ __forceinline__ void put4(const Out& o, int64_t r, int64_t c, f32x4 v) {
+    if (r >= o.rows || c >= o.cols) return;
+    const int64_t at = r * o.ld + c;
+    if (o.vec && c + 3 < o.cols) {
+        if (o.bf16) {
+            uint2* p = reinterpret_cast<uint2*>(static_cast<uint16_t*>(o.p) + at);
+            if (o.add) {
+                const uint2 g = *p;
+                v[0] += bf16_value(g.x & 0xFFFFu), v[1] += __uint_as_float(g.x & 0xFFFF0000u);
+                v[2] += bf16_value(g.y & 0xFFFFu), v[3] += __uint_as_float(g.y & 0xFFFF0000u);
+            }
+            *p = make_uint2(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]));
+        } else {
+            f32x4* p = reinterpret_cast<f32x4*>(static_cast<float*>(o.p) + at);
+            if (o.add) v += *p;
+            *p = v;
         }
-        __syncthreads();
-        const bf16x8 x = *reinterpret_cast<const bf16x8*>(&la[wave * 16 + (lane & 15)][(lane >> 4) * 8]);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const bf16x8 y = *reinterpret_cast<const bf16x8*>(&lb[j * 16 + (lane & 15)][(lane >> 4) * 8]);
-            acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, y, acc[j], 0, 0, 0);
-        }
-        __syncthreads();
+        return;
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int64_t m = m0 + wave * 16 + (lane >> 4) * 4 + i, n = n0 + j * 16 + (lane & 15);
-            if (m >= a.rows || n >= b.rows) continue;
-            const int64_t at = m * out.sm + n * out.sn;
-            float v = acc[j][i];
-            if (out.dtype == Q4MX_BF16) {
-                uint16_t* p = static_cast<uint16_t*>(out.p) + at;
-                if (out.add) v += bf16_value(*p);
-                *p = bf16_bits(v);
+    for (int k = 0; k < 4; ++k)
+        if (c + k < o.cols) {
+            if (o.bf16) {
+                uint16_t* p = static_cast<uint16_t*>(o.p) + at + k;
+                *p = bf16_bits(o.add ? v[k] + bf16_value(*p) : v[k]);
             } else {
-                float* p = static_cast<float*>(out.p) + at;
-                if (out.add) v += *p;
-                *p = v;
+                float* p = static_cast<float*>(o.p) + at + k;
+                *p = o.add ? v[k] + *p : v[k];
             }
         }
 }
 
-hipError_t product(const Operand& a, const Operand& b, const Result& out, hipStream_t st) {
-    const int64_t mt = (a.rows + 63) / 64, nt = (b.rows + 63) / 64;
-    k_mx_product<<<dim3((unsigned)(mt * nt)), dim3(256), 0, st>>>(a, b, out, nt);
+Out result(const Dense& d, int64_t rows, int64_t cols, bool add) {
+    const int64_t unit = d.dtype == Q4MX_BF16 ? 8 : 16;
+    const bool vec = reinterpret_cast<uintptr_t>(d.p) % unit == 0 && d.ld % 4 == 0;
+    return Out{d.p, d.ld, rows, cols, d.dtype == Q4MX_BF16, add, vec};
+}
+
+// ---- linear: codes by codes -------------------------------------------------------
+//
+// A work-group of WN x WT wavefronts forms BN outputs x BT tokens; a wavefront
+// FN x FT tiles of 16 x 16, 128 columns of the sum per instruction.  Both
+// operands are copied straight into shared memory, three steps of 128 columns
+// in a ring: while one is multiplied, the next two are on their way.  A row of
+// a step is 64 bytes (E2M1) or 128 (E4M3); its 16-byte pieces are permuted by
+// the row's low bits, so that the 16 rows of a fragment read different banks.
+//
+// The instruction's lane (r, g), r = lane % 16, g = lane / 16, holds of row r
+// the E2M1 codes of columns 32 g .. 32 g + 31, or the E4M3 codes of columns 16
+// g .. +15 and 64 + 16 g .. +15, and the scale byte of columns 32 g .. +31.
+template <int XF, int WN, int WT, int FN, int FT>
+__global__ __launch_bounds__(64 * WN* WT, 2) void k_mx_linear(MxMat x, MxMat w, Out y) {
+    constexpr int NW = WN * WT, BN = WN * FN * 16, BT = WT * FT * 16;
+    constexpr int XB = XF == Q4MX_FP4 ? 64 : 128;
+    constexpr int kW = BN * 64, kX = BT * XB, kStage = kW + kX + (BN + BT) * 4;
+    constexpr int CW = kW / 1024 / NW, CX = kX / 1024 / NW, kCopies = CW + CX + 1;
+    static_assert((BN + BT) == NW * 64 && kW % (1024 * NW) == 0 && kX % (1024 * NW) == 0, "tile");
+    __shared__ __attribute__((aligned(1024))) char lds[3 * kStage];
+
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    uint32_t in, it;
+    tile_of(blockIdx.x, (uint32_t)((w.rows + BN - 1) / BN), (uint32_t)((x.rows + BT - 1) / BT), in, it);
+    const int64_t n0 = (int64_t)in * BN, t0 = (int64_t)it * BT;
+    const int64_t wp = w.slices * 64, xp = x.slices * XB;
+    const int steps = (int)w.slices;
+
+    uint32_t woff[CW], xoff[CX];
+#pragma unroll
+    for (int j = 0; j < CW; ++j)
+        woff[j] = (uint32_t)((j * NW + wave) * 16 + lane / 4) * (uint32_t)wp + ((lane & 3) ^ ((lane >> 3) & 3)) * 16;
+#pragma unroll
+    for (int j = 0; j < CX; ++j)
+        xoff[j] = XF == Q4MX_FP4
+                      ? (uint32_t)((j * NW + wave) * 16 + lane / 4) * (uint32_t)xp + ((lane & 3) ^ ((lane >> 3) & 3)) * 16
+                      : (uint32_t)((j * NW + wave) * 8 + lane / 8) * (uint32_t)xp + ((lane & 7) ^ (lane >> 3)) * 16;
+    // wavefronts 0 .. BN/64-1 copy the scales of w, the others those of x
+    const bool xs = wave >= BN / 64;
+    const int64_t srows = xs ? x.rows : w.rows, s0 = xs ? t0 : n0;
+    const uint8_t* const sp = (xs ? x.scales : w.scales) + s0 * 4;
+    const int64_t sbytes = (srows - s0) * 4;
+    const uint32_t soff = (wave - (xs ? BN / 64 : 0)) * 256 + lane * 4;
+    const uint32_t base = lds_base(lds);
+
+    auto issue = [&](int s) {
+        const uint32_t at = base + (uint32_t)(s % 3) * kStage;
+        const i32x4 bw = buffer(w.codes + n0 * wp + (int64_t)s * 64, (w.rows - n0) * wp - (int64_t)s * 64);
+        const i32x4 bx = buffer(x.codes + t0 * xp + (int64_t)s * XB, (x.rows - t0) * xp - (int64_t)s * XB);
+        const i32x4 bs = buffer(sp + (int64_t)s * srows * 4, sbytes);
+#pragma unroll
+        for (int j = 0; j < CW; ++j) copy16(bw, woff[j], at + (j * NW + wave) * 1024);
+#pragma unroll
+        for (int j = 0; j < CX; ++j) copy16(bx, xoff[j], at + kW + (j * NW + wave) * 1024);
+        copy4(bs, soff, at + kW + kX + wave * 256);
+    };
+
+    const int r = lane & 15, g = lane >> 4, wn = wave % WN, wt = wave / WN;
+    const int wrow = wn * FN * 16 + r, xrow = wt * FT * 16 + r;
+    const int wat = wrow * 64 + ((g ^ ((r >> 1) & 3)) * 16);
+    const int xat = kW + xrow * XB + (XF == Q4MX_FP4 ? (g ^ ((r >> 1) & 3)) * 16 : (g ^ (r & 7)) * 16);
+    const int xat2 = kW + xrow * XB + ((4 + g) ^ (r & 7)) * 16;
+    const int wsat = kW + kX + wrow * 4 + g, xsat = kW + kX + BN * 4 + xrow * 4 + g;
+
+    f32x4 acc[FN][FT] = {};
+    if (steps > 0) issue(0);
+    if (steps > 1) issue(1);
+    for (int s = 0; s < steps; ++s) {
+        // this step's copies are done (the next step's may be under way), and
+        // every wavefront is done with the buffer that step s + 2 takes
+        if (s + 1 < steps) wait_copies_and_barrier<kCopies>();
+        else wait_copies_and_barrier<0>();
+        if (s + 2 < steps) issue(s + 2);
+        const char* const st = lds + (s % 3) * kStage;
+        i32x8 b[FT], a[FN];
+        int sa[FN], sb[FT];
+#pragma unroll
+        for (int j = 0; j < FT; ++j) {
+            const i32x4 lo = *reinterpret_cast<const i32x4*>(st + xat + j * 16 * XB);
+            i32x4 hi = {0, 0, 0, 0};
+            if (XF != Q4MX_FP4) hi = *reinterpret_cast<const i32x4*>(st + xat2 + j * 16 * XB);
+            b[j] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+            sb[j] = *reinterpret_cast<const uint8_t*>(st + xsat + j * 64);
+        }
+#pragma unroll
+        for (int i = 0; i < FN; ++i) {
+            const i32x4 lo = *reinterpret_cast<const i32x4*>(st + wat + i * 1024), none = {0, 0, 0, 0};
+            a[i] = __builtin_shufflevector(lo, none, 0, 1, 2, 3, 4, 5, 6, 7);
+            sa[i] = *reinterpret_cast<const uint8_t*>(st + wsat + i * 64);
+        }
+#pragma unroll
+        for (int i = 0; i < FN; ++i)
+#pragma unroll
+            for (int j = 0; j < FT; ++j)
+                acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a[i], b[j], acc[i][j], 4,
+                                                                             XF == Q4MX_FP4 ? 4 : 0, 0, sa[i], 0, sb[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < FT; ++j)
+#pragma unroll
+        for (int i = 0; i < FN; ++i)
+            put4(y, t0 + (wt * FT + j) * 16 + r, n0 + (wn * FN + i) * 16 + g * 4, acc[i][j]);
+}
+
+// ---- dgrad, wgrad: BF16 by codes ------------------------------------------------------
+//
+// Result (d, c): d runs over the dense operand's axis (a token for dgrad, an
+// output for wgrad), c over the code matrix's columns; the sum runs over the
+// code matrix's rows k (outputs for dgrad, tokens for wgrad), 64 per step.
+//
+// Codes are read 8 to a lane, decoded to BF16 with their block's scale and
+// written to shared memory as [k][c]; the transposing reads
+// (ds_read_b64_tr_b16) turn them into fragments, 16 columns x 8 k per lane
+// group.  The dense operand is copied straight to shared memory: as [d][k]
+// where k is its row's axis (dgrad), as [k][d] where it is not (TURNED:
+// wgrad), with the same transposing reads.  [k][..] rows are permuted in
+// 32-byte units by f(k) = k % 4 + 4 (k / 8 % 2), so that the four rows of a
+// transposing read, and those of the neighbouring lane group, lie in different
+// banks; [d][k] rows in 16-byte pieces by d % 8.
+//
+// Two steps in a ring: while step s is multiplied, s + 1 is decoded and copied.
+__device__ __forceinline__ bf16x8 read_turned(const char* p, int pitch) {
+    union {
+        s16x4 h[2];
+        bf16x8 v;
+    } t;
+    t.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Q4_LDS s16x4*)p);
+    t.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Q4_LDS s16x4*)(p + 4 * pitch));
+    return t.v;
+}
+
+__device__ __forceinline__ uint32_t bf16_pair_of(uint32_t w, float s, int fmt, int k) {
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    union {
+        bf16x2 v;
+        uint32_t u;
+    } t;
+    if (fmt == Q4MX_FP4) {
+        switch (k) {
+        case 0: t.v = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 0); break;
+        case 1: t.v = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 1); break;
+        case 2: t.v = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 2); break;
+        default: t.v = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3); break;
+        }
+    } else {
+        t.v = k == 0 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, s, false)
+                     : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, s, true);
+    }
+    return t.u;
+}
+
+// The dense operand: dgrad's rows d, or wgrad's (TURNED) rows k, 16-byte
+// aligned, of `span` elements, a multiple of 8 (where that is more than the
+// row's length, the rest is 0).
+struct Gradient {
+    const uint16_t* p;
+    int64_t ld, span, width;  // width: the extent of d
+};
+
+template <bool TURNED, int FMT, bool SWAP, int WC, int WD, int FC, int FD>
+__global__ __launch_bounds__(64 * WC* WD, 2) void k_mx_grad(Gradient a, MxMat m, Out out) {
+    constexpr int NW = WC * WD, BC = WC * FC * 16, BD = WD * FD * 16;
+    constexpr int kD = BD * 128, kC = BC * 128;  // bytes of a step
+    constexpr int CD = kD / 1024 / NW;
+    constexpr int LPR = BC / 8;  // lanes of a row of codes
+    static_assert(NW * 64 / LPR == 16 && kD % (1024 * NW) == 0, "tile");
+    __shared__ __attribute__((aligned(1024))) char lds[2 * (kD + kC)];
+
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    uint32_t ic, id;
+    tile_of(blockIdx.x, (uint32_t)((m.cols + BC - 1) / BC), (uint32_t)((a.width + BD - 1) / BD), ic, id);
+    const int64_t c0 = (int64_t)ic * BC, d0 = (int64_t)id * BD;
+    const int64_t depth = m.rows;
+    const int steps = (int)((depth + 63) / 64);
+    const uint32_t base = lds_base(lds);
+
+    // dense: this lane's pieces of the step's copies
+    uint32_t doff[CD];
+    int dk[CD];  // first k of the piece within the step (not TURNED)
+#pragma unroll
+    for (int j = 0; j < CD; ++j) {
+        if (TURNED) {
+            constexpr int PPR = BD / 8;  // 16-byte pieces of a row
+            const int k = (j * NW + wave) * (64 / PPR) + lane / PPR, piece = lane % PPR;
+            const int f = (k & 3) | (((k >> 3) & 1) << 2);
+            doff[j] = (uint32_t)k * (uint32_t)(a.ld * 2) + (uint32_t)(((piece >> 1) ^ f) * 32 + (piece & 1) * 16);
+            dk[j] = 0;
+        } else {
+            const int d = (j * NW + wave) * 8 + lane / 8, piece = (lane & 7) ^ (lane >> 3);
+            doff[j] = (uint32_t)d * (uint32_t)(a.ld * 2) + piece * 16;
+            dk[j] = piece * 8;
+        }
+    }
+    auto copy_dense = [&](int s) {
+        const uint32_t at = base + (uint32_t)(s & 1) * kD;
+        const int64_t k0 = (int64_t)s * 64;
+        if (TURNED) {
+            const i32x4 b = buffer(a.p + k0 * a.ld + d0, ((depth - 1 - k0) * a.ld + a.span - d0) * 2);
+#pragma unroll
+            for (int j = 0; j < CD; ++j) copy16(b, doff[j], at + (j * NW + wave) * 1024);
+        } else {
+            const i32x4 b = buffer(a.p + d0 * a.ld + k0, ((a.width - 1 - d0) * a.ld + a.span - k0) * 2);
+            const int left = (int)min((int64_t)64, depth - k0);
+#pragma unroll
+            for (int j = 0; j < CD; ++j)
+                copy16(b, dk[j] < left ? doff[j] : kOutside, at + (j * NW + wave) * 1024);
+        }
+    };
+
+    // codes: rows crow + 16 p, columns ccol .. ccol + 7 of the step
+    constexpr int kCode = FMT == Q4MX_FP4 ? 4 : 8;  // bytes of 8 codes
+    const int64_t cp = m.slices * (FMT == Q4MX_FP4 ? 64 : 128);
+    const int crow = tid / LPR, ccol = (tid % LPR) * 8;
+    const uint32_t coff = (uint32_t)crow * (uint32_t)cp + (uint32_t)(ccol / 8 * kCode);
+    const uint32_t soff = ((uint32_t)(ccol >> 7) * (uint32_t)m.rows + crow) * 4 + ((ccol >> 5) & 3);
+    const int cf = (crow & 3) | (((crow >> 3) & 1) << 2);
+    const int cat = 2 * kD + crow * (BC * 2) + (((tid % LPR) >> 1) ^ cf) * 32 + (tid & 1) * 16;
+    uint32_t code[4][kCode / 4];
+    uint32_t scale[4];
+    auto load_codes = [&](int s) {
+        const int64_t k0 = (int64_t)s * 64;
+        const auto b = readable(m.codes + k0 * cp + c0 / 8 * kCode, (m.rows - k0) * cp - c0 / 8 * kCode);
+        const int64_t sfirst = (c0 / 128) * m.rows + k0;
+        const auto bs = readable(m.scales + sfirst * 4, (m.slices * m.rows - sfirst) * 4);
+        const int left = (int)min((int64_t)64, m.rows - k0);
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+            // past the last row both read as 0 (the scale there is another
+            // row's, which may be a NaN's)
+            const bool here = crow + 16 * p < left;
+            const uint32_t o = here ? coff + (uint32_t)(16 * p) * (uint32_t)cp : kOutside;
+            if (FMT == Q4MX_FP4) {
+                code[p][0] = __builtin_amdgcn_raw_buffer_load_b32(b, (int)o, 0, 0);
+            } else {
+                const u32x2 t = __builtin_amdgcn_raw_buffer_load_b64(b, (int)o, 0, 0);
+                code[p][0] = t[0];
+                code[p][kCode / 4 - 1] = t[1];
+            }
+            scale[p] = __builtin_amdgcn_raw_buffer_load_b8(bs, (int)(here ? soff + 64 * p : kOutside), 0, 0);
+        }
+    };
+    auto decode = [&](int s) {
+        char* const at = lds + cat + (s & 1) * kC;
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+            const float f = scale_of(scale[p]);
+            uint4 v;
+            if (FMT == Q4MX_FP4)
+                v = make_uint4(bf16_pair_of(code[p][0], f, FMT, 0), bf16_pair_of(code[p][0], f, FMT, 1),
+                               bf16_pair_of(code[p][0], f, FMT, 2), bf16_pair_of(code[p][0], f, FMT, 3));
+            else
+                v = make_uint4(bf16_pair_of(code[p][0], f, FMT, 0), bf16_pair_of(code[p][0], f, FMT, 1),
+                               bf16_pair_of(code[p][kCode / 4 - 1], f, FMT, 0),
+                               bf16_pair_of(code[p][kCode / 4 - 1], f, FMT, 1));
+            *reinterpret_cast<uint4*>(at + p * 16 * (BC * 2)) = v;
+        }
+    };
+
+    // fragments: lane (r, g) reads rows k = 32 q + 8 g + r / 4 (+ 4) at columns 4 (r % 4)
+    const int r = lane & 15, g = lane >> 4, wc = wave % WC, wd = wave / WC;
+    const int f = (r >> 2) | ((g & 1) << 2), krow = g * 8 + (r >> 2);
+    int cread[FC], dread[FD];
+#pragma unroll
+    for (int i = 0; i < FC; ++i) cread[i] = 2 * kD + krow * (BC * 2) + ((wc * FC + i) ^ f) * 32 + (r & 3) * 8;
+#pragma unroll
+    for (int j = 0; j < FD; ++j)
+        dread[j] = TURNED ? krow * (BD * 2) + ((wd * FD + j) ^ f) * 32 + (r & 3) * 8 : ((wd * FD + j) * 16 + r) * 128;
+
+    f32x4 acc[FC][FD] = {};
+    if (steps > 0) {
+        copy_dense(0);
+        load_codes(0);
+        decode(0);
+        if (steps > 1) load_codes(1);
+    }
+    for (int s = 0; s < steps; ++s) {
+        // everything of step s has arrived, and every wavefront is done with
+        // the buffers that step s + 1 takes
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        if (s + 1 < steps) {
+            copy_dense(s + 1);
+            decode(s + 1);
+            if (s + 2 < steps) load_codes(s + 2);
+        }
+        const char* const cs = lds + (s & 1) * kC;
+        const char* const ds = lds + (s & 1) * kD;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            bf16x8 c[FC], d[FD];
+#pragma unroll
+            for (int j = 0; j < FD; ++j)
+                d[j] = TURNED ? read_turned(ds + dread[j] + q * 32 * (BD * 2), BD * 2)
+                              : *reinterpret_cast<const bf16x8*>(ds + dread[j] + ((4 * q + g) ^ (r & 7)) * 16);
+#pragma unroll
+            for (int i = 0; i < FC; ++i) c[i] = read_turned(cs + cread[i] + q * 32 * (BC * 2), BC * 2);
+#pragma unroll
+            for (int i = 0; i < FC; ++i)
+#pragma unroll
+                for (int j = 0; j < FD; ++j)
+                    acc[i][j] = SWAP ? __builtin_amdgcn_mfma_f32_16x16x32_bf16(d[j], c[i], acc[i][j], 0, 0, 0)
+                                     : __builtin_amdgcn_mfma_f32_16x16x32_bf16(c[i], d[j], acc[i][j], 0, 0, 0);
+        }
+    }
+    // a lane holds 4 neighbours along the first factor's axis
+#pragma unroll
+    for (int j = 0; j < FD; ++j)
+#pragma unroll
+        for (int i = 0; i < FC; ++i) {
+            const int64_t c = c0 + (wc * FC + i) * 16, d = d0 + (wd * FD + j) * 16;
+            if (SWAP) put4(out, c + r, d + g * 4, acc[i][j]);
+            else put4(out, d + r, c + g * 4, acc[i][j]);
+        }
+}
+
+// A dense operand whose rows are not 16-byte aligned runs of whole pieces:
+// copied first into rows of a multiple of 8 elements, 0 past the last.
+__global__ __launch_bounds__(256) void k_align_rows(const uint16_t* src, int64_t ld, int64_t cols, uint4* dst,
+                                                     int64_t pieces, int64_t total) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= total) return;
+    const int64_t row = i / pieces, c = (i - row * pieces) * 8;
+    const uint16_t* p = src + row * ld + c;
+    uint32_t v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const uint32_t lo = c + 2 * k < cols ? p[2 * k] : 0, hi = c + 2 * k + 1 < cols ? p[2 * k + 1] : 0;
+        v[k] = lo | (hi << 16);
+    }
+    dst[i] = make_uint4(v[0], v[1], v[2], v[3]);
+}
+
+int64_t tiles(int64_t n, int64_t b) { return (n + b - 1) / b; }
+
+// Tiles of 256 x 256 once they fill the 256 compute units, else 128 x 128.
+constexpr int64_t kFill = 192;
+
+template <bool TURNED, int FMT, bool SWAP>
+hipError_t grad(const Gradient& a, const MxMat& m, const Out& out, hipStream_t st) {
+    const int64_t big = tiles(m.cols, 256) * tiles(a.width, 256);
+    if (big >= kFill) {
+        k_mx_grad<TURNED, FMT, SWAP, 2, 4, 8, 4><<<dim3((unsigned)big), dim3(512), 0, st>>>(a, m, out);
+    } else {
+        const int64_t n = tiles(m.cols, 128) * tiles(a.width, 128);
+        k_mx_grad<TURNED, FMT, SWAP, 2, 2, 4, 4><<<dim3((unsigned)n), dim3(256), 0, st>>>(a, m, out);
+    }
     return hipGetLastError();
 }
 
-Operand dense(const Dense& d, int64_t rows, int64_t depth, bool turned) {
-    return Operand{d.p, MxMat{}, rows, depth, turned ? 1 : d.ld, turned ? d.ld : 1, false};
+// dy as the products read it: in place, or through the workspace.
+hipError_t aligned_gradient(const Dense& dy, int64_t rows, int64_t cols, void* ws, Gradient* g, hipStream_t st) {
+    *g = Gradient{static_cast<const uint16_t*>(dy.p), dy.ld, cols, 0};
+    const int64_t pieces = tiles(cols, 8), total = rows * pieces;
+    if (!dense_needs_copy(dy, rows, cols) || total == 0) return hipSuccess;
+    k_align_rows<<<dim3((unsigned)tiles(total, 256)), dim3(256), 0, st>>>(g->p, dy.ld, cols, static_cast<uint4*>(ws),
+                                                                        pieces, total);
+    *g = Gradient{static_cast<const uint16_t*>(ws), pieces * 8, pieces * 8, 0};
+    return hipGetLastError();
 }
-Operand codes(const MxMat& m, bool turned) {
-    return Operand{nullptr, m, turned ? m.cols : m.rows, turned ? m.rows : m.cols, 0, 0, turned};
+
+template <int XF> hipError_t linear(const MxMat& x, const MxMat& w, const Out& y, hipStream_t st) {
+    const int64_t big = tiles(w.rows, 256) * tiles(x.rows, 256);
+    if (big >= kFill) {
+        k_mx_linear<XF, 2, 4, 8, 4><<<dim3((unsigned)big), dim3(512), 0, st>>>(x, w, y);
+    } else {
+        const int64_t n = tiles(w.rows, 128) * tiles(x.rows, 128);
+        k_mx_linear<XF, 2, 2, 4, 4><<<dim3((unsigned)n), dim3(256), 0, st>>>(x, w, y);
+    }
+    return hipGetLastError();
 }
 
 }  // namespace
 
+bool dense_needs_copy(const Dense& d, int64_t rows, int64_t cols) {
+    return (reinterpret_cast<uintptr_t>(d.p) & 15) != 0 || (rows > 1 && d.ld % 8 != 0) || cols % 8 != 0;
+}
+size_t dense_copy_bytes(int64_t rows, int64_t cols) { return (size_t)(rows * tiles(cols, 8) * 16); }
+
 hipError_t launch_linear(const MxMat& x, const MxMat& w, const Dense& y, hipStream_t st) {
-    return product(codes(x, false), codes(w, false), Result{y.p, y.ld, 1, y.dtype, false}, st);
+    const Out out = result(y, x.rows, w.rows, false);
+    return x.fmt == Q4MX_FP4 ? linear<Q4MX_FP4>(x, w, out, st) : linear<Q4MX_FP8>(x, w, out, st);
 }
 
-hipError_t launch_dgrad(const Dense& dy, int64_t tokens, const MxMat& w, const Dense& dx, hipStream_t st) {
-    return product(dense(dy, tokens, w.rows, false), codes(w, true), Result{dx.p, dx.ld, 1, dx.dtype, false}, st);
+hipError_t launch_dgrad(const Dense& dy, int64_t tokens, const MxMat& w, const Dense& dx, void* ws, hipStream_t st) {
+    Gradient g;
+    const hipError_t e = aligned_gradient(dy, tokens, w.rows, ws, &g, st);
+    if (e != hipSuccess) return e;
+    g.width = tokens;
+    return grad<false, Q4MX_FP4, false>(g, w, result(dx, tokens, w.cols, false), st);
 }
 
 hipError_t launch_wgrad(const Dense& dy, int64_t n, const MxMat& x, const Dense& dw, bool transposed, bool add,
-                        hipStream_t st) {
-    return product(dense(dy, n, x.rows, true), codes(x, true),
-                   Result{dw.p, transposed ? 1 : dw.ld, transposed ? dw.ld : 1, dw.dtype, add}, st);
+                        void* ws, hipStream_t st) {
+    Gradient g;
+    const hipError_t e = aligned_gradient(dy, x.rows, n, ws, &g, st);
+    if (e != hipSuccess) return e;
+    g.width = n;
+    const Out out = transposed ? result(dw, x.cols, n, add) : result(dw, n, x.cols, add);
+    if (x.fmt == Q4MX_FP4)
+        return transposed ? grad<true, Q4MX_FP4, true>(g, x, out, st) : grad<true, Q4MX_FP4, false>(g, x, out, st);
+    return transposed ? grad<true, Q4MX_FP8, true>(g, x, out, st) : grad<true, Q4MX_FP8, false>(g, x, out, st);
 }
 
 }  // namespace q4
