@@ -42,11 +42,16 @@ hipError_t launch_act_backward(int act, const MxMat& kx, const MxMat& ku, const 
 bool dense_needs_copy(const Dense& d, int64_t rows, int64_t cols);
 size_t dense_copy_bytes(int64_t rows, int64_t cols);
 
-// The three products.  add: the result is added to what out holds.  ws: the
-// copy of dy, if it needs one.
-hipError_t launch_linear(const MxMat& x, const MxMat& w, const Dense& y, hipStream_t st);
-hipError_t launch_dgrad(const Dense& dy, int64_t tokens, const MxMat& w, const Dense& dx, void* ws, hipStream_t st);
+// Workspaces of the products: the sums of tiles that are split along the sum.
+size_t linear_workspace(const MxMat& x, const MxMat& w);
+size_t grad_workspace(const MxMat& m, int64_t width);  // m: w (width: tokens) or x (width: n)
+
+// The three products.  add: the result is added to what out holds.  copy: room
+// for the copy of dy, if it needs one.
+hipError_t launch_linear(const MxMat& x, const MxMat& w, const Dense& y, void* ws, hipStream_t st);
+hipError_t launch_dgrad(const Dense& dy, int64_t tokens, const MxMat& w, const Dense& dx, void* copy, void* ws,
+                        hipStream_t st);
 hipError_t launch_wgrad(const Dense& dy, int64_t n, const MxMat& x, const Dense& dw, bool transposed, bool add,
-                        void* ws, hipStream_t st);
+                        void* copy, void* ws, hipStream_t st);
 
 }  // namespace q4

@@ -94,7 +94,16 @@ Quantized quantized(int64_t tokens, int64_t cols) {
     return Quantized{round256((size_t)(tokens * padded(cols))), round256((size_t)(tokens * padded(cols) / 32))};
 }
 
-// Workspace of a gradient product: the copy of a dy whose rows are not aligned.
+// The same product's workspace: those, then the product's own.
+MxMat quantized_at(uint8_t* p, const Quantized& q, int64_t tokens, int64_t cols) {
+    return MxMat{p, p ? p + q.codes : nullptr, tokens, cols, padded(cols) / kMxPad, Q4MX_FP8};
+}
+size_t bf16_workspace(int64_t tokens, const q4mx_matrix* w) {
+    const Quantized q = quantized(tokens, w->cols);
+    return q.bytes() + linear_workspace(quantized_at(nullptr, q, tokens, w->cols), mat(w));
+}
+
+// Workspace of a gradient product, in front of the product's own: the copy of a dy whose rows are not aligned.
 size_t copy_bytes(const uint16_t* dy, int64_t lddy, int64_t rows, int64_t cols) {
     if (rows == 0 || cols == 0 || !dense_needs_copy(Dense{const_cast<uint16_t*>(dy), lddy, Q4MX_BF16}, rows, cols))
         return 0;
@@ -163,7 +172,7 @@ q4_status q4mx_linear_workspace_bytes(const q4mx_matrix* x, const q4mx_matrix* w
     if (!bytes) return bad(Q4_ERR_INVALID_ARG, "output is NULL");
     Q4_TRY(check_mx_shape("x", x));
     Q4_TRY(check_mx_shape("w", w));
-    *bytes = 0;
+    *bytes = linear_workspace(mat(x), mat(w));
     return ok();
 }
 
@@ -179,7 +188,7 @@ q4_status q4mx_linear(const q4mx_matrix* x, const q4mx_matrix* w, void* y, int32
     Q4_TRY(q4mx_linear_workspace_bytes(x, w, &need));
     Q4_TRY(check_ws(ws, ws_bytes, need));
     Q4_TRY(device());
-    return launched(launch_linear(mat(x), mat(w), Dense{y, ldy, dtype}, reinterpret_cast<hipStream_t>(stream)),
+    return launched(launch_linear(mat(x), mat(w), Dense{y, ldy, dtype}, ws, reinterpret_cast<hipStream_t>(stream)),
                     "linear launch");
 }
 
@@ -187,7 +196,7 @@ q4_status q4mx_linear_bf16_workspace_bytes(int64_t tokens, const q4mx_matrix* w,
     if (!bytes) return bad(Q4_ERR_INVALID_ARG, "output is NULL");
     Q4_TRY(check_mx_shape("w", w));
     Q4_TRY(check_shape("x", Q4MX_FP8, tokens, w->cols));
-    *bytes = quantized(tokens, w->cols).bytes();
+    *bytes = bf16_workspace(tokens, w);
     return ok();
 }
 
@@ -199,17 +208,17 @@ q4_status q4mx_linear_bf16(const uint16_t* x, int64_t ldx, int64_t tokens, const
     Q4_TRY(check_dense("y", y, dtype, tokens, w->rows, ldy));
     if (tokens == 0 || w->rows == 0) return ok();
     const Quantized q = quantized(tokens, w->cols);
-    Q4_TRY(check_ws(ws, ws_bytes, q.bytes()));
+    Q4_TRY(check_ws(ws, ws_bytes, bf16_workspace(tokens, w)));
     Q4_TRY(device());
     hipStream_t st = reinterpret_cast<hipStream_t>(stream);
     uint8_t* p = static_cast<uint8_t*>(ws);
-    const MxMat xq{p, p + q.codes, tokens, w->cols, padded(w->cols) / kMxPad, Q4MX_FP8};
+    const MxMat xq = quantized_at(p, q, tokens, w->cols);
     if (w->cols > 0) {
         const hipError_t e =
             launch_mx_quantize(Dense{const_cast<uint16_t*>(x), ldx, Q4MX_BF16}, false, xq, st);
         if (e != hipSuccess) return launched(e, "quantize launch");
     }
-    return launched(launch_linear(xq, mat(w), Dense{y, ldy, dtype}, st), "linear launch");
+    return launched(launch_linear(xq, mat(w), Dense{y, ldy, dtype}, p + q.bytes(), st), "linear launch");
 }
 
 q4_status q4mx_dgrad_workspace_bytes(const uint16_t* dy, int64_t lddy, int64_t tokens, const q4mx_matrix* w,
@@ -217,7 +226,7 @@ q4_status q4mx_dgrad_workspace_bytes(const uint16_t* dy, int64_t lddy, int64_t t
     if (!bytes) return bad(Q4_ERR_INVALID_ARG, "output is NULL");
     Q4_TRY(check_mx_shape("w", w));
     Q4_TRY(check_dense("dy", dy, Q4MX_BF16, tokens, w->rows, lddy));
-    *bytes = copy_bytes(dy, lddy, tokens, w->rows);
+    *bytes = copy_bytes(dy, lddy, tokens, w->rows) + grad_workspace(mat(w), tokens);
     return ok();
 }
 
@@ -233,7 +242,8 @@ q4_status q4mx_dgrad(const uint16_t* dy, int64_t lddy, int64_t tokens, const q4m
     Q4_TRY(check_ws(ws, ws_bytes, need));
     Q4_TRY(device());
     return launched(launch_dgrad(Dense{const_cast<uint16_t*>(dy), lddy, Q4MX_BF16}, tokens, mat(w),
-                                 Dense{dx, lddx, dtype}, ws, reinterpret_cast<hipStream_t>(stream)),
+                                 Dense{dx, lddx, dtype}, ws,
+                                 static_cast<char*>(ws) + copy_bytes(dy, lddy, tokens, w->rows), reinterpret_cast<hipStream_t>(stream)),
                     "dgrad launch");
 }
 
@@ -243,7 +253,7 @@ q4_status q4mx_wgrad_workspace_bytes(const uint16_t* dy, int64_t lddy, int64_t n
     if (flags & ~(Q4MX_WGRAD_TRANSPOSED | Q4MX_WGRAD_ADD)) return bad(Q4_ERR_INVALID_ARG, "unknown flags 0x%x", flags);
     Q4_TRY(check_mx_shape("x", x));
     Q4_TRY(check_dense("dy", dy, Q4MX_BF16, x->rows, n, lddy));
-    *bytes = copy_bytes(dy, lddy, x->rows, n);
+    *bytes = copy_bytes(dy, lddy, x->rows, n) + grad_workspace(mat(x), n);
     return ok();
 }
 
@@ -261,7 +271,8 @@ q4_status q4mx_wgrad(const uint16_t* dy, int64_t lddy, int64_t n, const q4mx_mat
     Q4_TRY(check_ws(ws, ws_bytes, need));
     Q4_TRY(device());
     return launched(launch_wgrad(Dense{const_cast<uint16_t*>(dy), lddy, Q4MX_BF16}, n, mat(x), Dense{dw, lddw, dtype},
-                                 t, (flags & Q4MX_WGRAD_ADD) != 0, ws, reinterpret_cast<hipStream_t>(stream)),
+                                 t, (flags & Q4MX_WGRAD_ADD) != 0, ws, static_cast<char*>(ws) + copy_bytes(dy, lddy, x->rows, n),
+                                 reinterpret_cast<hipStream_t>(stream)),
                     "wgrad launch");
 }
 

@@ -26,18 +26,51 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 // ---- tiles, buffers, shared memory -------------------------------------------
 
-// Work-group -> tile.  Consecutive work-groups go to the 8 XCDs in turn, each
-// with an L2 of its own; the renumbering gives each XCD one contiguous run of
-// tiles, taken in bands of 4 along the first axis, so that the tiles that run
-// together on an XCD share rows of both operands.
-__device__ __forceinline__ void tile_of(uint32_t bid, uint32_t n0, uint32_t n1, uint32_t& i0, uint32_t& i1) {
-    const uint32_t total = n0 * n1, q = total / 8, r = total % 8, x = bid % 8;
-    const uint32_t id = x * q + min(x, r) + bid / 8;
+// How a product is cut into work-groups: `full` tiles whole, then the other
+// `rest` tiles each in `split` runs of steps whose sums are joined afterwards
+// (split = 1: those are whole too).
+struct Cut {
+    uint32_t n0, n1;  // tiles along both axes
+    uint32_t full, rest, split;
+    f32x4* part;      // sums of the runs, [rest * split][fragments][threads]
+};
+
+struct Unit {
+    uint32_t i0, i1;
+    int first, last;  // its steps
+    f32x4* part;      // where its sums go; NULL: it forms the whole sum
+};
+
+// Tile number -> tile, in bands of 4 along the first axis: tiles that run
+// together share rows of both operands.
+__device__ __forceinline__ void tile_at(const Cut& c, uint32_t id, uint32_t& i0, uint32_t& i1) {
     constexpr uint32_t kBand = 4;
-    const uint32_t band = id / (kBand * n1), first = band * kBand, h = min(n0 - first, kBand);
-    const uint32_t in = id - band * (kBand * n1);
+    const uint32_t band = id / (kBand * c.n1), first = band * kBand, h = min(c.n0 - first, kBand);
+    const uint32_t in = id - band * (kBand * c.n1);
     i0 = first + in % h;
     i1 = in / h;
+}
+
+// Work-group -> unit.  Consecutive work-groups go to the 8 XCDs in turn, each
+// with an L2 of its own; the renumbering gives each XCD contiguous runs of
+// tiles.  Units of the split tiles come run by run, so that those that run
+// together are different tiles of the same steps.
+__device__ __forceinline__ Unit unit_of(const Cut& c, int steps, int frags) {
+    const uint32_t bid = blockIdx.x, n = bid < c.full ? c.full : c.rest * c.split;
+    const uint32_t local = bid < c.full ? bid : bid - c.full, q = n / 8, r = n % 8, x = local % 8;
+    const uint32_t id = x * q + min(x, r) + local / 8;
+    Unit u;
+    if (bid < c.full || c.split == 1) {
+        tile_at(c, bid < c.full ? id : c.full + id, u.i0, u.i1);
+        u.first = 0, u.last = steps, u.part = nullptr;
+        return u;
+    }
+    const uint32_t run = id / c.rest, tile = id - run * c.rest;
+    tile_at(c, c.full + tile, u.i0, u.i1);
+    u.first = (int)((int64_t)steps * run / c.split);
+    u.last = (int)((int64_t)steps * (run + 1) / c.split);
+    u.part = c.part + ((int64_t)tile * c.split + run) * frags * blockDim.x;
+    return u;
 }
 
 // A raw buffer: loads past `bytes` read as 0 (checked per dword).
@@ -57,7 +90,8 @@ __device__ __forceinline__ auto readable(const void* p, int64_t bytes) {
     return __builtin_amdgcn_make_buffer_rsrc(
         reinterpret_cast<void*>((uint64_t)(uint32_t)b[0] | ((uint64_t)(uint32_t)b[1] << 32)), 0, b[2], b[3]);
 }
-constexpr uint32_t kOutside = 0xFFFFFFF0u;  // an offset past every buffer
+// `off` where i < n, else an offset past every buffer (without a branch).
+__device__ __forceinline__ uint32_t inside(uint32_t off, int i, int n) { return off | (uint32_t)((n - 1 - i) >> 31); }
 
 // A wavefront copies 64 x 16 (or 4) bytes into shared memory from byte `lds`
 // on, lane i's piece at lds + 16 i (4 i), without passing through registers.
@@ -138,7 +172,7 @@ Out result(const Dense& d, int64_t rows, int64_t cols, bool add) {
 // the E2M1 codes of columns 32 g .. 32 g + 31, or the E4M3 codes of columns 16
 // g .. +15 and 64 + 16 g .. +15, and the scale byte of columns 32 g .. +31.
 template <int XF, int WN, int WT, int FN, int FT>
-__global__ __launch_bounds__(64 * WN* WT, 2) void k_mx_linear(MxMat x, MxMat w, Out y) {
+__global__ __launch_bounds__(64 * WN* WT, 2) void k_mx_linear(MxMat x, MxMat w, Out y, Cut cut) {
     constexpr int NW = WN * WT, BN = WN * FN * 16, BT = WT * FT * 16;
     constexpr int XB = XF == Q4MX_FP4 ? 64 : 128;
     constexpr int kW = BN * 64, kX = BT * XB, kStage = kW + kX + (BN + BT) * 4;
@@ -147,11 +181,9 @@ __global__ __launch_bounds__(64 * WN* WT, 2) void k_mx_linear(MxMat x, MxMat w, 
     __shared__ __attribute__((aligned(1024))) char lds[3 * kStage];
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    uint32_t in, it;
-    tile_of(blockIdx.x, (uint32_t)((w.rows + BN - 1) / BN), (uint32_t)((x.rows + BT - 1) / BT), in, it);
-    const int64_t n0 = (int64_t)in * BN, t0 = (int64_t)it * BT;
+    const Unit u = unit_of(cut, (int)w.slices, FN * FT);
+    const int64_t n0 = (int64_t)u.i0 * BN, t0 = (int64_t)u.i1 * BT;
     const int64_t wp = w.slices * 64, xp = x.slices * XB;
-    const int steps = (int)w.slices;
 
     uint32_t woff[CW], xoff[CX];
 #pragma unroll
@@ -190,14 +222,14 @@ __global__ __launch_bounds__(64 * WN* WT, 2) void k_mx_linear(MxMat x, MxMat w, 
     const int wsat = kW + kX + wrow * 4 + g, xsat = kW + kX + BN * 4 + xrow * 4 + g;
 
     f32x4 acc[FN][FT] = {};
-    if (steps > 0) issue(0);
-    if (steps > 1) issue(1);
-    for (int s = 0; s < steps; ++s) {
+    if (u.first < u.last) issue(u.first);
+    if (u.first + 1 < u.last) issue(u.first + 1);
+    for (int s = u.first; s < u.last; ++s) {
         // this step's copies are done (the next step's may be under way), and
         // every wavefront is done with the buffer that step s + 2 takes
-        if (s + 1 < steps) wait_copies_and_barrier<kCopies>();
+        if (s + 1 < u.last) wait_copies_and_barrier<kCopies>();
         else wait_copies_and_barrier<0>();
-        if (s + 2 < steps) issue(s + 2);
+        if (s + 2 < u.last) issue(s + 2);
         const char* const st = lds + (s % 3) * kStage;
         i32x8 b[FT], a[FN];
         int sa[FN], sb[FT];
@@ -221,6 +253,13 @@ __global__ __launch_bounds__(64 * WN* WT, 2) void k_mx_linear(MxMat x, MxMat w, 
             for (int j = 0; j < FT; ++j)
                 acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a[i], b[j], acc[i][j], 4,
                                                                              XF == Q4MX_FP4 ? 4 : 0, 0, sa[i], 0, sb[j]);
+    }
+    if (u.part) {
+#pragma unroll
+        for (int i = 0; i < FN; ++i)
+#pragma unroll
+            for (int j = 0; j < FT; ++j) u.part[(i * FT + j) * blockDim.x + threadIdx.x] = acc[i][j];
+        return;
     }
 #pragma unroll
     for (int j = 0; j < FT; ++j)
@@ -285,7 +324,7 @@ struct Gradient {
 };
 
 template <bool TURNED, int FMT, bool SWAP, int WC, int WD, int FC, int FD>
-__global__ __launch_bounds__(64 * WC* WD, 2) void k_mx_grad(Gradient a, MxMat m, Out out) {
+__global__ __launch_bounds__(64 * WC* WD, 2) void k_mx_grad(Gradient a, MxMat m, Out out, Cut cut) {
     constexpr int NW = WC * WD, BC = WC * FC * 16, BD = WD * FD * 16;
     constexpr int kD = BD * 128, kC = BC * 128;  // bytes of a step
     constexpr int CD = kD / 1024 / NW;
@@ -294,11 +333,9 @@ __global__ __launch_bounds__(64 * WC* WD, 2) void k_mx_grad(Gradient a, MxMat m,
     __shared__ __attribute__((aligned(1024))) char lds[2 * (kD + kC)];
 
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    uint32_t ic, id;
-    tile_of(blockIdx.x, (uint32_t)((m.cols + BC - 1) / BC), (uint32_t)((a.width + BD - 1) / BD), ic, id);
-    const int64_t c0 = (int64_t)ic * BC, d0 = (int64_t)id * BD;
     const int64_t depth = m.rows;
-    const int steps = (int)((depth + 63) / 64);
+    const Unit u = unit_of(cut, (int)((depth + 63) / 64), FC * FD);
+    const int64_t c0 = (int64_t)u.i0 * BC, d0 = (int64_t)u.i1 * BD;
     const uint32_t base = lds_base(lds);
 
     // dense: this lane's pieces of the step's copies
@@ -330,7 +367,7 @@ __global__ __launch_bounds__(64 * WC* WD, 2) void k_mx_grad(Gradient a, MxMat m,
             const int left = (int)min((int64_t)64, depth - k0);
 #pragma unroll
             for (int j = 0; j < CD; ++j)
-                copy16(b, dk[j] < left ? doff[j] : kOutside, at + (j * NW + wave) * 1024);
+                copy16(b, inside(doff[j], dk[j], left), at + (j * NW + wave) * 1024);
         }
     };
 
@@ -354,8 +391,7 @@ __global__ __launch_bounds__(64 * WC* WD, 2) void k_mx_grad(Gradient a, MxMat m,
         for (int p = 0; p < 4; ++p) {
             // past the last row both read as 0 (the scale there is another
             // row's, which may be a NaN's)
-            const bool here = crow + 16 * p < left;
-            const uint32_t o = here ? coff + (uint32_t)(16 * p) * (uint32_t)cp : kOutside;
+            const uint32_t o = inside(coff + (uint32_t)(16 * p) * (uint32_t)cp, crow + 16 * p, left);
             if (FMT == Q4MX_FP4) {
                 code[p][0] = __builtin_amdgcn_raw_buffer_load_b32(b, (int)o, 0, 0);
             } else {
@@ -363,7 +399,7 @@ __global__ __launch_bounds__(64 * WC* WD, 2) void k_mx_grad(Gradient a, MxMat m,
                 code[p][0] = t[0];
                 code[p][kCode / 4 - 1] = t[1];
             }
-            scale[p] = __builtin_amdgcn_raw_buffer_load_b8(bs, (int)(here ? soff + 64 * p : kOutside), 0, 0);
+            scale[p] = __builtin_amdgcn_raw_buffer_load_b8(bs, (int)inside(soff + 64 * p, crow + 16 * p, left), 0, 0);
         }
     };
     auto decode = [&](int s) {
@@ -394,23 +430,23 @@ __global__ __launch_bounds__(64 * WC* WD, 2) void k_mx_grad(Gradient a, MxMat m,
         dread[j] = TURNED ? krow * (BD * 2) + ((wd * FD + j) ^ f) * 32 + (r & 3) * 8 : ((wd * FD + j) * 16 + r) * 128;
 
     f32x4 acc[FC][FD] = {};
-    if (steps > 0) {
-        copy_dense(0);
-        load_codes(0);
-        decode(0);
-        if (steps > 1) load_codes(1);
+    if (u.first < u.last) {
+        copy_dense(u.first);
+        load_codes(u.first);
+        decode(u.first);
+        if (u.first + 1 < u.last) load_codes(u.first + 1);
     }
-    for (int s = 0; s < steps; ++s) {
+    for (int s = u.first; s < u.last; ++s) {
         // everything of step s has arrived, and every wavefront is done with
         // the buffers that step s + 1 takes
         asm volatile("" ::: "memory");
         __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
-        if (s + 1 < steps) {
+        if (s + 1 < u.last) {
             copy_dense(s + 1);
             decode(s + 1);
-            if (s + 2 < steps) load_codes(s + 2);
+            if (s + 2 < u.last) load_codes(s + 2);
         }
         const char* const cs = lds + (s & 1) * kC;
         const char* const ds = lds + (s & 1) * kD;
@@ -430,6 +466,13 @@ __global__ __launch_bounds__(64 * WC* WD, 2) void k_mx_grad(Gradient a, MxMat m,
                     acc[i][j] = SWAP ? __builtin_amdgcn_mfma_f32_16x16x32_bf16(d[j], c[i], acc[i][j], 0, 0, 0)
                                      : __builtin_amdgcn_mfma_f32_16x16x32_bf16(c[i], d[j], acc[i][j], 0, 0, 0);
         }
+    }
+    if (u.part) {
+#pragma unroll
+        for (int i = 0; i < FC; ++i)
+#pragma unroll
+            for (int j = 0; j < FD; ++j) u.part[(i * FD + j) * blockDim.x + threadIdx.x] = acc[i][j];
+        return;
     }
     // a lane holds 4 neighbours along the first factor's axis
 #pragma unroll
@@ -459,42 +502,117 @@ __global__ __launch_bounds__(256) void k_align_rows(const uint16_t* src, int64_t
     dst[i] = make_uint4(v[0], v[1], v[2], v[3]);
 }
 
+// Joins the runs of split tiles: the sums of one fragment (16 x 16 results of
+// every wavefront), in the order of the runs, and their place in the result.
+// SWAP: a lane's 4 results lie along the second axis of the tile grid, else
+// along the first.
+template <int W0, int W1, int F0, int F1, bool SWAP>
+__global__ __launch_bounds__(64 * W0* W1) void k_mx_join(Cut cut, Out out) {
+    constexpr int B0 = W0 * F0 * 16, B1 = W1 * F1 * 16;
+    const uint32_t tile = blockIdx.x / (F0 * F1), frag = blockIdx.x % (F0 * F1);
+    uint32_t i0, i1;
+    tile_at(cut, cut.full + tile, i0, i1);
+    const f32x4* p = cut.part + ((int64_t)tile * cut.split * (F0 * F1) + frag) * blockDim.x + threadIdx.x;
+    f32x4 v = {0, 0, 0, 0};
+    for (uint32_t k = 0; k < cut.split; ++k) v += p[(int64_t)k * (F0 * F1) * blockDim.x];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
+    const int64_t a = (int64_t)i0 * B0 + (wave % W0 * F0 + frag / F1) * 16;
+    const int64_t b = (int64_t)i1 * B1 + (wave / W0 * F1 + frag % F1) * 16;
+    if (SWAP) put4(out, a + r, b + g * 4, v);
+    else put4(out, b + r, a + g * 4, v);
+}
+
+// ---- how a product is cut ---------------------------------------------------------
+//
+// Two tiles: 256 x 256 by 8 wavefronts, one work-group per compute unit, and
+// 128 x 128 by 4, two per unit (their step costs less than half as much, but
+// more per result).  Where the last round of tiles would leave most units
+// idle, its tiles are split along the sum.  The choice minimizes an estimate
+// of the time: rounds of work-groups times steps, plus what the runs' sums
+// cost to write, read and join.
+struct TileCost {
+    double step;  // microseconds of a step with every unit busy
+    double ends;  // of a work-group's start and end
+};
+constexpr double kPartBytesPerUs = 4.0e6, kJoinUs = 4.0;
+
+struct Plan {
+    bool big;
+    Cut cut;
+    size_t bytes;  // of the runs' sums
+};
+
 int64_t tiles(int64_t n, int64_t b) { return (n + b - 1) / b; }
 
-// Tiles of 256 x 256 once they fill the 256 compute units, else 128 x 128.
-constexpr int64_t kFill = 192;
+Plan plan_of(int64_t n0, int64_t n1, int64_t steps, const TileCost& big, const TileCost& small) {
+    Plan best{};
+    double best_us = 0;
+    for (int k = 0; k < 2; ++k) {
+        const int64_t b = k == 0 ? 256 : 128, slots = k == 0 ? 256 : 512;
+        const TileCost& c = k == 0 ? big : small;
+        const int64_t t0 = tiles(n0, b), t1 = tiles(n1, b), total = t0 * t1;
+        const int64_t full = total / slots * slots, rest = total - full;
+        for (int64_t split = 1; split <= 32 && (split == 1 || (rest > 0 && steps / split >= 2)); ++split) {
+            const int64_t rounds = tiles(rest * split, slots);
+            const size_t bytes = split == 1 ? 0 : (size_t)(rest * split * b * b * 4);
+            double us = (double)(full / slots) * ((double)steps * c.step + c.ends) +
+                        (double)rounds * ((double)tiles(steps, split) * c.step + c.ends);
+            if (split > 1) us += kJoinUs + 2.0 * (double)bytes / kPartBytesPerUs;
+            if (best.cut.n0 == 0 || us < best_us) {
+                best_us = us;
+                best = Plan{k == 0, Cut{(uint32_t)t0, (uint32_t)t1, (uint32_t)full, (uint32_t)rest, (uint32_t)split, nullptr},
+                            bytes};
+            }
+        }
+    }
+    return best;
+}
+
+Plan linear_plan(const MxMat& x, const MxMat& w) {
+    return x.fmt == Q4MX_FP4 ? plan_of(w.rows, x.rows, w.slices, TileCost{1.2, 4}, TileCost{0.8, 3})
+                             : plan_of(w.rows, x.rows, w.slices, TileCost{1.9, 4}, TileCost{1.2, 3});
+}
+Plan grad_plan(const MxMat& m, int64_t width) {
+    return plan_of(m.cols, width, tiles(m.rows, 64), TileCost{1.7, 4}, TileCost{1.1, 3});
+}
 
 template <bool TURNED, int FMT, bool SWAP>
-hipError_t grad(const Gradient& a, const MxMat& m, const Out& out, hipStream_t st) {
-    const int64_t big = tiles(m.cols, 256) * tiles(a.width, 256);
-    if (big >= kFill) {
-        k_mx_grad<TURNED, FMT, SWAP, 2, 4, 8, 4><<<dim3((unsigned)big), dim3(512), 0, st>>>(a, m, out);
-    } else {
-        const int64_t n = tiles(m.cols, 128) * tiles(a.width, 128);
-        k_mx_grad<TURNED, FMT, SWAP, 2, 2, 4, 4><<<dim3((unsigned)n), dim3(256), 0, st>>>(a, m, out);
-    }
+hipError_t grad(const Gradient& a, const MxMat& m, const Out& out, void* ws, hipStream_t st) {
+    const Plan p = grad_plan(m, a.width);
+    Cut cut = p.cut;
+    cut.part = static_cast<f32x4*>(ws);
+    const dim3 units(cut.full + cut.rest * cut.split), joins(cut.rest * (p.big ? 32 : 16));
+    if (p.big) k_mx_grad<TURNED, FMT, SWAP, 2, 4, 8, 4><<<units, dim3(512), 0, st>>>(a, m, out, cut);
+    else k_mx_grad<TURNED, FMT, SWAP, 2, 2, 4, 4><<<units, dim3(256), 0, st>>>(a, m, out, cut);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || cut.split == 1) return e;
+    if (p.big) k_mx_join<2, 4, 8, 4, SWAP><<<joins, dim3(512), 0, st>>>(cut, out);
+    else k_mx_join<2, 2, 4, 4, SWAP><<<joins, dim3(256), 0, st>>>(cut, out);
+    return hipGetLastError();
+}
+
+template <int XF> hipError_t linear(const MxMat& x, const MxMat& w, const Out& y, void* ws, hipStream_t st) {
+    const Plan p = linear_plan(x, w);
+    Cut cut = p.cut;
+    cut.part = static_cast<f32x4*>(ws);
+    const dim3 units(cut.full + cut.rest * cut.split), joins(cut.rest * (p.big ? 32 : 16));
+    if (p.big) k_mx_linear<XF, 2, 4, 8, 4><<<units, dim3(512), 0, st>>>(x, w, y, cut);
+    else k_mx_linear<XF, 2, 2, 4, 4><<<units, dim3(256), 0, st>>>(x, w, y, cut);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || cut.split == 1) return e;
+    if (p.big) k_mx_join<2, 4, 8, 4, false><<<joins, dim3(512), 0, st>>>(cut, y);
+    else k_mx_join<2, 2, 4, 4, false><<<joins, dim3(256), 0, st>>>(cut, y);
     return hipGetLastError();
 }
 
 // dy as the products read it: in place, or through the workspace.
-hipError_t aligned_gradient(const Dense& dy, int64_t rows, int64_t cols, void* ws, Gradient* g, hipStream_t st) {
+hipError_t aligned_gradient(const Dense& dy, int64_t rows, int64_t cols, void* copy, Gradient* g, hipStream_t st) {
     *g = Gradient{static_cast<const uint16_t*>(dy.p), dy.ld, cols, 0};
     const int64_t pieces = tiles(cols, 8), total = rows * pieces;
     if (!dense_needs_copy(dy, rows, cols) || total == 0) return hipSuccess;
-    k_align_rows<<<dim3((unsigned)tiles(total, 256)), dim3(256), 0, st>>>(g->p, dy.ld, cols, static_cast<uint4*>(ws),
+    k_align_rows<<<dim3((unsigned)tiles(total, 256)), dim3(256), 0, st>>>(g->p, dy.ld, cols, static_cast<uint4*>(copy),
                                                                         pieces, total);
-    *g = Gradient{static_cast<const uint16_t*>(ws), pieces * 8, pieces * 8, 0};
-    return hipGetLastError();
-}
-
-template <int XF> hipError_t linear(const MxMat& x, const MxMat& w, const Out& y, hipStream_t st) {
-    const int64_t big = tiles(w.rows, 256) * tiles(x.rows, 256);
-    if (big >= kFill) {
-        k_mx_linear<XF, 2, 4, 8, 4><<<dim3((unsigned)big), dim3(512), 0, st>>>(x, w, y);
-    } else {
-        const int64_t n = tiles(w.rows, 128) * tiles(x.rows, 128);
-        k_mx_linear<XF, 2, 2, 4, 4><<<dim3((unsigned)n), dim3(256), 0, st>>>(x, w, y);
-    }
+    *g = Gradient{static_cast<const uint16_t*>(copy), pieces * 8, pieces * 8, 0};
     return hipGetLastError();
 }
 
@@ -505,29 +623,33 @@ bool dense_needs_copy(const Dense& d, int64_t rows, int64_t cols) {
 }
 size_t dense_copy_bytes(int64_t rows, int64_t cols) { return (size_t)(rows * tiles(cols, 8) * 16); }
 
-hipError_t launch_linear(const MxMat& x, const MxMat& w, const Dense& y, hipStream_t st) {
+size_t linear_workspace(const MxMat& x, const MxMat& w) { return linear_plan(x, w).bytes; }
+size_t grad_workspace(const MxMat& m, int64_t width) { return grad_plan(m, width).bytes; }
+
+hipError_t launch_linear(const MxMat& x, const MxMat& w, const Dense& y, void* ws, hipStream_t st) {
     const Out out = result(y, x.rows, w.rows, false);
-    return x.fmt == Q4MX_FP4 ? linear<Q4MX_FP4>(x, w, out, st) : linear<Q4MX_FP8>(x, w, out, st);
+    return x.fmt == Q4MX_FP4 ? linear<Q4MX_FP4>(x, w, out, ws, st) : linear<Q4MX_FP8>(x, w, out, ws, st);
 }
 
-hipError_t launch_dgrad(const Dense& dy, int64_t tokens, const MxMat& w, const Dense& dx, void* ws, hipStream_t st) {
+hipError_t launch_dgrad(const Dense& dy, int64_t tokens, const MxMat& w, const Dense& dx, void* copy, void* ws,
+                        hipStream_t st) {
     Gradient g;
-    const hipError_t e = aligned_gradient(dy, tokens, w.rows, ws, &g, st);
+    const hipError_t e = aligned_gradient(dy, tokens, w.rows, copy, &g, st);
     if (e != hipSuccess) return e;
     g.width = tokens;
-    return grad<false, Q4MX_FP4, false>(g, w, result(dx, tokens, w.cols, false), st);
+    return grad<false, Q4MX_FP4, false>(g, w, result(dx, tokens, w.cols, false), ws, st);
 }
 
 hipError_t launch_wgrad(const Dense& dy, int64_t n, const MxMat& x, const Dense& dw, bool transposed, bool add,
-                        void* ws, hipStream_t st) {
+                        void* copy, void* ws, hipStream_t st) {
     Gradient g;
-    const hipError_t e = aligned_gradient(dy, x.rows, n, ws, &g, st);
+    const hipError_t e = aligned_gradient(dy, x.rows, n, copy, &g, st);
     if (e != hipSuccess) return e;
     g.width = n;
     const Out out = transposed ? result(dw, x.cols, n, add) : result(dw, n, x.cols, add);
     if (x.fmt == Q4MX_FP4)
-        return transposed ? grad<true, Q4MX_FP4, true>(g, x, out, st) : grad<true, Q4MX_FP4, false>(g, x, out, st);
-    return transposed ? grad<true, Q4MX_FP8, true>(g, x, out, st) : grad<true, Q4MX_FP8, false>(g, x, out, st);
+        return transposed ? grad<true, Q4MX_FP4, true>(g, x, out, ws, st) : grad<true, Q4MX_FP4, false>(g, x, out, ws, st);
+    return transposed ? grad<true, Q4MX_FP8, true>(g, x, out, ws, st) : grad<true, Q4MX_FP8, false>(g, x, out, ws, st);
 }
 
 }  // namespace q4
