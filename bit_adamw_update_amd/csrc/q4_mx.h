@@ -48,6 +48,7 @@ size_t grad_workspace(const MxMat& m, int64_t width);  // m: w (width: tokens) o
 
 // The three products.  add: the result is added to what out holds.  copy: room
 // for the copy of dy, if it needs one.
+hipError_t launch_linear_few(const Dense& x, int64_t tokens, const MxMat& w, const Dense& y, hipStream_t st);  // BF16 x
 hipError_t launch_linear(const MxMat& x, const MxMat& w, const Dense& y, void* ws, hipStream_t st);
 hipError_t launch_dgrad(const Dense& dy, int64_t tokens, const MxMat& w, const Dense& dx, void* copy, void* ws,
                         hipStream_t st);

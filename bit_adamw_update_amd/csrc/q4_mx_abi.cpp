@@ -99,6 +99,7 @@ MxMat quantized_at(uint8_t* p, const Quantized& q, int64_t tokens, int64_t cols)
     return MxMat{p, p ? p + q.codes : nullptr, tokens, cols, padded(cols) / kMxPad, Q4MX_FP8};
 }
 size_t bf16_workspace(int64_t tokens, const q4mx_matrix* w) {
+    if (tokens <= Q4MX_FEW_TOKENS) return 0;
     const Quantized q = quantized(tokens, w->cols);
     return q.bytes() + linear_workspace(quantized_at(nullptr, q, tokens, w->cols), mat(w));
 }
@@ -125,6 +126,12 @@ q4_status device() {
 constexpr int64_t kMaxWidth = int64_t(1) << 23;
 q4_status check_width(const char* name, int64_t n) {
     if (n >= kMaxWidth) return bad(Q4_ERR_SHAPE, "%s is %lld, a product takes less than 2^23", name, (long long)n);
+    return Q4_OK;
+}
+
+q4_status check_result(int64_t rows, int64_t cols) {
+    if (rows > 0 && cols > 0 && rows >= (int64_t(1) << 38) / cols)
+        return bad(Q4_ERR_SHAPE, "a result of %lld x %lld has 2^38 elements or more", (long long)rows, (long long)cols);
     return Q4_OK;
 }
 
@@ -183,6 +190,7 @@ q4_status q4mx_linear(const q4mx_matrix* x, const q4mx_matrix* w, void* y, int32
     if (x->cols != w->cols)
         return bad(Q4_ERR_SHAPE, "x has %lld columns, w has %lld", (long long)x->cols, (long long)w->cols);
     Q4_TRY(check_dense("y", y, dtype, x->rows, w->rows, ldy));
+    Q4_TRY(check_result(x->rows, w->rows));
     if (x->rows == 0 || w->rows == 0) return ok();
     size_t need = 0;
     Q4_TRY(q4mx_linear_workspace_bytes(x, w, &need));
@@ -206,11 +214,17 @@ q4_status q4mx_linear_bf16(const uint16_t* x, int64_t ldx, int64_t tokens, const
     Q4_TRY(check_shape("x", Q4MX_FP8, tokens, w->cols));
     Q4_TRY(check_dense("x", x, Q4MX_BF16, tokens, w->cols, ldx));
     Q4_TRY(check_dense("y", y, dtype, tokens, w->rows, ldy));
+    Q4_TRY(check_result(tokens, w->rows));
     if (tokens == 0 || w->rows == 0) return ok();
+    Q4_TRY(check_width("ldx", tokens > 1 && w->cols > 0 ? ldx : 0));
     const Quantized q = quantized(tokens, w->cols);
     Q4_TRY(check_ws(ws, ws_bytes, bf16_workspace(tokens, w)));
     Q4_TRY(device());
     hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+    if (tokens <= Q4MX_FEW_TOKENS)
+        return launched(launch_linear_few(Dense{const_cast<uint16_t*>(x), ldx, Q4MX_BF16}, tokens, mat(w),
+                                          Dense{y, ldy, dtype}, st),
+                        "linear launch");
     uint8_t* p = static_cast<uint8_t*>(ws);
     const MxMat xq = quantized_at(p, q, tokens, w->cols);
     if (w->cols > 0) {
@@ -236,6 +250,7 @@ q4_status q4mx_dgrad(const uint16_t* dy, int64_t lddy, int64_t tokens, const q4m
     Q4_TRY(check_dense("dy", dy, Q4MX_BF16, tokens, w->rows, lddy));
     Q4_TRY(check_width("lddy", tokens > 0 && w->rows > 0 ? lddy : 0));
     Q4_TRY(check_dense("dx", dx, dtype, tokens, w->cols, lddx));
+    Q4_TRY(check_result(tokens, w->cols));
     if (tokens == 0 || w->cols == 0) return ok();
     size_t need = 0;
     Q4_TRY(q4mx_dgrad_workspace_bytes(dy, lddy, tokens, w, &need));
@@ -266,7 +281,7 @@ q4_status q4mx_wgrad(const uint16_t* dy, int64_t lddy, int64_t n, const q4mx_mat
     Q4_TRY(q4mx_wgrad_workspace_bytes(dy, lddy, n, x, flags, &need));
     const bool t = (flags & Q4MX_WGRAD_TRANSPOSED) != 0;
     Q4_TRY(check_dense("dw", dw, dtype, t ? x->cols : n, t ? n : x->cols, lddw));
-    if (n < 0) return bad(Q4_ERR_SHAPE, "n is negative");
+    Q4_TRY(check_result(n, x->cols));
     if (n == 0 || x->cols == 0) return ok();
     Q4_TRY(check_ws(ws, ws_bytes, need));
     Q4_TRY(device());

@@ -268,6 +268,154 @@ __global__ __launch_bounds__(64 * WN* WT, 2) void k_mx_linear(MxMat x, MxMat w, 
             put4(y, t0 + (wt * FT + j) * 16 + r, n0 + (wn * FN + i) * 16 + g * 4, acc[i][j]);
 }
 
+// ---- linear for few tokens ------------------------------------------------------------
+//
+// Up to 16 tokens (a decoding step) are one fragment, and the weights' bytes
+// are all that counts: a work-group takes 16 outputs, its NW wavefronts every
+// NW-th slice of 128 columns, straight from memory into registers, and their
+// sums meet in shared memory.  Four slices (two) are loaded before the first
+// is multiplied.  A BF16 x is quantized by the lane that needs it: lane (r, g)
+// holds columns 16 g .. +15 and 64 + 16 g .. +15 of token r, half of blocks
+// g / 2 and 2 + g / 2, the other half in lane g ^ 1.
+constexpr int kFromBf16 = 2;  // beside the formats, what x is
+
+struct Few {
+    MxMat mx;           // x as codes
+    const uint16_t* p;  // or BF16
+    int64_t ld, tokens, cols;
+    bool wide;  // BF16 rows are whole 4-byte words
+};
+
+struct FewX {
+    i32x8 codes;
+    int scale;
+};
+
+template <int XF> struct FewRaw {
+    i32x4 lo, hi;
+    int scale;
+};
+template <> struct FewRaw<kFromBf16> {
+    i32x4 v[4];  // columns 16 g + 0, 8 and 64 + 16 g + 0, 8
+};
+
+template <int XF> __device__ __forceinline__ FewRaw<XF> few_load(const Few& x, int s, int slices, int r, int g) {
+    FewRaw<XF> f;
+    const int n = r < x.tokens ? slices : 0;
+    if constexpr (XF == kFromBf16) {
+        const auto b = readable(x.p, ((x.tokens - 1) * x.ld + x.cols) * 2);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int64_t c = (int64_t)s * 128 + (k >> 1) * 64 + g * 16 + (k & 1) * 8;
+            const int left = c < x.cols ? (int)min((int64_t)8, x.cols - c) : 0;
+            const uint32_t off = (uint32_t)(r * x.ld + c) * 2;
+            const int here = s < n ? left : 0;  // columns to read
+            if (x.wide) {
+                f.v[k] = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(b, (int)inside(off, 0, here), 0, 0));
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t lo = __builtin_amdgcn_raw_buffer_load_b16(b, (int)inside(off + 4 * i, 2 * i, here), 0, 0);
+                    const uint32_t hi =
+                        __builtin_amdgcn_raw_buffer_load_b16(b, (int)inside(off + 4 * i + 2, 2 * i + 1, here), 0, 0);
+                    f.v[k][i] = (int)(lo | (hi << 16));
+                }
+            }
+            // what lies behind the last column belongs to something else
+            if ((int64_t)s * 128 + 128 > x.cols)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    f.v[k][i] &= (2 * i < left ? 0xFFFF : 0) | (2 * i + 1 < left ? (int)0xFFFF0000 : 0);
+        }
+    } else {
+        constexpr int kRow = XF == Q4MX_FP4 ? 64 : 128;
+        const int64_t pitch = x.mx.slices * kRow;
+        const auto b = readable(x.mx.codes, x.mx.rows * pitch);
+        const auto bs = readable(x.mx.scales, x.mx.slices * x.mx.rows * 4);
+        const uint32_t off = (uint32_t)(r * pitch) + (uint32_t)(s * kRow) + g * 16;
+        f.lo = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(b, (int)inside(off, s, n), 0, 0));
+        f.hi = i32x4{0, 0, 0, 0};
+        if (XF == Q4MX_FP8)
+            f.hi = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(b, (int)inside(off + 64, s, n), 0, 0));
+        f.scale = __builtin_amdgcn_raw_buffer_load_b8(bs, (int)inside(((uint32_t)s * (uint32_t)x.mx.rows + r) * 4 + g, s, n), 0, 0);
+    }
+    return f;
+}
+
+template <int XF> __device__ __forceinline__ FewX few_operand(const FewRaw<XF>& f, int lane) {
+    FewX x;
+    if constexpr (XF == kFromBf16) {
+        uint32_t e[2];
+        i32x4 half[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float v[16];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t w = (uint32_t)f.v[2 * h + i / 4][i % 4];
+                v[2 * i] = bf16_value(w & 0xFFFFu);
+                v[2 * i + 1] = __uint_as_float(w & 0xFFFF0000u);
+            }
+            uint32_t top = 0;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+            top = max(top, (uint32_t)__shfl_xor((int)top, 16));
+            e[h] = scale_byte<Q4MX_FP8>(top);
+            const float s = scale_of(e[h]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) half[h][i] = e[h] == 255 ? 0 : (int)enc8x4(v + 4 * i, s);
+        }
+        x.codes = __builtin_shufflevector(half[0], half[1], 0, 1, 2, 3, 4, 5, 6, 7);
+        // the scale of block g: blocks 0, 1 are in lanes 0, 2's first halves, 2, 3 in the second
+        const int r = lane & 15, g = lane >> 4;
+        const int first = __shfl((int)e[0], r + 32), second = __shfl((int)e[1], r);
+        x.scale = g == 0 ? (int)e[0] : g == 1 ? first : g == 2 ? second : (int)e[1];
+    } else {
+        x.codes = __builtin_shufflevector(f.lo, f.hi, 0, 1, 2, 3, 4, 5, 6, 7);
+        x.scale = f.scale;
+    }
+    return x;
+}
+
+template <int XF, int NW> __global__ __launch_bounds__(64 * NW) void k_mx_linear_few(Few x, MxMat w, Out y) {
+    __shared__ f32x4 sums[NW][64];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int r = lane & 15, g = lane >> 4;
+    const int64_t n0 = (int64_t)blockIdx.x * 16, wp = w.slices * 64;
+    const int slices = (int)w.slices;
+    const auto b = readable(w.codes + n0 * wp, (w.rows - n0) * wp);
+    const auto bs = readable(w.scales, w.slices * w.rows * 4);
+    const uint32_t off = (uint32_t)(r * wp) + g * 16, soff = (uint32_t)(n0 + r) * 4 + g;
+    constexpr int kAhead = NW < 16 ? 4 : 2;  // 1024 threads have 128 registers each
+    f32x4 acc = {0, 0, 0, 0};
+    for (int s0 = wave; s0 < slices; s0 += NW * kAhead) {
+        i32x4 a[kAhead];
+        int sa[kAhead];
+        FewRaw<XF> f[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int s = s0 + k * NW;
+            a[k] = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(b, (int)inside(off + (uint32_t)s * 64, s, slices), 0, 0));
+            sa[k] = __builtin_amdgcn_raw_buffer_load_b8(bs, (int)inside(soff + (uint32_t)s * (uint32_t)w.rows * 4, s, slices), 0, 0);
+            f[k] = few_load<XF>(x, s, slices, r, g);
+        }
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const FewX o = few_operand<XF>(f[k], lane);
+            const i32x4 none = {0, 0, 0, 0};
+            acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                __builtin_shufflevector(a[k], none, 0, 1, 2, 3, 4, 5, 6, 7), o.codes, acc, 4, XF == Q4MX_FP4 ? 4 : 0, 0,
+                sa[k], 0, o.scale);
+        }
+    }
+    sums[wave][lane] = acc;
+    __syncthreads();
+    if (wave != 0) return;
+#pragma unroll
+    for (int k = 1; k < NW; ++k) acc += sums[k][lane];
+    put4(y, r, n0 + g * 4, acc);
+}
+
 // ---- dgrad, wgrad: BF16 by codes ------------------------------------------------------
 //
 // Result (d, c): d runs over the dense operand's axis (a token for dgrad, an
@@ -616,6 +764,19 @@ hipError_t aligned_gradient(const Dense& dy, int64_t rows, int64_t cols, void* c
     return hipGetLastError();
 }
 
+// Wavefronts of a work-group: as many as give each two slices, up to 16, but
+// no more than fill the chip (8 a compute unit).
+template <int XF> hipError_t few(const Few& x, const MxMat& w, const Out& y, hipStream_t st) {
+    const int64_t groups = tiles(w.rows, 16);
+    int waves = 4;
+    while (waves < 16 && w.slices >= 4 * waves && groups * waves < 2048) waves *= 2;
+    const dim3 g((unsigned)groups);
+    if (waves == 4) k_mx_linear_few<XF, 4><<<g, dim3(256), 0, st>>>(x, w, y);
+    else if (waves == 8) k_mx_linear_few<XF, 8><<<g, dim3(512), 0, st>>>(x, w, y);
+    else k_mx_linear_few<XF, 16><<<g, dim3(1024), 0, st>>>(x, w, y);
+    return hipGetLastError();
+}
+
 }  // namespace
 
 bool dense_needs_copy(const Dense& d, int64_t rows, int64_t cols) {
@@ -623,11 +784,23 @@ bool dense_needs_copy(const Dense& d, int64_t rows, int64_t cols) {
 }
 size_t dense_copy_bytes(int64_t rows, int64_t cols) { return (size_t)(rows * tiles(cols, 8) * 16); }
 
-size_t linear_workspace(const MxMat& x, const MxMat& w) { return linear_plan(x, w).bytes; }
+size_t linear_workspace(const MxMat& x, const MxMat& w) {
+    return x.rows <= Q4MX_FEW_TOKENS ? 0 : linear_plan(x, w).bytes;
+}
 size_t grad_workspace(const MxMat& m, int64_t width) { return grad_plan(m, width).bytes; }
+
+hipError_t launch_linear_few(const Dense& x, int64_t tokens, const MxMat& w, const Dense& y, hipStream_t st) {
+    const bool wide = (reinterpret_cast<uintptr_t>(x.p) & 3) == 0 && w.cols % 2 == 0 && (tokens == 1 || x.ld % 2 == 0);
+    return few<kFromBf16>(Few{MxMat{}, static_cast<const uint16_t*>(x.p), x.ld, tokens, w.cols, wide}, w,
+                          result(y, tokens, w.rows, false), st);
+}
 
 hipError_t launch_linear(const MxMat& x, const MxMat& w, const Dense& y, void* ws, hipStream_t st) {
     const Out out = result(y, x.rows, w.rows, false);
+    if (x.rows <= Q4MX_FEW_TOKENS) {
+        const Few f{x, nullptr, 0, x.rows, x.cols, false};
+        return x.fmt == Q4MX_FP4 ? few<Q4MX_FP4>(f, w, out, st) : few<Q4MX_FP8>(f, w, out, st);
+    }
     return x.fmt == Q4MX_FP4 ? linear<Q4MX_FP4>(x, w, out, ws, st) : linear<Q4MX_FP8>(x, w, out, ws, st);
 }
 

@@ -20,8 +20,6 @@ calls are the layer's backward pass.
 """
 from __future__ import annotations
 
-import contextlib
-
 import torch
 
 from . import api
@@ -38,35 +36,62 @@ class MXMatrix:
             a multiple of 128;
     scales: uint8 [P / 128, rows, 4].
     """
-    __slots__ = ("rows", "cols", "format", "codes", "scales", "desc")
+    __slots__ = ("rows", "cols", "format", "device", "desc", "_codes", "_scales", "_buf")
 
     def __init__(self, rows: int, cols: int, format: str, codes=None, scales=None, device="cuda"):
         if format not in FORMATS:
             raise ValueError(f"unknown format {format!r}; expected one of {sorted(FORMATS)}")
-        api.q4mx_matrix_bytes(FORMATS[format], rows, cols)   # refuses sizes out of range
-        slices = (cols + 127) // 128
-        shapes = ((rows, slices * (64 if format == "fp4" else 128)), (slices, rows, 4))
-        if (codes is None) != (scales is None):
+        code = FORMATS[format]
+        ncodes, nscales = api.q4mx_matrix_bytes(code, rows, cols)   # refuses sizes out of range
+        self.rows, self.cols, self.format = rows, cols, format
+        self._codes, self._scales, self._buf = codes, scales, None
+        if codes is None and scales is None:
+            # one buffer for both; the views are made when they are asked for
+            offset = (ncodes + 255) // 256 * 256
+            self._buf = buf = torch.empty(offset + nscales, dtype=torch.uint8, device=device)
+            self.device = buf.device
+            if not buf.is_cuda:
+                raise ValueError("device must be a GPU")
+            at = buf.data_ptr()
+            pointers = (at, at + offset)
+        elif codes is None or scales is None:
             raise ValueError("codes and scales come together")
-        if codes is None:
-            codes, scales = (torch.empty(s, dtype=torch.uint8, device=device) for s in shapes)
-        for name, t, shape in (("codes", codes, shapes[0]), ("scales", scales, shapes[1])):
-            if t.dtype != torch.uint8 or tuple(t.shape) != shape or not t.is_contiguous():
-                raise ValueError(f"{name} must be a contiguous uint8 tensor of shape {shape}")
-            if not t.is_cuda:
-                raise ValueError(f"{name} must be on a GPU")
-        if codes.device != scales.device:
-            raise ValueError("codes and scales must be on one device")
-        self.rows, self.cols, self.format, self.codes, self.scales = rows, cols, format, codes, scales
-        self.desc = api.Q4MXMatrix(FORMATS[format], 0, rows, cols, codes.data_ptr(), scales.data_ptr())
+        else:
+            for name, t, shape in (("codes", codes, self._code_shape()), ("scales", scales, self._scale_shape())):
+                if t.dtype != torch.uint8 or tuple(t.shape) != shape or not t.is_contiguous():
+                    raise ValueError(f"{name} must be a contiguous uint8 tensor of shape {shape}")
+                if not t.is_cuda:
+                    raise ValueError(f"{name} must be on a GPU")
+            if codes.device != scales.device:
+                raise ValueError("codes and scales must be on one device")
+            self.device = codes.device
+            pointers = (codes.data_ptr(), scales.data_ptr())
+        self.desc = api.Q4MXMatrix(code, 0, rows, cols, *pointers)
+
+    def _code_shape(self) -> tuple:
+        return (self.rows, (self.cols + 127) // 128 * (64 if self.format == "fp4" else 128))
+
+    def _scale_shape(self) -> tuple:
+        return ((self.cols + 127) // 128, self.rows, 4)
+
+    @property
+    def codes(self):
+        if self._codes is None:
+            shape = self._code_shape()
+            self._codes = self._buf[:shape[0] * shape[1]].view(shape)
+        return self._codes
+
+    @property
+    def scales(self):
+        if self._scales is None:
+            shape = self._scale_shape()
+            n = shape[0] * shape[1] * 4
+            self._scales = self._buf[self._buf.numel() - n:].view(shape)
+        return self._scales
 
     @property
     def shape(self) -> tuple:
         return (self.rows, self.cols)
-
-    @property
-    def device(self):
-        return self.codes.device
 
     def __repr__(self) -> str:
         return f"MXMatrix({self.rows} x {self.cols}, {self.format!r}, device='{self.device}')"
@@ -114,22 +139,39 @@ def _mx_result(out, rows, cols, fmt, device):
     return out
 
 
-def _same_device(*operands):
-    device = operands[0].device
-    for t in operands:
+def _same_device(first, *others):
+    device = first.device
+    for t in others:
         if t is not None and t.device != device:
             raise ValueError(f"the operands are on different devices ({device} and {t.device})")
     return device
 
 
-@contextlib.contextmanager
+class _Here:
+    """The current device and stream: nothing to enter."""
+
+    def __enter__(self):
+        return None
+
+    def __exit__(self, *exc):
+        return None
+
+
+_HERE = _Here()
+
+
 def _on(device, stream):
-    with torch.cuda.device(device):
-        if stream is None:
-            yield
-        else:
-            with torch.cuda.stream(stream):
-                yield
+    """The device and stream of a call as a context."""
+    if stream is not None:
+        return torch.cuda.stream(stream)   # makes the stream's device current
+    if torch._C._cuda_getDevice() == device.index:
+        return _HERE
+    return torch.cuda.device(device)
+
+
+def _raw(device) -> int:
+    """The current stream of the operands' device, as the C calls take it."""
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _workspace(nbytes, device):
@@ -147,7 +189,7 @@ def quantize(src, format: str, transpose: bool = False, out: MXMatrix | None = N
     device = _same_device(src, out)
     with _on(device, stream):
         out = _mx_result(out, rows, cols, format, device)
-        api.q4mx_quantize(src, _DTYPES[src.dtype], ld, transpose, out.desc)
+        api.q4mx_quantize(src, _DTYPES[src.dtype], ld, transpose, out.desc, _raw(device))
     return out
 
 
@@ -156,7 +198,7 @@ def dequantize(a: MXMatrix, dtype=torch.bfloat16, out=None, stream=None) -> torc
     device = _same_device(_matrix("a", a), out)
     with _on(device, stream):
         out, code, ld = _result(out, a.shape, dtype, device)
-        api.q4mx_dequantize(a.desc, out, code, ld)
+        api.q4mx_dequantize(a.desc, out, code, ld, _raw(device))
     return out
 
 
@@ -167,8 +209,10 @@ def linear(x, w: MXMatrix, out=None, dtype=torch.bfloat16, stream=None) -> torch
     if isinstance(x, MXMatrix):
         with _on(device, stream):
             out, code, ld = _result(out, (x.rows, w.rows), dtype, device)
-            ws = _workspace(api.q4mx_linear_workspace_bytes(x.desc, w.desc), device)
-            api.q4mx_linear(x.desc, w.desc, out, code, ld, ws)
+            ws = None
+            if x.rows > api.MX_FEW_TOKENS:
+                ws = _workspace(api.q4mx_linear_workspace_bytes(x.desc, w.desc), device)
+            api.q4mx_linear(x.desc, w.desc, out, code, ld, ws, stream=_raw(device))
         return out
     ldx = _dense("x", x)
     if x.shape[1] != w.cols:
@@ -176,8 +220,10 @@ def linear(x, w: MXMatrix, out=None, dtype=torch.bfloat16, stream=None) -> torch
     tokens = x.shape[0]
     with _on(device, stream):
         out, code, ld = _result(out, (tokens, w.rows), dtype, device)
-        ws = _workspace(api.q4mx_linear_bf16_workspace_bytes(tokens, w.desc), device)
-        api.q4mx_linear_bf16(x, ldx, tokens, w.desc, out, code, ld, ws)
+        ws = None
+        if tokens > api.MX_FEW_TOKENS:
+            ws = _workspace(api.q4mx_linear_bf16_workspace_bytes(tokens, w.desc), device)
+        api.q4mx_linear_bf16(x, ldx, tokens, w.desc, out, code, ld, ws, stream=_raw(device))
     return out
 
 
@@ -191,7 +237,7 @@ def linear_dgrad(dy, w: MXMatrix, out=None, dtype=torch.bfloat16, stream=None) -
     with _on(device, stream):
         out, code, ld = _result(out, (tokens, w.cols), dtype, device)
         ws = _workspace(api.q4mx_dgrad_workspace_bytes(dy, lddy, tokens, w.desc), device)
-        api.q4mx_dgrad(dy, lddy, tokens, w.desc, out, code, ld, ws)
+        api.q4mx_dgrad(dy, lddy, tokens, w.desc, out, code, ld, ws, stream=_raw(device))
     return out
 
 
@@ -210,7 +256,7 @@ def linear_wgrad(dy, x: MXMatrix, out=None, transposed: bool = False, accumulate
     with _on(device, stream):
         out, code, ld = _result(out, (x.cols, n) if transposed else (n, x.cols), dtype, device)
         ws = _workspace(api.q4mx_wgrad_workspace_bytes(dy, lddy, n, x.desc, flags), device)
-        api.q4mx_wgrad(dy, lddy, n, x.desc, out, code, ld, flags, ws)
+        api.q4mx_wgrad(dy, lddy, n, x.desc, out, code, ld, flags, ws, stream=_raw(device))
     return out
 
 
@@ -250,7 +296,7 @@ def act_forward(kind: str, x, up=None, out_format: str | None = None, stream=Non
         if up is not None:
             kept_up = MXMatrix(rows, cols, "fp8", device=device)
         api.q4mx_act_forward(act, x, ldx, up, ldup, rows, cols, y, ldy, y_mx.desc if y_mx is not None else None,
-                             kept_x.desc, kept_up.desc if kept_up is not None else None)
+                             kept_x.desc, kept_up.desc if kept_up is not None else None, _raw(device))
     return (y if y_mx is None else y_mx), (kept_x, kept_up)
 
 
@@ -270,5 +316,5 @@ def act_backward(kind: str, kept, dy, stream=None) -> tuple:
         dx = torch.empty(dy.shape, dtype=torch.bfloat16, device=device)
         dup = torch.empty_like(dx) if kept_up is not None else None
         api.q4mx_act_backward(act, kept_x.desc, kept_up.desc if kept_up is not None else None, dy, lddy, dx, ld, dup,
-                              ld)
+                              ld, _raw(device))
     return (dx,) if dup is None else (dx, dup)

@@ -426,8 +426,8 @@ q4_status q4mx_linear_workspace_bytes(const q4mx_matrix* x, const q4mx_matrix* w
 
 /* The same from a dense BF16 x (tokens x w->cols), which is quantized to
  * Q4MX_FP8 on the way: the same result as q4mx_quantize, then q4mx_linear.
- * Up to Q4MX_FEW_TOKENS tokens (a decoding step) take one launch and no
- * workspace. */
+ * Either product of up to Q4MX_FEW_TOKENS tokens (a decoding step) takes one
+ * launch and no workspace. */
 #define Q4MX_FEW_TOKENS 16
 q4_status q4mx_linear_bf16(const uint16_t* x, int64_t ldx, int64_t tokens, const q4mx_matrix* w, void* y,
                            int32_t dtype, int64_t ldy, void* ws, size_t ws_bytes, void* stream);
