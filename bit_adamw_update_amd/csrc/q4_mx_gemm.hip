@@ -9,6 +9,8 @@
 // tile on their way into shared memory.  All sums are FP32 in the matrix
 // cores' accumulators.
 
+#include <algorithm>
+
 #include "q4_mx.h"
 #include "q4_mx_dev.h"
 
@@ -51,17 +53,19 @@ __device__ __forceinline__ void tile_at(const Cut& c, uint32_t id, uint32_t& i0,
     i1 = in / h;
 }
 
-// Work-group -> unit.  Consecutive work-groups go to the 8 XCDs in turn, each
-// with an L2 of its own; the renumbering gives each XCD contiguous runs of
-// tiles.  Units of the split tiles come run by run, so that those that run
-// together are different tiles of the same steps.
-__device__ __forceinline__ Unit unit_of(const Cut& c, int steps, int frags) {
-    const uint32_t bid = blockIdx.x, n = bid < c.full ? c.full : c.rest * c.split;
-    const uint32_t local = bid < c.full ? bid : bid - c.full, q = n / 8, r = n % 8, x = local % 8;
+// A work-group forms units blockIdx.x, + gridDim.x, ...  Consecutive
+// work-groups go to the 8 XCDs in turn, each with an L2 of its own; the
+// renumbering gives each XCD contiguous runs of tiles.  Units of the split
+// tiles come run by run, so that those that run together are different tiles
+// of the same steps.
+__device__ __forceinline__ uint32_t units_of(const Cut& c) { return c.full + c.rest * c.split; }
+__device__ __forceinline__ Unit unit_of(const Cut& c, uint32_t index, int steps, int frags) {
+    const uint32_t n = index < c.full ? c.full : c.rest * c.split;
+    const uint32_t local = index < c.full ? index : index - c.full, q = n / 8, r = n % 8, x = local % 8;
     const uint32_t id = x * q + min(x, r) + local / 8;
     Unit u;
-    if (bid < c.full || c.split == 1) {
-        tile_at(c, bid < c.full ? id : c.full + id, u.i0, u.i1);
+    if (index < c.full || c.split == 1) {
+        tile_at(c, index < c.full ? id : c.full + id, u.i0, u.i1);
         u.first = 0, u.last = steps, u.part = nullptr;
         return u;
     }
@@ -84,6 +88,23 @@ __device__ __forceinline__ i32x4 buffer(const void* p, int64_t bytes) {
     r[3] = 0x00020000;
     return r;
 }
+// The same, moved along as the steps of a product go.
+struct Window {
+    uint64_t at;
+    uint32_t bytes;
+    __device__ __forceinline__ void open(const void* p, int64_t n) {
+        const i32x4 b = buffer(p, n);
+        at = (uint64_t)(uint32_t)b[0] | ((uint64_t)(uint32_t)b[1] << 32);
+        bytes = (uint32_t)b[2];
+    }
+    __device__ __forceinline__ void move(uint64_t by, uint32_t fewer) {
+        at += by;
+        bytes -= fewer;
+    }
+    __device__ __forceinline__ i32x4 get() const {
+        return i32x4{(int)(uint32_t)at, (int)(uint32_t)(at >> 32), (int)bytes, 0x00020000};
+    }
+};
 // The same for the compiler's own loads.
 __device__ __forceinline__ auto readable(const void* p, int64_t bytes) {
     const i32x4 b = buffer(p, bytes);
@@ -108,6 +129,12 @@ template <int N> __device__ __forceinline__ void wait_copies_and_barrier() {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
+__device__ __forceinline__ void phase_end() { asm volatile("s_barrier" ::: "memory"); }
+
+// Holds a value in registers at this point: what makes it stays before, what
+// uses it behind (barriers alone do not keep register work in its phase).
+template <class T> __device__ __forceinline__ void pin(T& v) { asm volatile("" : "+v"(v)); }
+
 __device__ __forceinline__ uint32_t lds_base(const void* p) {
     return (uint32_t) reinterpret_cast<uintptr_t>((Q4_LDS const char*)p);
 }
@@ -118,7 +145,7 @@ __device__ __forceinline__ uint32_t lds_base(const void* p) {
 struct Out {
     void* p;
     int64_t ld, rows, cols;
-    bool bf16, add, vec;  // vec: 4 consecutive columns from a multiple of 4 are one access
+    bool bf16, add, vec, vec8;  // vec, vec8: 4 or 8 columns from such a multiple are one or two whole accesses
 };
 
 __device__ __forceinline__ void put4(const Out& o, int64_t r, int64_t c, f32x4 v) {
@@ -156,7 +183,8 @@ __device__ __forceinline__ void put4(const Out& o, int64_t r, int64_t c, f32x4 v
 Out result(const Dense& d, int64_t rows, int64_t cols, bool add) {
     const int64_t unit = d.dtype == Q4MX_BF16 ? 8 : 16;
     const bool vec = reinterpret_cast<uintptr_t>(d.p) % unit == 0 && d.ld % 4 == 0;
-    return Out{d.p, d.ld, rows, cols, d.dtype == Q4MX_BF16, add, vec};
+    const bool vec8 = reinterpret_cast<uintptr_t>(d.p) % 16 == 0 && d.ld % 8 == 0;
+    return Out{d.p, d.ld, rows, cols, d.dtype == Q4MX_BF16, add, vec, vec8};
 }
 
 // ---- linear: codes by codes -------------------------------------------------------
@@ -167,6 +195,10 @@ Out result(const Dense& d, int64_t rows, int64_t cols, bool add) {
 // in a ring: while one is multiplied, the next two are on their way.  A row of
 // a step is 64 bytes (E2M1) or 128 (E4M3); its 16-byte pieces are permuted by
 // the row's low bits, so that the 16 rows of a fragment read different banks.
+//
+// Rows of w are dealt to fragments in fours: rows 8 q .. 8 q + 3 of 32 to an
+// even fragment's rows 4 q .., 8 q + 4 .. 8 q + 7 to the next one's, so that a
+// lane's 2 x 4 results are 8 neighbouring outputs, one 16-byte store.
 //
 // The instruction's lane (r, g), r = lane % 16, g = lane / 16, holds of row r
 // the E2M1 codes of columns 32 g .. 32 g + 31, or the E4M3 codes of columns 16
@@ -181,14 +213,15 @@ __global__ __launch_bounds__(64 * WN* WT, 2) void k_mx_linear(MxMat x, MxMat w, 
     __shared__ __attribute__((aligned(1024))) char lds[3 * kStage];
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const Unit u = unit_of(cut, (int)w.slices, FN * FT);
-    const int64_t n0 = (int64_t)u.i0 * BN, t0 = (int64_t)u.i1 * BT;
     const int64_t wp = w.slices * 64, xp = x.slices * XB;
+    const int steps = (int)w.slices;
+    const uint32_t units = units_of(cut);
 
     uint32_t woff[CW], xoff[CX];
 #pragma unroll
     for (int j = 0; j < CW; ++j)
-        woff[j] = (uint32_t)((j * NW + wave) * 16 + lane / 4) * (uint32_t)wp + ((lane & 3) ^ ((lane >> 3) & 3)) * 16;
+        woff[j] = (uint32_t)((j * NW + wave) * 16 + lane / 4) * (uint32_t)wp +
+                  ((lane & 3) ^ (((lane >> 3) & 1) | ((lane >> 5) << 1))) * 16;
 #pragma unroll
     for (int j = 0; j < CX; ++j)
         xoff[j] = XF == Q4MX_FP4
@@ -196,76 +229,157 @@ __global__ __launch_bounds__(64 * WN* WT, 2) void k_mx_linear(MxMat x, MxMat w, 
                       : (uint32_t)((j * NW + wave) * 8 + lane / 8) * (uint32_t)xp + ((lane & 7) ^ (lane >> 3)) * 16;
     // wavefronts 0 .. BN/64-1 copy the scales of w, the others those of x
     const bool xs = wave >= BN / 64;
-    const int64_t srows = xs ? x.rows : w.rows, s0 = xs ? t0 : n0;
-    const uint8_t* const sp = (xs ? x.scales : w.scales) + s0 * 4;
-    const int64_t sbytes = (srows - s0) * 4;
+    const int64_t srows = xs ? x.rows : w.rows;
+    const uint8_t* const scales = xs ? x.scales : w.scales;
     const uint32_t soff = (wave - (xs ? BN / 64 : 0)) * 256 + lane * 4;
     const uint32_t base = lds_base(lds);
 
-    auto issue = [&](int s) {
-        const uint32_t at = base + (uint32_t)(s % 3) * kStage;
-        const i32x4 bw = buffer(w.codes + n0 * wp + (int64_t)s * 64, (w.rows - n0) * wp - (int64_t)s * 64);
-        const i32x4 bx = buffer(x.codes + t0 * xp + (int64_t)s * XB, (x.rows - t0) * xp - (int64_t)s * XB);
-        const i32x4 bs = buffer(sp + (int64_t)s * srows * 4, sbytes);
+    // The steps of this work-group's units form one stream; copies run two
+    // steps ahead of the products, into the next unit's while one ends.
+    uint32_t next_unit = blockIdx.x, next_at = base;
+    int next_left = 0;
+    Window ww, wx, ws;
+    auto open = [&] {
+        if (next_unit < units) {
+            const Unit u = unit_of(cut, next_unit, steps, FN * FT);
+            const int64_t n0 = (int64_t)u.i0 * BN, t0 = (int64_t)u.i1 * BT, s0 = xs ? t0 : n0, s = u.first;
+            ww.open(w.codes + n0 * wp + s * 64, (w.rows - n0) * wp - s * 64);
+            wx.open(x.codes + t0 * xp + s * XB, (x.rows - t0) * xp - s * XB);
+            ws.open(scales + (s * srows + s0) * 4, (srows - s0) * 4);
+            next_left = u.last - u.first;
+        }
+    };
+    auto issue = [&] {
+        const i32x4 bw = ww.get(), bx = wx.get(), bs = ws.get();
 #pragma unroll
-        for (int j = 0; j < CW; ++j) copy16(bw, woff[j], at + (j * NW + wave) * 1024);
+        for (int j = 0; j < CW; ++j) copy16(bw, woff[j], next_at + (j * NW + wave) * 1024);
 #pragma unroll
-        for (int j = 0; j < CX; ++j) copy16(bx, xoff[j], at + kW + (j * NW + wave) * 1024);
-        copy4(bs, soff, at + kW + kX + wave * 256);
+        for (int j = 0; j < CX; ++j) copy16(bx, xoff[j], next_at + kW + (j * NW + wave) * 1024);
+        copy4(bs, soff, next_at + kW + kX + wave * 256);
+        next_at = next_at == base + 2 * kStage ? base : next_at + kStage;
+        if (--next_left == 0) {
+            next_unit += gridDim.x;
+            open();
+        } else {
+            ww.move(64, 64);
+            wx.move(XB, XB);
+            ws.move((uint64_t)srows * 4, 0);
+        }
     };
 
     const int r = lane & 15, g = lane >> 4, wn = wave % WN, wt = wave / WN;
-    const int wrow = wn * FN * 16 + r, xrow = wt * FT * 16 + r;
-    const int wat = wrow * 64 + ((g ^ ((r >> 1) & 3)) * 16);
+    const int wrow = wn * FN * 16 + (r >> 2) * 8 + (r & 3), xrow = wt * FT * 16 + r;
+    const int wat = wrow * 64 + ((g ^ (((r >> 1) & 1) | (((r >> 2) & 1) << 1))) * 16);
     const int xat = kW + xrow * XB + (XF == Q4MX_FP4 ? (g ^ ((r >> 1) & 3)) * 16 : (g ^ (r & 7)) * 16);
     const int xat2 = kW + xrow * XB + ((4 + g) ^ (r & 7)) * 16;
     const int wsat = kW + kX + wrow * 4 + g, xsat = kW + kX + BN * 4 + xrow * 4 + g;
 
     f32x4 acc[FN][FT] = {};
-    if (u.first < u.last) issue(u.first);
-    if (u.first + 1 < u.last) issue(u.first + 1);
-    for (int s = u.first; s < u.last; ++s) {
-        // this step's copies are done (the next step's may be under way), and
-        // every wavefront is done with the buffer that step s + 2 takes
-        if (s + 1 < u.last) wait_copies_and_barrier<kCopies>();
-        else wait_copies_and_barrier<0>();
-        if (s + 2 < u.last) issue(s + 2);
-        const char* const st = lds + (s % 3) * kStage;
-        i32x8 b[FT], a[FN];
-        int sa[FN], sb[FT];
+    i32x4 blo[FT], bhi[FT], a[FN];
+    int sa[FN], sb[FT];
+    auto read = [&](int slot) {
+        const char* const st = lds + slot * kStage;
 #pragma unroll
         for (int j = 0; j < FT; ++j) {
-            const i32x4 lo = *reinterpret_cast<const i32x4*>(st + xat + j * 16 * XB);
-            i32x4 hi = {0, 0, 0, 0};
-            if (XF != Q4MX_FP4) hi = *reinterpret_cast<const i32x4*>(st + xat2 + j * 16 * XB);
-            b[j] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+            blo[j] = *reinterpret_cast<const i32x4*>(st + xat + j * 16 * XB);
+            if (XF != Q4MX_FP4) bhi[j] = *reinterpret_cast<const i32x4*>(st + xat2 + j * 16 * XB);
             sb[j] = *reinterpret_cast<const uint8_t*>(st + xsat + j * 64);
         }
 #pragma unroll
         for (int i = 0; i < FN; ++i) {
-            const i32x4 lo = *reinterpret_cast<const i32x4*>(st + wat + i * 1024), none = {0, 0, 0, 0};
-            a[i] = __builtin_shufflevector(lo, none, 0, 1, 2, 3, 4, 5, 6, 7);
-            sa[i] = *reinterpret_cast<const uint8_t*>(st + wsat + i * 64);
+            a[i] = *reinterpret_cast<const i32x4*>(st + wat + ((i >> 1) * 32 + (i & 1) * 4) * 64);
+            sa[i] = *reinterpret_cast<const uint8_t*>(st + wsat + ((i >> 1) * 32 + (i & 1) * 4) * 4);
         }
+#pragma unroll
+        for (int j = 0; j < FT; ++j) pin(blo[j]), pin(sb[j]);
+        if (XF != Q4MX_FP4)
+#pragma unroll
+            for (int j = 0; j < FT; ++j) pin(bhi[j]);
+#pragma unroll
+        for (int i = 0; i < FN; ++i) pin(a[i]), pin(sa[i]);
+    };
+    auto multiply = [&] {
+        const i32x4 none = {0, 0, 0, 0};
 #pragma unroll
         for (int i = 0; i < FN; ++i)
 #pragma unroll
             for (int j = 0; j < FT; ++j)
-                acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a[i], b[j], acc[i][j], 4,
-                                                                             XF == Q4MX_FP4 ? 4 : 0, 0, sa[i], 0, sb[j]);
-    }
-    if (u.part) {
+                acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                    __builtin_shufflevector(a[i], none, 0, 1, 2, 3, 4, 5, 6, 7),
+                    __builtin_shufflevector(blo[j], XF == Q4MX_FP4 ? none : bhi[j], 0, 1, 2, 3, 4, 5, 6, 7), acc[i][j], 4,
+                    XF == Q4MX_FP4 ? 4 : 0, 0, sa[i], 0, sb[j]);
 #pragma unroll
         for (int i = 0; i < FN; ++i)
 #pragma unroll
-            for (int j = 0; j < FT; ++j) u.part[(i * FT + j) * blockDim.x + threadIdx.x] = acc[i][j];
-        return;
-    }
-#pragma unroll
-    for (int j = 0; j < FT; ++j)
+            for (int j = 0; j < FT; ++j) pin(acc[i][j]);
+    };
+
+    // The second half of the wavefronts runs one phase behind the first, so
+    // that on every SIMD one reads fragments while the other multiplies (4
+    // wavefronts have a SIMD each: there the other work-group of the compute
+    // unit does that).  At the start of a step's reads every wavefront is done
+    // reading the step before, whose buffer the copies of the step after next
+    // take; at their end this one's copies of the next step have arrived.
+    constexpr bool kPhases = NW == 8;
+    const bool second = kPhases && wave >= NW / 2;
+    open();
+    issue();
+    if (next_unit < units) issue();
+    wait_copies_and_barrier<0>();
+    if (second) phase_end();
+    int slot = 0;
+    bool stored = false;  // the last thing issued is kStores stores
+    constexpr int kStores = FN * FT / 2;
+    for (uint32_t index = blockIdx.x; index < units; index += gridDim.x) {
+        const Unit u = unit_of(cut, index, steps, FN * FT);
 #pragma unroll
         for (int i = 0; i < FN; ++i)
-            put4(y, t0 + (wt * FT + j) * 16 + r, n0 + (wn * FN + i) * 16 + g * 4, acc[i][j]);
+#pragma unroll
+            for (int j = 0; j < FT; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+        for (int s = u.first; s < u.last; ++s) {
+            const bool more = next_unit < units;
+            if (more) issue();
+            read(slot);
+            if (!more) wait_copies_and_barrier<0>();
+            else if (stored) wait_copies_and_barrier<kCopies + kStores>();
+            else wait_copies_and_barrier<kCopies>();
+            stored = false;
+            __builtin_amdgcn_sched_barrier(0);
+            if (kPhases) __builtin_amdgcn_s_setprio(1);
+            multiply();
+            if (kPhases) __builtin_amdgcn_s_setprio(0);
+            __builtin_amdgcn_sched_barrier(0);
+            if (kPhases && s + 1 < u.last) phase_end();
+            slot = slot == 2 ? 0 : slot + 1;
+        }
+        const int64_t n0 = (int64_t)u.i0 * BN, t0 = (int64_t)u.i1 * BT;
+        if (u.part) {
+#pragma unroll
+            for (int i = 0; i < FN; ++i)
+#pragma unroll
+                for (int j = 0; j < FT; ++j) u.part[(i * FT + j) * blockDim.x + threadIdx.x] = acc[i][j];
+        } else if (y.bf16 && y.vec8 && n0 + BN <= y.cols && t0 + BT <= y.rows) {
+            // whole tile: exactly kStores stores
+            uint16_t* const p = static_cast<uint16_t*>(y.p) + (t0 + xrow) * y.ld + n0 + wn * FN * 16 + g * 8;
+#pragma unroll
+            for (int j = 0; j < FT; ++j)
+#pragma unroll
+                for (int i = 0; i < FN; i += 2)
+                    *reinterpret_cast<uint4*>(p + j * 16 * y.ld + i * 16) =
+                        make_uint4(bf16_pair(acc[i][j][0], acc[i][j][1]), bf16_pair(acc[i][j][2], acc[i][j][3]),
+                                   bf16_pair(acc[i + 1][j][0], acc[i + 1][j][1]),
+                                   bf16_pair(acc[i + 1][j][2], acc[i + 1][j][3]));
+            stored = true;
+        } else {
+#pragma unroll
+            for (int j = 0; j < FT; ++j)
+#pragma unroll
+                for (int i = 0; i < FN; ++i)
+                    put4(y, t0 + (wt * FT + j) * 16 + r, n0 + wn * FN * 16 + (i >> 1) * 32 + (i & 1) * 4 + g * 8, acc[i][j]);
+        }
+        if (kPhases) phase_end();
+    }
+    if (kPhases && !second) phase_end();
 }
 
 // ---- linear for few tokens ------------------------------------------------------------
@@ -273,140 +387,89 @@ __global__ __launch_bounds__(64 * WN* WT, 2) void k_mx_linear(MxMat x, MxMat w, 
 // Up to 16 tokens (a decoding step) are one fragment, and the weights' bytes
 // are all that counts: a work-group takes 16 outputs, its NW wavefronts every
 // NW-th slice of 128 columns, straight from memory into registers, and their
-// sums meet in shared memory.  Four slices (two) are loaded before the first
-// is multiplied.  A BF16 x is quantized by the lane that needs it: lane (r, g)
-// holds columns 16 g .. +15 and 64 + 16 g .. +15 of token r, half of blocks
-// g / 2 and 2 + g / 2, the other half in lane g ^ 1.
+// sums meet in shared memory.  The weights of two slices per wavefront are on
+// their way before x is looked at.  A BF16 x is quantized by the work-group, 8
+// columns to a lane, into shared memory (a slice of 16 rows x 128 codes, its
+// 16-byte pieces permuted by the row as in the large product); x in codes
+// comes from memory as the weights do.
 constexpr int kFromBf16 = 2;  // beside the formats, what x is
 
 struct Few {
     MxMat mx;           // x as codes
     const uint16_t* p;  // or BF16
     int64_t ld, tokens, cols;
-    bool wide;  // BF16 rows are whole 4-byte words
+    bool vec;
 };
-
-struct FewX {
-    i32x8 codes;
-    int scale;
-};
-
-template <int XF> struct FewRaw {
-    i32x4 lo, hi;
-    int scale;
-};
-template <> struct FewRaw<kFromBf16> {
-    i32x4 v[4];  // columns 16 g + 0, 8 and 64 + 16 g + 0, 8
-};
-
-template <int XF> __device__ __forceinline__ FewRaw<XF> few_load(const Few& x, int s, int slices, int r, int g) {
-    FewRaw<XF> f;
-    const int n = r < x.tokens ? slices : 0;
-    if constexpr (XF == kFromBf16) {
-        const auto b = readable(x.p, ((x.tokens - 1) * x.ld + x.cols) * 2);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int64_t c = (int64_t)s * 128 + (k >> 1) * 64 + g * 16 + (k & 1) * 8;
-            const int left = c < x.cols ? (int)min((int64_t)8, x.cols - c) : 0;
-            const uint32_t off = (uint32_t)(r * x.ld + c) * 2;
-            const int here = s < n ? left : 0;  // columns to read
-            if (x.wide) {
-                f.v[k] = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(b, (int)inside(off, 0, here), 0, 0));
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t lo = __builtin_amdgcn_raw_buffer_load_b16(b, (int)inside(off + 4 * i, 2 * i, here), 0, 0);
-                    const uint32_t hi =
-                        __builtin_amdgcn_raw_buffer_load_b16(b, (int)inside(off + 4 * i + 2, 2 * i + 1, here), 0, 0);
-                    f.v[k][i] = (int)(lo | (hi << 16));
-                }
-            }
-            // what lies behind the last column belongs to something else
-            if ((int64_t)s * 128 + 128 > x.cols)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    f.v[k][i] &= (2 * i < left ? 0xFFFF : 0) | (2 * i + 1 < left ? (int)0xFFFF0000 : 0);
-        }
-    } else {
-        constexpr int kRow = XF == Q4MX_FP4 ? 64 : 128;
-        const int64_t pitch = x.mx.slices * kRow;
-        const auto b = readable(x.mx.codes, x.mx.rows * pitch);
-        const auto bs = readable(x.mx.scales, x.mx.slices * x.mx.rows * 4);
-        const uint32_t off = (uint32_t)(r * pitch) + (uint32_t)(s * kRow) + g * 16;
-        f.lo = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(b, (int)inside(off, s, n), 0, 0));
-        f.hi = i32x4{0, 0, 0, 0};
-        if (XF == Q4MX_FP8)
-            f.hi = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(b, (int)inside(off + 64, s, n), 0, 0));
-        f.scale = __builtin_amdgcn_raw_buffer_load_b8(bs, (int)inside(((uint32_t)s * (uint32_t)x.mx.rows + r) * 4 + g, s, n), 0, 0);
-    }
-    return f;
-}
-
-template <int XF> __device__ __forceinline__ FewX few_operand(const FewRaw<XF>& f, int lane) {
-    FewX x;
-    if constexpr (XF == kFromBf16) {
-        uint32_t e[2];
-        i32x4 half[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            float v[16];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const uint32_t w = (uint32_t)f.v[2 * h + i / 4][i % 4];
-                v[2 * i] = bf16_value(w & 0xFFFFu);
-                v[2 * i + 1] = __uint_as_float(w & 0xFFFF0000u);
-            }
-            uint32_t top = 0;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-            top = max(top, (uint32_t)__shfl_xor((int)top, 16));
-            e[h] = scale_byte<Q4MX_FP8>(top);
-            const float s = scale_of(e[h]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) half[h][i] = e[h] == 255 ? 0 : (int)enc8x4(v + 4 * i, s);
-        }
-        x.codes = __builtin_shufflevector(half[0], half[1], 0, 1, 2, 3, 4, 5, 6, 7);
-        // the scale of block g: blocks 0, 1 are in lanes 0, 2's first halves, 2, 3 in the second
-        const int r = lane & 15, g = lane >> 4;
-        const int first = __shfl((int)e[0], r + 32), second = __shfl((int)e[1], r);
-        x.scale = g == 0 ? (int)e[0] : g == 1 ? first : g == 2 ? second : (int)e[1];
-    } else {
-        x.codes = __builtin_shufflevector(f.lo, f.hi, 0, 1, 2, 3, 4, 5, 6, 7);
-        x.scale = f.scale;
-    }
-    return x;
-}
 
 template <int XF, int NW> __global__ __launch_bounds__(64 * NW) void k_mx_linear_few(Few x, MxMat w, Out y) {
+    constexpr int kAhead = 2, kSeg = NW * kAhead;  // slices per segment
     __shared__ f32x4 sums[NW][64];
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    __shared__ __attribute__((aligned(16))) char xcodes[XF == kFromBf16 ? kSeg * 2048 : 16];
+    __shared__ uint8_t xscales[XF == kFromBf16 ? kSeg * 64 : 4];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int r = lane & 15, g = lane >> 4;
     const int64_t n0 = (int64_t)blockIdx.x * 16, wp = w.slices * 64;
     const int slices = (int)w.slices;
     const auto b = readable(w.codes + n0 * wp, (w.rows - n0) * wp);
     const auto bs = readable(w.scales, w.slices * w.rows * 4);
     const uint32_t off = (uint32_t)(r * wp) + g * 16, soff = (uint32_t)(n0 + r) * 4 + g;
-    constexpr int kAhead = NW < 16 ? 4 : 2;  // 1024 threads have 128 registers each
+    const i32x4 none = {0, 0, 0, 0};
     f32x4 acc = {0, 0, 0, 0};
-    for (int s0 = wave; s0 < slices; s0 += NW * kAhead) {
-        i32x4 a[kAhead];
-        int sa[kAhead];
-        FewRaw<XF> f[kAhead];
+    for (int s0 = 0; s0 < slices; s0 += kSeg) {
+        i32x4 a[kAhead], lo[kAhead], hi[kAhead];
+        int sa[kAhead], sx[kAhead];
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
-            const int s = s0 + k * NW;
+            const int s = s0 + k * NW + wave;
             a[k] = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(b, (int)inside(off + (uint32_t)s * 64, s, slices), 0, 0));
             sa[k] = __builtin_amdgcn_raw_buffer_load_b8(bs, (int)inside(soff + (uint32_t)s * (uint32_t)w.rows * 4, s, slices), 0, 0);
-            f[k] = few_load<XF>(x, s, slices, r, g);
+            if constexpr (XF != kFromBf16) {
+                constexpr int kRow = XF == Q4MX_FP4 ? 64 : 128;
+                const int n = r < x.tokens ? slices : 0;
+                const auto bx = readable(x.mx.codes, x.mx.rows * x.mx.slices * kRow);
+                const auto bxs = readable(x.mx.scales, x.mx.slices * x.mx.rows * 4);
+                const uint32_t o = (uint32_t)(r * x.mx.slices + s) * kRow + g * 16;
+                lo[k] = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(bx, (int)inside(o, s, n), 0, 0));
+                hi[k] = none;
+                if (XF == Q4MX_FP8)
+                    hi[k] = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(bx, (int)inside(o + 64, s, n), 0, 0));
+                sx[k] = __builtin_amdgcn_raw_buffer_load_b8(
+                    bxs, (int)inside(((uint32_t)s * (uint32_t)x.mx.rows + r) * 4 + g, s, n), 0, 0);
+            }
+        }
+        if constexpr (XF == kFromBf16) {
+            if (s0 > 0) __syncthreads();  // the segment before is read
+            // rows past the last token stay as they are: their results are not stored
+            for (int i = tid; i < (int)x.tokens * kSeg * 16; i += 64 * NW) {
+                const int row = i / (kSeg * 16), c = i % (kSeg * 16), sl = c >> 4;
+                const int64_t col = (int64_t)s0 * 128 + c * 8;
+                float v[8];
+                if (x.vec) load8<true, true>(x.p, row * x.ld + col, x.cols - col, v);
+                else load8<true, false>(x.p, row * x.ld + col, x.cols - col, v);
+                uint32_t top = 0;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) top = max(top, __float_as_uint(v[k]) & 0x7FFFFFFFu);
+                const uint32_t e = scale_byte<Q4MX_FP8>(quad_max(top));
+                const float s = scale_of(e);
+                *reinterpret_cast<uint2*>(xcodes + sl * 2048 + row * 128 + ((((c & 15) >> 1) ^ (row & 7)) * 16) + (c & 1) * 8) =
+                    e == 255 ? make_uint2(0, 0) : make_uint2(enc8x4(v, s), enc8x4(v + 4, s));
+                if ((c & 3) == 0) xscales[(sl * 16 + row) * 4 + ((c & 15) >> 2)] = (uint8_t)e;
+            }
+            __syncthreads();
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                const char* const p = xcodes + (k * NW + wave) * 2048 + r * 128;
+                lo[k] = *reinterpret_cast<const i32x4*>(p + ((g ^ (r & 7)) * 16));
+                hi[k] = *reinterpret_cast<const i32x4*>(p + (((4 + g) ^ (r & 7)) * 16));
+                sx[k] = xscales[((k * NW + wave) * 16 + r) * 4 + g];
+            }
         }
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-            const FewX o = few_operand<XF>(f[k], lane);
-            const i32x4 none = {0, 0, 0, 0};
+        for (int k = 0; k < kAhead; ++k)
             acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                __builtin_shufflevector(a[k], none, 0, 1, 2, 3, 4, 5, 6, 7), o.codes, acc, 4, XF == Q4MX_FP4 ? 4 : 0, 0,
-                sa[k], 0, o.scale);
-        }
+                __builtin_shufflevector(a[k], none, 0, 1, 2, 3, 4, 5, 6, 7),
+                __builtin_shufflevector(lo[k], hi[k], 0, 1, 2, 3, 4, 5, 6, 7), acc, 4, XF == Q4MX_FP4 ? 4 : 0, 0, sa[k],
+                0, sx[k]);
     }
     sums[wave][lane] = acc;
     __syncthreads();
@@ -482,7 +545,7 @@ __global__ __launch_bounds__(64 * WC* WD, 2) void k_mx_grad(Gradient a, MxMat m,
 
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int64_t depth = m.rows;
-    const Unit u = unit_of(cut, (int)((depth + 63) / 64), FC * FD);
+    const Unit u = unit_of(cut, blockIdx.x, (int)((depth + 63) / 64), FC * FD);
     const int64_t c0 = (int64_t)u.i0 * BC, d0 = (int64_t)u.i1 * BD;
     const uint32_t base = lds_base(lds);
 
@@ -653,8 +716,8 @@ __global__ __launch_bounds__(256) void k_align_rows(const uint16_t* src, int64_t
 // Joins the runs of split tiles: the sums of one fragment (16 x 16 results of
 // every wavefront), in the order of the runs, and their place in the result.
 // SWAP: a lane's 4 results lie along the second axis of the tile grid, else
-// along the first.
-template <int W0, int W1, int F0, int F1, bool SWAP>
+// along the first; PAIRED: there as linear has them.
+template <int W0, int W1, int F0, int F1, bool SWAP, bool PAIRED>
 __global__ __launch_bounds__(64 * W0* W1) void k_mx_join(Cut cut, Out out) {
     constexpr int B0 = W0 * F0 * 16, B1 = W1 * F1 * 16;
     const uint32_t tile = blockIdx.x / (F0 * F1), frag = blockIdx.x % (F0 * F1);
@@ -664,10 +727,11 @@ __global__ __launch_bounds__(64 * W0* W1) void k_mx_join(Cut cut, Out out) {
     f32x4 v = {0, 0, 0, 0};
     for (uint32_t k = 0; k < cut.split; ++k) v += p[(int64_t)k * (F0 * F1) * blockDim.x];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
-    const int64_t a = (int64_t)i0 * B0 + (wave % W0 * F0 + frag / F1) * 16;
-    const int64_t b = (int64_t)i1 * B1 + (wave / W0 * F1 + frag % F1) * 16;
-    if (SWAP) put4(out, a + r, b + g * 4, v);
-    else put4(out, b + r, a + g * 4, v);
+    const int64_t a = (int64_t)i0 * B0 + wave % W0 * F0 * 16, b = (int64_t)i1 * B1 + wave / W0 * F1 * 16;
+    const int i = frag / F1, j = frag % F1;
+    if (PAIRED) put4(out, b + j * 16 + r, a + (i >> 1) * 32 + (i & 1) * 4 + g * 8, v);
+    else if (SWAP) put4(out, a + i * 16 + r, b + j * 16 + g * 4, v);
+    else put4(out, b + j * 16 + r, a + i * 16 + g * 4, v);
 }
 
 // ---- how a product is cut ---------------------------------------------------------
@@ -734,22 +798,28 @@ hipError_t grad(const Gradient& a, const MxMat& m, const Out& out, void* ws, hip
     else k_mx_grad<TURNED, FMT, SWAP, 2, 2, 4, 4><<<units, dim3(256), 0, st>>>(a, m, out, cut);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || cut.split == 1) return e;
-    if (p.big) k_mx_join<2, 4, 8, 4, SWAP><<<joins, dim3(512), 0, st>>>(cut, out);
-    else k_mx_join<2, 2, 4, 4, SWAP><<<joins, dim3(256), 0, st>>>(cut, out);
+    if (p.big) k_mx_join<2, 4, 8, 4, SWAP, false><<<joins, dim3(512), 0, st>>>(cut, out);
+    else k_mx_join<2, 2, 4, 4, SWAP, false><<<joins, dim3(256), 0, st>>>(cut, out);
     return hipGetLastError();
 }
 
 template <int XF> hipError_t linear(const MxMat& x, const MxMat& w, const Out& y, void* ws, hipStream_t st) {
-    const Plan p = linear_plan(x, w);
+    Plan p = linear_plan(x, w);
+    if (w.slices == 0) p.cut = Cut{p.cut.n0, p.cut.n1, 0, p.cut.n0 * p.cut.n1, 0, nullptr};  // joins no runs: zeros
     Cut cut = p.cut;
     cut.part = static_cast<f32x4*>(ws);
-    const dim3 units(cut.full + cut.rest * cut.split), joins(cut.rest * (p.big ? 32 : 16));
-    if (p.big) k_mx_linear<XF, 2, 4, 8, 4><<<units, dim3(512), 0, st>>>(x, w, y, cut);
-    else k_mx_linear<XF, 2, 2, 4, 4><<<units, dim3(256), 0, st>>>(x, w, y, cut);
+    const uint32_t units = cut.full + cut.rest * cut.split;
+    const dim3 joins(cut.rest * (p.big ? 32 : 16));
+    if (units == 0) {
+    } else if (p.big) {
+        k_mx_linear<XF, 2, 4, 8, 4><<<dim3(std::min(units, 256u)), dim3(512), 0, st>>>(x, w, y, cut);
+    } else {
+        k_mx_linear<XF, 2, 2, 4, 4><<<dim3(std::min(units, 512u)), dim3(256), 0, st>>>(x, w, y, cut);
+    }
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || cut.split == 1) return e;
-    if (p.big) k_mx_join<2, 4, 8, 4, false><<<joins, dim3(512), 0, st>>>(cut, y);
-    else k_mx_join<2, 2, 4, 4, false><<<joins, dim3(256), 0, st>>>(cut, y);
+    if (p.big) k_mx_join<2, 4, 8, 4, false, true><<<joins, dim3(512), 0, st>>>(cut, y);
+    else k_mx_join<2, 2, 4, 4, false, true><<<joins, dim3(256), 0, st>>>(cut, y);
     return hipGetLastError();
 }
 
@@ -790,8 +860,8 @@ size_t linear_workspace(const MxMat& x, const MxMat& w) {
 size_t grad_workspace(const MxMat& m, int64_t width) { return grad_plan(m, width).bytes; }
 
 hipError_t launch_linear_few(const Dense& x, int64_t tokens, const MxMat& w, const Dense& y, hipStream_t st) {
-    const bool wide = (reinterpret_cast<uintptr_t>(x.p) & 3) == 0 && w.cols % 2 == 0 && (tokens == 1 || x.ld % 2 == 0);
-    return few<kFromBf16>(Few{MxMat{}, static_cast<const uint16_t*>(x.p), x.ld, tokens, w.cols, wide}, w,
+    const bool vec = (reinterpret_cast<uintptr_t>(x.p) & 15) == 0 && (tokens == 1 || x.ld % 8 == 0);
+    return few<kFromBf16>(Few{MxMat{}, static_cast<const uint16_t*>(x.p), x.ld, tokens, w.cols, vec}, w,
                           result(y, tokens, w.rows, false), st);
 }
 
