@@ -81,24 +81,27 @@ template <bool BF16> __device__ __forceinline__ float load1(const void* p, int64
     return BF16 ? bf16_value(static_cast<const uint16_t*>(p)[i]) : static_cast<const float*>(p)[i];
 }
 
+// Vectors at any element's alignment: the memory path takes them whole.
+typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(2)));
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
+
 // 8 elements from index i, of which the first `left` exist (the others read
-// as 0).  VEC: i is a multiple of 8 from a 16-byte aligned base.
-template <bool BF16, bool VEC>
-__device__ __forceinline__ void load8(const void* p, int64_t i, int64_t left, float* v) {
-    if (VEC && left >= 8) {
+// as 0).
+template <bool BF16> __device__ __forceinline__ void load8(const void* p, int64_t i, int64_t left, float* v) {
+    if (left >= 8) {
         if (BF16) {
-            const uint4 q = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
-            const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+            const u32x4_any q = *reinterpret_cast<const u32x4_any*>(static_cast<const uint16_t*>(p) + i);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                v[2 * k] = bf16_value(w[k] & 0xFFFFu);
-                v[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
+                v[2 * k] = bf16_value(q[k] & 0xFFFFu);
+                v[2 * k + 1] = __uint_as_float(q[k] & 0xFFFF0000u);
             }
         } else {
-            const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
-            const float4 a = q[0], b = q[1];
-            v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-            v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+            const f32x4_any* q = reinterpret_cast<const f32x4_any*>(static_cast<const float*>(p) + i);
+            const f32x4_any a = q[0], b = q[1];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k] = a[k], v[4 + k] = b[k];
         }
         return;
     }
@@ -106,16 +109,15 @@ __device__ __forceinline__ void load8(const void* p, int64_t i, int64_t left, fl
     for (int k = 0; k < 8; ++k) v[k] = k < left ? load1<BF16>(p, i + k) : 0.0f;
 }
 
-template <bool BF16, bool VEC>
-__device__ __forceinline__ void store8(void* p, int64_t i, int64_t left, const float* v) {
-    if (VEC && left >= 8) {
+template <bool BF16> __device__ __forceinline__ void store8(void* p, int64_t i, int64_t left, const float* v) {
+    if (left >= 8) {
         if (BF16) {
-            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + i) =
-                make_uint4(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7]));
+            *reinterpret_cast<u32x4_any*>(static_cast<uint16_t*>(p) + i) =
+                u32x4_any{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7])};
         } else {
-            float4* q = reinterpret_cast<float4*>(static_cast<float*>(p) + i);
-            q[0] = make_float4(v[0], v[1], v[2], v[3]);
-            q[1] = make_float4(v[4], v[5], v[6], v[7]);
+            f32x4_any* q = reinterpret_cast<f32x4_any*>(static_cast<float*>(p) + i);
+            q[0] = f32x4_any{v[0], v[1], v[2], v[3]};
+            q[1] = f32x4_any{v[4], v[5], v[6], v[7]};
         }
         return;
     }

@@ -34,14 +34,14 @@ __device__ __forceinline__ Lane lane_of(int64_t tile, int64_t slices, int pass) 
     return l;
 }
 
-template <bool BF16, bool VEC>
+template <bool BF16>
 __global__ __launch_bounds__(256) void k_mx_quantize(const void* src, int64_t ld, MxMat out) {
 #pragma unroll
     for (int pass = 0; pass < 2; ++pass) {
         const Lane l = lane_of(blockIdx.x, out.slices, pass);
         if (l.row >= out.rows) return;
         float v[8];
-        load8<BF16, VEC>(src, l.row * ld + l.col, out.cols - l.col, v);
+        load8<BF16>(src, l.row * ld + l.col, out.cols - l.col, v);
         store_mx8(out, l.row, l.col, v);
     }
 }
@@ -90,7 +90,7 @@ __global__ __launch_bounds__(256) void k_mx_quantize_t(const void* src, int64_t 
             *reinterpret_cast<const uint32_t*>(lds_scale[threadIdx.x]);
 }
 
-template <bool BF16, bool VEC>
+template <bool BF16>
 __global__ __launch_bounds__(256) void k_mx_dequantize(MxMat a, void* dst, int64_t ld) {
 #pragma unroll
     for (int pass = 0; pass < 2; ++pass) {
@@ -98,7 +98,7 @@ __global__ __launch_bounds__(256) void k_mx_dequantize(MxMat a, void* dst, int64
         if (l.row >= a.rows || l.col >= a.cols) return;
         float v[8];
         load_mx8(a, l.row, l.col, v);
-        store8<BF16, VEC>(dst, l.row * ld + l.col, a.cols - l.col, v);
+        store8<BF16>(dst, l.row * ld + l.col, a.cols - l.col, v);
     }
 }
 
@@ -143,7 +143,7 @@ template <int ACT> __device__ __forceinline__ ActValue act_value(float x) {
     return {x * p, __builtin_fmaf(x, n, p)};
 }
 
-template <int ACT, bool VEC>
+template <int ACT>
 __global__ __launch_bounds__(256) void k_act_forward(const void* x, int64_t ldx, const void* up, int64_t ldup,
                                                       int64_t rows, int64_t cols, int64_t slices, void* y, int64_t ldy,
                                                       MxMat ymx, MxMat kx, MxMat ku) {
@@ -153,22 +153,22 @@ __global__ __launch_bounds__(256) void k_act_forward(const void* x, int64_t ldx,
         if (l.row >= rows) return;
         const int64_t left = cols - l.col;
         float v[8], u[8], r[8];
-        load8<true, VEC>(x, l.row * ldx + l.col, left, v);
-        if (ACT == Q4MX_SWIGLU) load8<true, VEC>(up, l.row * ldup + l.col, left, u);
+        load8<true>(x, l.row * ldx + l.col, left, v);
+        if (ACT == Q4MX_SWIGLU) load8<true>(up, l.row * ldup + l.col, left, u);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             r[i] = act_value<ACT>(v[i]).f;
             if (ACT == Q4MX_SWIGLU) r[i] *= u[i];
             r[i] = round_bf16(r[i]);
         }
-        if (y && left > 0) store8<true, VEC>(y, l.row * ldy + l.col, left, r);
+        if (y && left > 0) store8<true>(y, l.row * ldy + l.col, left, r);
         if (ymx.codes) store_mx8(ymx, l.row, l.col, r);
         if (kx.codes) store_mx8(kx, l.row, l.col, v);
         if (ACT == Q4MX_SWIGLU && ku.codes) store_mx8(ku, l.row, l.col, u);
     }
 }
 
-template <int ACT, bool VEC>
+template <int ACT>
 __global__ __launch_bounds__(256) void k_act_backward(MxMat kx, MxMat ku, const void* dy, int64_t lddy, void* dx,
                                                        int64_t lddx, void* dup, int64_t lddup) {
 #pragma unroll
@@ -177,7 +177,7 @@ __global__ __launch_bounds__(256) void k_act_backward(MxMat kx, MxMat ku, const 
         if (l.row >= kx.rows || l.col >= kx.cols) return;
         const int64_t left = kx.cols - l.col;
         float g[8], v[8], u[8];
-        load8<true, VEC>(dy, l.row * lddy + l.col, left, g);
+        load8<true>(dy, l.row * lddy + l.col, left, g);
         load_mx8(kx, l.row, l.col, v);
         if (ACT == Q4MX_SWIGLU) load_mx8(ku, l.row, l.col, u);
         float a[8], b[8];
@@ -187,16 +187,9 @@ __global__ __launch_bounds__(256) void k_act_backward(MxMat kx, MxMat ku, const 
             a[i] = ACT == Q4MX_SWIGLU ? g[i] * u[i] * t.d : g[i] * t.d;
             b[i] = g[i] * t.f;
         }
-        store8<true, VEC>(dx, l.row * lddx + l.col, left, a);
-        if (ACT == Q4MX_SWIGLU) store8<true, VEC>(dup, l.row * lddup + l.col, left, b);
+        store8<true>(dx, l.row * lddx + l.col, left, a);
+        if (ACT == Q4MX_SWIGLU) store8<true>(dup, l.row * lddup + l.col, left, b);
     }
-}
-
-// Whether 8 consecutive elements from a multiple of 8 are 16-byte accesses.
-bool vec_ok(const Dense& d) {
-    if (!d.p) return true;
-    const int64_t per16 = d.dtype == Q4MX_F32 ? 4 : 8;
-    return (reinterpret_cast<uintptr_t>(d.p) & 15) == 0 && d.ld % per16 == 0;
 }
 
 int64_t row_tiles(int64_t rows, int64_t slices) { return (rows + kTileRows - 1) / kTileRows * slices; }
@@ -215,21 +208,15 @@ hipError_t launch_mx_quantize(const Dense& src, bool transpose, const MxMat& out
         return hipGetLastError();
     }
     const dim3 g((unsigned)row_tiles(out.rows, out.slices)), b(256);
-    const bool vec = vec_ok(src);
-    if (bf && vec) k_mx_quantize<true, true><<<g, b, 0, st>>>(src.p, src.ld, out);
-    else if (bf) k_mx_quantize<true, false><<<g, b, 0, st>>>(src.p, src.ld, out);
-    else if (vec) k_mx_quantize<false, true><<<g, b, 0, st>>>(src.p, src.ld, out);
-    else k_mx_quantize<false, false><<<g, b, 0, st>>>(src.p, src.ld, out);
+    if (bf) k_mx_quantize<true><<<g, b, 0, st>>>(src.p, src.ld, out);
+    else k_mx_quantize<false><<<g, b, 0, st>>>(src.p, src.ld, out);
     return hipGetLastError();
 }
 
 hipError_t launch_mx_dequantize(const MxMat& a, const Dense& dst, hipStream_t st) {
     const dim3 g((unsigned)row_tiles(a.rows, a.slices)), b(256);
-    const bool bf = dst.dtype == Q4MX_BF16, vec = vec_ok(dst);
-    if (bf && vec) k_mx_dequantize<true, true><<<g, b, 0, st>>>(a, dst.p, dst.ld);
-    else if (bf) k_mx_dequantize<true, false><<<g, b, 0, st>>>(a, dst.p, dst.ld);
-    else if (vec) k_mx_dequantize<false, true><<<g, b, 0, st>>>(a, dst.p, dst.ld);
-    else k_mx_dequantize<false, false><<<g, b, 0, st>>>(a, dst.p, dst.ld);
+    if (dst.dtype == Q4MX_BF16) k_mx_dequantize<true><<<g, b, 0, st>>>(a, dst.p, dst.ld);
+    else k_mx_dequantize<false><<<g, b, 0, st>>>(a, dst.p, dst.ld);
     return hipGetLastError();
 }
 
@@ -237,12 +224,11 @@ hipError_t launch_act_forward(int act, const Dense& x, const Dense& up, int64_t 
                               const MxMat& y_mx, const MxMat& kx, const MxMat& ku, hipStream_t st) {
     const int64_t slices = (cols + kMxPad - 1) / kMxPad;
     const dim3 g((unsigned)row_tiles(rows, slices)), b(256);
-    const bool vec = vec_ok(x) && vec_ok(up) && vec_ok(y);
-#define Q4_ACT_FWD(A, V) \
-    k_act_forward<A, V><<<g, b, 0, st>>>(x.p, x.ld, up.p, up.ld, rows, cols, slices, y.p, y.ld, y_mx, kx, ku)
-    if (act == Q4MX_GELU) vec ? Q4_ACT_FWD(Q4MX_GELU, true) : Q4_ACT_FWD(Q4MX_GELU, false);
-    else if (act == Q4MX_GELU_ERF) vec ? Q4_ACT_FWD(Q4MX_GELU_ERF, true) : Q4_ACT_FWD(Q4MX_GELU_ERF, false);
-    else vec ? Q4_ACT_FWD(Q4MX_SWIGLU, true) : Q4_ACT_FWD(Q4MX_SWIGLU, false);
+#define Q4_ACT_FWD(A) \
+    k_act_forward<A><<<g, b, 0, st>>>(x.p, x.ld, up.p, up.ld, rows, cols, slices, y.p, y.ld, y_mx, kx, ku)
+    if (act == Q4MX_GELU) Q4_ACT_FWD(Q4MX_GELU);
+    else if (act == Q4MX_GELU_ERF) Q4_ACT_FWD(Q4MX_GELU_ERF);
+    else Q4_ACT_FWD(Q4MX_SWIGLU);
 #undef Q4_ACT_FWD
     return hipGetLastError();
 }
@@ -250,11 +236,10 @@ hipError_t launch_act_forward(int act, const Dense& x, const Dense& up, int64_t 
 hipError_t launch_act_backward(int act, const MxMat& kx, const MxMat& ku, const Dense& dy, const Dense& dx,
                                const Dense& dup, hipStream_t st) {
     const dim3 g((unsigned)row_tiles(kx.rows, kx.slices)), b(256);
-    const bool vec = vec_ok(dy) && vec_ok(dx) && vec_ok(dup);
-#define Q4_ACT_BWD(A, V) k_act_backward<A, V><<<g, b, 0, st>>>(kx, ku, dy.p, dy.ld, dx.p, dx.ld, dup.p, dup.ld)
-    if (act == Q4MX_GELU) vec ? Q4_ACT_BWD(Q4MX_GELU, true) : Q4_ACT_BWD(Q4MX_GELU, false);
-    else if (act == Q4MX_GELU_ERF) vec ? Q4_ACT_BWD(Q4MX_GELU_ERF, true) : Q4_ACT_BWD(Q4MX_GELU_ERF, false);
-    else vec ? Q4_ACT_BWD(Q4MX_SWIGLU, true) : Q4_ACT_BWD(Q4MX_SWIGLU, false);
+#define Q4_ACT_BWD(A) k_act_backward<A><<<g, b, 0, st>>>(kx, ku, dy.p, dy.ld, dx.p, dx.ld, dup.p, dup.ld)
+    if (act == Q4MX_GELU) Q4_ACT_BWD(Q4MX_GELU);
+    else if (act == Q4MX_GELU_ERF) Q4_ACT_BWD(Q4MX_GELU_ERF);
+    else Q4_ACT_BWD(Q4MX_SWIGLU);
 #undef Q4_ACT_BWD
     return hipGetLastError();
 }

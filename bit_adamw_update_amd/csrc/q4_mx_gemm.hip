@@ -77,10 +77,10 @@ __device__ __forceinline__ Unit unit_of(const Cut& c, uint32_t index, int steps,
     return u;
 }
 
-// A raw buffer: loads past `bytes` read as 0 (checked per dword).
+// A raw buffer: loads past `bytes` (>= 0) read as 0 (checked per dword).
 __device__ __forceinline__ i32x4 buffer(const void* p, int64_t bytes) {
     const uint64_t a = reinterpret_cast<uint64_t>(p);
-    const uint32_t n = bytes < 0 ? 0u : bytes > 0xFFFFFF00ll ? 0xFFFFFF00u : (uint32_t)bytes;
+    const uint32_t n = (uint32_t)(bytes >> 32) != 0 ? 0xFFFFFF00u : min((uint32_t)bytes, 0xFFFFFF00u);
     i32x4 r;
     r[0] = __builtin_amdgcn_readfirstlane((int)(uint32_t)a);
     r[1] = __builtin_amdgcn_readfirstlane((int)(uint32_t)(a >> 32));
@@ -91,19 +91,10 @@ __device__ __forceinline__ i32x4 buffer(const void* p, int64_t bytes) {
 // The same, moved along as the steps of a product go.
 struct Window {
     uint64_t at;
-    uint32_t bytes;
-    __device__ __forceinline__ void open(const void* p, int64_t n) {
-        const i32x4 b = buffer(p, n);
-        at = (uint64_t)(uint32_t)b[0] | ((uint64_t)(uint32_t)b[1] << 32);
-        bytes = (uint32_t)b[2];
-    }
-    __device__ __forceinline__ void move(uint64_t by, uint32_t fewer) {
-        at += by;
-        bytes -= fewer;
-    }
-    __device__ __forceinline__ i32x4 get() const {
-        return i32x4{(int)(uint32_t)at, (int)(uint32_t)(at >> 32), (int)bytes, 0x00020000};
-    }
+    int64_t left;
+    __device__ __forceinline__ void open(const void* p, int64_t n) { at = reinterpret_cast<uint64_t>(p), left = n; }
+    __device__ __forceinline__ void move(int64_t by) { at += by, left -= by; }
+    __device__ __forceinline__ i32x4 get() const { return buffer(reinterpret_cast<const void*>(at), left); }
 };
 // The same for the compiler's own loads.
 __device__ __forceinline__ auto readable(const void* p, int64_t bytes) {
@@ -111,6 +102,7 @@ __device__ __forceinline__ auto readable(const void* p, int64_t bytes) {
     return __builtin_amdgcn_make_buffer_rsrc(
         reinterpret_cast<void*>((uint64_t)(uint32_t)b[0] | ((uint64_t)(uint32_t)b[1] << 32)), 0, b[2], b[3]);
 }
+__device__ __forceinline__ auto readable(const Window& w) { return readable(reinterpret_cast<const void*>(w.at), w.left); }
 // `off` where i < n, else an offset past every buffer (without a branch).
 __device__ __forceinline__ uint32_t inside(uint32_t off, int i, int n) { return off | (uint32_t)((n - 1 - i) >> 31); }
 
@@ -129,6 +121,7 @@ template <int N> __device__ __forceinline__ void wait_copies_and_barrier() {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
+__device__ __forceinline__ void wait_shared_and_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 __device__ __forceinline__ void phase_end() { asm volatile("s_barrier" ::: "memory"); }
 
 // Holds a value in registers at this point: what makes it stays before, what
@@ -141,50 +134,48 @@ __device__ __forceinline__ uint32_t lds_base(const void* p) {
 
 // ---- results -------------------------------------------------------------------
 
-// A result whose element (r, c) is p[r * ld + c]; `add`: added to what is there.
+// A result whose element (r, c) is p[r * ld + c]; `add`: added to what is
+// there.  Stores are 8 or 16 bytes wherever the columns are there: the memory
+// path takes them at any element's alignment.
 struct Out {
     void* p;
     int64_t ld, rows, cols;
-    bool bf16, add, vec, vec8;  // vec, vec8: 4 or 8 columns from such a multiple are one or two whole accesses
+    bool bf16, add;
 };
 
 __device__ __forceinline__ void put4(const Out& o, int64_t r, int64_t c, f32x4 v) {
     if (r >= o.rows || c >= o.cols) return;
     const int64_t at = r * o.ld + c;
-    if (o.vec && c + 3 < o.cols) {
+    if (c + 3 < o.cols) {
         if (o.bf16) {
-            uint2* p = reinterpret_cast<uint2*>(static_cast<uint16_t*>(o.p) + at);
+            u32x2_any* p = reinterpret_cast<u32x2_any*>(static_cast<uint16_t*>(o.p) + at);
             if (o.add) {
-                const uint2 g = *p;
-                v[0] += bf16_value(g.x & 0xFFFFu), v[1] += __uint_as_float(g.x & 0xFFFF0000u);
-                v[2] += bf16_value(g.y & 0xFFFFu), v[3] += __uint_as_float(g.y & 0xFFFF0000u);
+                const u32x2_any g = *p;
+                v[0] += bf16_value(g[0] & 0xFFFFu), v[1] += __uint_as_float(g[0] & 0xFFFF0000u);
+                v[2] += bf16_value(g[1] & 0xFFFFu), v[3] += __uint_as_float(g[1] & 0xFFFF0000u);
             }
-            *p = make_uint2(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]));
+            *p = u32x2_any{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
         } else {
-            f32x4* p = reinterpret_cast<f32x4*>(static_cast<float*>(o.p) + at);
+            f32x4_any* p = reinterpret_cast<f32x4_any*>(static_cast<float*>(o.p) + at);
             if (o.add) v += *p;
             *p = v;
         }
         return;
     }
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-        if (c + k < o.cols) {
-            if (o.bf16) {
-                uint16_t* p = static_cast<uint16_t*>(o.p) + at + k;
-                *p = bf16_bits(o.add ? v[k] + bf16_value(*p) : v[k]);
-            } else {
-                float* p = static_cast<float*>(o.p) + at + k;
-                *p = o.add ? v[k] + *p : v[k];
-            }
+    for (int k = 0; k < 4 && c + k < o.cols; ++k) {
+        const float x = k == 0 ? v[0] : k == 1 ? v[1] : k == 2 ? v[2] : v[3];
+        if (o.bf16) {
+            uint16_t* p = static_cast<uint16_t*>(o.p) + at + k;
+            *p = bf16_bits(o.add ? x + bf16_value(*p) : x);
+        } else {
+            float* p = static_cast<float*>(o.p) + at + k;
+            *p = o.add ? x + *p : x;
         }
+    }
 }
 
 Out result(const Dense& d, int64_t rows, int64_t cols, bool add) {
-    const int64_t unit = d.dtype == Q4MX_BF16 ? 8 : 16;
-    const bool vec = reinterpret_cast<uintptr_t>(d.p) % unit == 0 && d.ld % 4 == 0;
-    const bool vec8 = reinterpret_cast<uintptr_t>(d.p) % 16 == 0 && d.ld % 8 == 0;
-    return Out{d.p, d.ld, rows, cols, d.dtype == Q4MX_BF16, add, vec, vec8};
+    return Out{d.p, d.ld, rows, cols, d.dtype == Q4MX_BF16, add};
 }
 
 // ---- linear: codes by codes -------------------------------------------------------
@@ -245,11 +236,13 @@ __global__ __launch_bounds__(64 * WN* WT, 2) void k_mx_linear(MxMat x, MxMat w, 
             const int64_t n0 = (int64_t)u.i0 * BN, t0 = (int64_t)u.i1 * BT, s0 = xs ? t0 : n0, s = u.first;
             ww.open(w.codes + n0 * wp + s * 64, (w.rows - n0) * wp - s * 64);
             wx.open(x.codes + t0 * xp + s * XB, (x.rows - t0) * xp - s * XB);
-            ws.open(scales + (s * srows + s0) * 4, (srows - s0) * 4);
+            ws.open(scales + (s * srows + s0) * 4, ((w.slices - s) * srows - s0) * 4);
             next_left = u.last - u.first;
         }
     };
     auto issue = [&] {
+        // past the last row the scales are another slice's: its codes are 0,
+        // and what a row of NaN there gives is not stored
         const i32x4 bw = ww.get(), bx = wx.get(), bs = ws.get();
 #pragma unroll
         for (int j = 0; j < CW; ++j) copy16(bw, woff[j], next_at + (j * NW + wave) * 1024);
@@ -261,9 +254,9 @@ __global__ __launch_bounds__(64 * WN* WT, 2) void k_mx_linear(MxMat x, MxMat w, 
             next_unit += gridDim.x;
             open();
         } else {
-            ww.move(64, 64);
-            wx.move(XB, XB);
-            ws.move((uint64_t)srows * 4, 0);
+            ww.move(64);
+            wx.move(XB);
+            ws.move(srows * 4);
         }
     };
 
@@ -358,17 +351,17 @@ __global__ __launch_bounds__(64 * WN* WT, 2) void k_mx_linear(MxMat x, MxMat w, 
             for (int i = 0; i < FN; ++i)
 #pragma unroll
                 for (int j = 0; j < FT; ++j) u.part[(i * FT + j) * blockDim.x + threadIdx.x] = acc[i][j];
-        } else if (y.bf16 && y.vec8 && n0 + BN <= y.cols && t0 + BT <= y.rows) {
+        } else if (y.bf16 && n0 + BN <= y.cols && t0 + BT <= y.rows) {
             // whole tile: exactly kStores stores
             uint16_t* const p = static_cast<uint16_t*>(y.p) + (t0 + xrow) * y.ld + n0 + wn * FN * 16 + g * 8;
 #pragma unroll
             for (int j = 0; j < FT; ++j)
 #pragma unroll
                 for (int i = 0; i < FN; i += 2)
-                    *reinterpret_cast<uint4*>(p + j * 16 * y.ld + i * 16) =
-                        make_uint4(bf16_pair(acc[i][j][0], acc[i][j][1]), bf16_pair(acc[i][j][2], acc[i][j][3]),
-                                   bf16_pair(acc[i + 1][j][0], acc[i + 1][j][1]),
-                                   bf16_pair(acc[i + 1][j][2], acc[i + 1][j][3]));
+                    *reinterpret_cast<u32x4_any*>(p + j * 16 * y.ld + i * 16) =
+                        u32x4_any{bf16_pair(acc[i][j][0], acc[i][j][1]), bf16_pair(acc[i][j][2], acc[i][j][3]),
+                                  bf16_pair(acc[i + 1][j][0], acc[i + 1][j][1]),
+                                  bf16_pair(acc[i + 1][j][2], acc[i + 1][j][3])};
             stored = true;
         } else {
 #pragma unroll
@@ -398,7 +391,6 @@ struct Few {
     MxMat mx;           // x as codes
     const uint16_t* p;  // or BF16
     int64_t ld, tokens, cols;
-    bool vec;
 };
 
 template <int XF, int NW> __global__ __launch_bounds__(64 * NW) void k_mx_linear_few(Few x, MxMat w, Out y) {
@@ -444,8 +436,7 @@ template <int XF, int NW> __global__ __launch_bounds__(64 * NW) void k_mx_linear
                 const int row = i / (kSeg * 16), c = i % (kSeg * 16), sl = c >> 4;
                 const int64_t col = (int64_t)s0 * 128 + c * 8;
                 float v[8];
-                if (x.vec) load8<true, true>(x.p, row * x.ld + col, x.cols - col, v);
-                else load8<true, false>(x.p, row * x.ld + col, x.cols - col, v);
+                load8<true>(x.p, row * x.ld + col, x.cols - col, v);
                 uint32_t top = 0;
 #pragma unroll
                 for (int k = 0; k < 8; ++k) top = max(top, __float_as_uint(v[k]) & 0x7FFFFFFFu);
@@ -495,7 +486,10 @@ template <int XF, int NW> __global__ __launch_bounds__(64 * NW) void k_mx_linear
 // transposing read, and those of the neighbouring lane group, lie in different
 // banks; [d][k] rows in 16-byte pieces by d % 8.
 //
-// Two steps in a ring: while step s is multiplied, s + 1 is decoded and copied.
+// The steps of a work-group's units form one stream, as in linear, and half of
+// the wavefronts run a phase behind: while one wavefront of a SIMD multiplies
+// (half a step), the other decodes, copies and reads fragments.  Three steps
+// of the dense operand and two of the codes are in rings.
 __device__ __forceinline__ bf16x8 read_turned(const char* p, int pitch) {
     union {
         s16x4 h[2];
@@ -541,12 +535,12 @@ __global__ __launch_bounds__(64 * WC* WD, 2) void k_mx_grad(Gradient a, MxMat m,
     constexpr int CD = kD / 1024 / NW;
     constexpr int LPR = BC / 8;  // lanes of a row of codes
     static_assert(NW * 64 / LPR == 16 && kD % (1024 * NW) == 0, "tile");
-    __shared__ __attribute__((aligned(1024))) char lds[2 * (kD + kC)];
+    __shared__ __attribute__((aligned(1024))) char lds[3 * kD + 2 * kC];
 
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int64_t depth = m.rows;
-    const Unit u = unit_of(cut, blockIdx.x, (int)((depth + 63) / 64), FC * FD);
-    const int64_t c0 = (int64_t)u.i0 * BC, d0 = (int64_t)u.i1 * BD;
+    const int steps = (int)((depth + 63) / 64);
+    const uint32_t units = units_of(cut);
     const uint32_t base = lds_base(lds);
 
     // dense: this lane's pieces of the step's copies
@@ -566,22 +560,6 @@ __global__ __launch_bounds__(64 * WC* WD, 2) void k_mx_grad(Gradient a, MxMat m,
             dk[j] = piece * 8;
         }
     }
-    auto copy_dense = [&](int s) {
-        const uint32_t at = base + (uint32_t)(s & 1) * kD;
-        const int64_t k0 = (int64_t)s * 64;
-        if (TURNED) {
-            const i32x4 b = buffer(a.p + k0 * a.ld + d0, ((depth - 1 - k0) * a.ld + a.span - d0) * 2);
-#pragma unroll
-            for (int j = 0; j < CD; ++j) copy16(b, doff[j], at + (j * NW + wave) * 1024);
-        } else {
-            const i32x4 b = buffer(a.p + d0 * a.ld + k0, ((a.width - 1 - d0) * a.ld + a.span - k0) * 2);
-            const int left = (int)min((int64_t)64, depth - k0);
-#pragma unroll
-            for (int j = 0; j < CD; ++j)
-                copy16(b, inside(doff[j], dk[j], left), at + (j * NW + wave) * 1024);
-        }
-    };
-
     // codes: rows crow + 16 p, columns ccol .. ccol + 7 of the step
     constexpr int kCode = FMT == Q4MX_FP4 ? 4 : 8;  // bytes of 8 codes
     const int64_t cp = m.slices * (FMT == Q4MX_FP4 ? 64 : 128);
@@ -589,20 +567,35 @@ __global__ __launch_bounds__(64 * WC* WD, 2) void k_mx_grad(Gradient a, MxMat m,
     const uint32_t coff = (uint32_t)crow * (uint32_t)cp + (uint32_t)(ccol / 8 * kCode);
     const uint32_t soff = ((uint32_t)(ccol >> 7) * (uint32_t)m.rows + crow) * 4 + ((ccol >> 5) & 3);
     const int cf = (crow & 3) | (((crow >> 3) & 1) << 2);
-    const int cat = 2 * kD + crow * (BC * 2) + (((tid % LPR) >> 1) ^ cf) * 32 + (tid & 1) * 16;
+    const int cat = 3 * kD + crow * (BC * 2) + (((tid % LPR) >> 1) ^ cf) * 32 + (tid & 1) * 16;
     uint32_t code[4][kCode / 4];
     uint32_t scale[4];
-    auto load_codes = [&](int s) {
-        const int64_t k0 = (int64_t)s * 64;
-        const auto b = readable(m.codes + k0 * cp + c0 / 8 * kCode, (m.rows - k0) * cp - c0 / 8 * kCode);
-        const int64_t sfirst = (c0 / 128) * m.rows + k0;
-        const auto bs = readable(m.scales + sfirst * 4, (m.slices * m.rows - sfirst) * 4);
-        const int left = (int)min((int64_t)64, m.rows - k0);
+    // the stream, two steps ahead of the products
+    uint32_t next_unit = blockIdx.x, next_at = base;
+    int next_left = 0, next_rows = 0;  // steps of the unit, rows of the sum
+    Window wd, wk, ws;
+    auto open = [&] {
+        if (next_unit < units) {
+            const Unit u = unit_of(cut, next_unit, steps, FC * FD);
+            const int64_t c0 = (int64_t)u.i0 * BC, d0 = (int64_t)u.i1 * BD, k0 = (int64_t)u.first * 64;
+            if (TURNED) wd.open(a.p + k0 * a.ld + d0, ((depth - 1 - k0) * a.ld + a.span - d0) * 2);
+            else wd.open(a.p + d0 * a.ld + k0, ((a.width - 1 - d0) * a.ld + a.span - k0) * 2);
+            wk.open(m.codes + k0 * cp + c0 / 8 * kCode, (depth - k0) * cp - c0 / 8 * kCode);
+            const int64_t s0 = (c0 / 128) * m.rows + k0;
+            ws.open(m.scales + s0 * 4, (m.slices * m.rows - s0) * 4);
+            next_left = u.last - u.first;
+            next_rows = (int)(depth - k0);
+        }
+    };
+    // Loads the stream's next step: codes to registers, the dense operand's
+    // pieces to shared memory.
+    auto load = [&] {
+        const auto b = readable(wk), bs = readable(ws);
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
             // past the last row both read as 0 (the scale there is another
             // row's, which may be a NaN's)
-            const uint32_t o = inside(coff + (uint32_t)(16 * p) * (uint32_t)cp, crow + 16 * p, left);
+            const uint32_t o = inside(coff + (uint32_t)(16 * p) * (uint32_t)cp, crow + 16 * p, next_rows);
             if (FMT == Q4MX_FP4) {
                 code[p][0] = __builtin_amdgcn_raw_buffer_load_b32(b, (int)o, 0, 0);
             } else {
@@ -610,11 +603,26 @@ __global__ __launch_bounds__(64 * WC* WD, 2) void k_mx_grad(Gradient a, MxMat m,
                 code[p][0] = t[0];
                 code[p][kCode / 4 - 1] = t[1];
             }
-            scale[p] = __builtin_amdgcn_raw_buffer_load_b8(bs, (int)inside(soff + 64 * p, crow + 16 * p, left), 0, 0);
+            scale[p] = __builtin_amdgcn_raw_buffer_load_b8(bs, (int)inside(soff + 64 * p, crow + 16 * p, next_rows), 0, 0);
+        }
+        const i32x4 bd = wd.get();
+#pragma unroll
+        for (int j = 0; j < CD; ++j)
+            copy16(bd, TURNED ? doff[j] : inside(doff[j], dk[j], next_rows), next_at + (j * NW + wave) * 1024);
+        next_at = next_at == base + 2 * kD ? base : next_at + kD;
+        if (--next_left == 0) {
+            next_unit += gridDim.x;
+            open();
+        } else {
+            wd.move(TURNED ? 128 * a.ld : 128);
+            wk.move(64 * cp);
+            ws.move(256);
+            next_rows -= 64;
         }
     };
-    auto decode = [&](int s) {
-        char* const at = lds + cat + (s & 1) * kC;
+    // Decodes the step that was loaded last into the ring's buffer `slot`.
+    auto decode = [&](int slot) {
+        char* const at = lds + cat + slot * kC;
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
             const float f = scale_of(scale[p]);
@@ -631,69 +639,115 @@ __global__ __launch_bounds__(64 * WC* WD, 2) void k_mx_grad(Gradient a, MxMat m,
     };
 
     // fragments: lane (r, g) reads rows k = 32 q + 8 g + r / 4 (+ 4) at columns 4 (r % 4)
-    const int r = lane & 15, g = lane >> 4, wc = wave % WC, wd = wave / WC;
+    const int r = lane & 15, g = lane >> 4, wc = wave % WC, wdn = wave / WC;
     const int f = (r >> 2) | ((g & 1) << 2), krow = g * 8 + (r >> 2);
     int cread[FC], dread[FD];
 #pragma unroll
-    for (int i = 0; i < FC; ++i) cread[i] = 2 * kD + krow * (BC * 2) + ((wc * FC + i) ^ f) * 32 + (r & 3) * 8;
+    for (int i = 0; i < FC; ++i) cread[i] = 3 * kD + krow * (BC * 2) + ((wc * FC + i) ^ f) * 32 + (r & 3) * 8;
 #pragma unroll
     for (int j = 0; j < FD; ++j)
-        dread[j] = TURNED ? krow * (BD * 2) + ((wd * FD + j) ^ f) * 32 + (r & 3) * 8 : ((wd * FD + j) * 16 + r) * 128;
+        dread[j] = TURNED ? krow * (BD * 2) + ((wdn * FD + j) ^ f) * 32 + (r & 3) * 8 : ((wdn * FD + j) * 16 + r) * 128;
 
     f32x4 acc[FC][FD] = {};
-    if (u.first < u.last) {
-        copy_dense(u.first);
-        load_codes(u.first);
-        decode(u.first);
-        if (u.first + 1 < u.last) load_codes(u.first + 1);
-    }
-    for (int s = u.first; s < u.last; ++s) {
-        // everything of step s has arrived, and every wavefront is done with
-        // the buffers that step s + 1 takes
-        asm volatile("" ::: "memory");
-        __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
-        __builtin_amdgcn_s_barrier();
-        asm volatile("" ::: "memory");
-        if (s + 1 < u.last) {
-            copy_dense(s + 1);
-            decode(s + 1);
-            if (s + 2 < u.last) load_codes(s + 2);
-        }
-        const char* const cs = lds + (s & 1) * kC;
-        const char* const ds = lds + (s & 1) * kD;
+    bf16x8 c[FC], d[FD];
+    auto read = [&](int ds, int cs, int q) {
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            bf16x8 c[FC], d[FD];
+        for (int j = 0; j < FD; ++j)
+            d[j] = TURNED ? read_turned(lds + ds * kD + dread[j] + q * 32 * (BD * 2), BD * 2)
+                          : *reinterpret_cast<const bf16x8*>(lds + ds * kD + dread[j] + ((4 * q + g) ^ (r & 7)) * 16);
 #pragma unroll
-            for (int j = 0; j < FD; ++j)
-                d[j] = TURNED ? read_turned(ds + dread[j] + q * 32 * (BD * 2), BD * 2)
-                              : *reinterpret_cast<const bf16x8*>(ds + dread[j] + ((4 * q + g) ^ (r & 7)) * 16);
+        for (int i = 0; i < FC; ++i) c[i] = read_turned(lds + cs * kC + cread[i] + q * 32 * (BC * 2), BC * 2);
 #pragma unroll
-            for (int i = 0; i < FC; ++i) c[i] = read_turned(cs + cread[i] + q * 32 * (BC * 2), BC * 2);
+        for (int j = 0; j < FD; ++j) pin(d[j]);
 #pragma unroll
-            for (int i = 0; i < FC; ++i)
-#pragma unroll
-                for (int j = 0; j < FD; ++j)
-                    acc[i][j] = SWAP ? __builtin_amdgcn_mfma_f32_16x16x32_bf16(d[j], c[i], acc[i][j], 0, 0, 0)
-                                     : __builtin_amdgcn_mfma_f32_16x16x32_bf16(c[i], d[j], acc[i][j], 0, 0, 0);
-        }
-    }
-    if (u.part) {
+        for (int i = 0; i < FC; ++i) pin(c[i]);
+    };
+    constexpr bool kPhases = NW == 8;  // as in linear
+    auto multiply = [&] {
+        __builtin_amdgcn_sched_barrier(0);
+        if (kPhases) __builtin_amdgcn_s_setprio(1);
 #pragma unroll
         for (int i = 0; i < FC; ++i)
 #pragma unroll
-            for (int j = 0; j < FD; ++j) u.part[(i * FD + j) * blockDim.x + threadIdx.x] = acc[i][j];
-        return;
+            for (int j = 0; j < FD; ++j)
+                acc[i][j] = SWAP ? __builtin_amdgcn_mfma_f32_16x16x32_bf16(d[j], c[i], acc[i][j], 0, 0, 0)
+                                 : __builtin_amdgcn_mfma_f32_16x16x32_bf16(c[i], d[j], acc[i][j], 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < FC; ++i)
+#pragma unroll
+            for (int j = 0; j < FD; ++j) pin(acc[i][j]);
+        if (kPhases) __builtin_amdgcn_s_setprio(0);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    // Everything this wavefront has asked of memory and of shared memory.
+    auto wait_all = [] {
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
+        asm volatile("" ::: "memory");
+    };
+
+    // Before the products: step 0 decoded, step 1 loaded.
+    const bool second = kPhases && wave >= NW / 2;
+    int ds = 0, cs = 0;
+    bool more = false;  // a step is loaded and not yet decoded
+    if (steps > 0) {
+        open();
+        load();
+        wait_all();
+        decode(0);
+        more = next_unit < units;
+        if (more) load();
+        wait_copies_and_barrier<0>();
+        if (second) phase_end();
     }
-    // a lane holds 4 neighbours along the first factor's axis
+    for (uint32_t index = blockIdx.x; index < units; index += gridDim.x) {
+        const Unit u = unit_of(cut, index, steps, FC * FD);
 #pragma unroll
-    for (int j = 0; j < FD; ++j)
+        for (int i = 0; i < FC; ++i)
 #pragma unroll
-        for (int i = 0; i < FC; ++i) {
-            const int64_t c = c0 + (wc * FC + i) * 16, d = d0 + (wd * FD + j) * 16;
-            if (SWAP) put4(out, c + r, d + g * 4, acc[i][j]);
-            else put4(out, d + r, c + g * 4, acc[i][j]);
+            for (int j = 0; j < FD; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+        for (int s = u.first; s < u.last; ++s) {
+            // At this point every wavefront is done reading the step before:
+            // the next step's codes and the dense pieces of the one after
+            // take its places.  The next step's dense pieces have arrived
+            // when wait_all returns.
+            if (more) {
+                wait_all();
+                decode(cs ^ 1);
+                more = next_unit < units;
+                if (more) load();
+            }
+            read(ds, cs, 0);
+            wait_shared_and_barrier();
+            multiply();
+            if (kPhases) phase_end();
+            read(ds, cs, 1);
+            wait_shared_and_barrier();
+            multiply();
+            if (kPhases && s + 1 < u.last) phase_end();
+            ds = ds == 2 ? 0 : ds + 1;
+            cs ^= 1;
         }
+        const int64_t c0 = (int64_t)u.i0 * BC, d0 = (int64_t)u.i1 * BD;
+        if (u.part) {
+#pragma unroll
+            for (int i = 0; i < FC; ++i)
+#pragma unroll
+                for (int j = 0; j < FD; ++j) u.part[(i * FD + j) * blockDim.x + threadIdx.x] = acc[i][j];
+        } else {
+            // a lane holds 4 neighbours along the first factor's axis
+#pragma unroll
+            for (int j = 0; j < FD; ++j)
+#pragma unroll
+                for (int i = 0; i < FC; ++i) {
+                    const int64_t cc = c0 + (wc * FC + i) * 16, dd = d0 + (wdn * FD + j) * 16;
+                    if (SWAP) put4(out, cc + r, dd + g * 4, acc[i][j]);
+                    else put4(out, dd + r, cc + g * 4, acc[i][j]);
+                }
+        }
+        if (kPhases && steps > 0) phase_end();
+    }
+    if (kPhases && !second && steps > 0) phase_end();
 }
 
 // A dense operand whose rows are not 16-byte aligned runs of whole pieces:
@@ -793,9 +847,10 @@ hipError_t grad(const Gradient& a, const MxMat& m, const Out& out, void* ws, hip
     const Plan p = grad_plan(m, a.width);
     Cut cut = p.cut;
     cut.part = static_cast<f32x4*>(ws);
-    const dim3 units(cut.full + cut.rest * cut.split), joins(cut.rest * (p.big ? 32 : 16));
-    if (p.big) k_mx_grad<TURNED, FMT, SWAP, 2, 4, 8, 4><<<units, dim3(512), 0, st>>>(a, m, out, cut);
-    else k_mx_grad<TURNED, FMT, SWAP, 2, 2, 4, 4><<<units, dim3(256), 0, st>>>(a, m, out, cut);
+    const uint32_t units = cut.full + cut.rest * cut.split;
+    const dim3 joins(cut.rest * (p.big ? 32 : 16));
+    if (p.big) k_mx_grad<TURNED, FMT, SWAP, 2, 4, 8, 4><<<dim3(std::min(units, 256u)), dim3(512), 0, st>>>(a, m, out, cut);
+    else k_mx_grad<TURNED, FMT, SWAP, 2, 2, 4, 4><<<dim3(std::min(units, 512u)), dim3(256), 0, st>>>(a, m, out, cut);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || cut.split == 1) return e;
     if (p.big) k_mx_join<2, 4, 8, 4, SWAP, false><<<joins, dim3(512), 0, st>>>(cut, out);
@@ -860,15 +915,14 @@ size_t linear_workspace(const MxMat& x, const MxMat& w) {
 size_t grad_workspace(const MxMat& m, int64_t width) { return grad_plan(m, width).bytes; }
 
 hipError_t launch_linear_few(const Dense& x, int64_t tokens, const MxMat& w, const Dense& y, hipStream_t st) {
-    const bool vec = (reinterpret_cast<uintptr_t>(x.p) & 15) == 0 && (tokens == 1 || x.ld % 8 == 0);
-    return few<kFromBf16>(Few{MxMat{}, static_cast<const uint16_t*>(x.p), x.ld, tokens, w.cols, vec}, w,
+    return few<kFromBf16>(Few{MxMat{}, static_cast<const uint16_t*>(x.p), x.ld, tokens, w.cols}, w,
                           result(y, tokens, w.rows, false), st);
 }
 
 hipError_t launch_linear(const MxMat& x, const MxMat& w, const Dense& y, void* ws, hipStream_t st) {
     const Out out = result(y, x.rows, w.rows, false);
     if (x.rows <= Q4MX_FEW_TOKENS) {
-        const Few f{x, nullptr, 0, x.rows, x.cols, false};
+        const Few f{x, nullptr, 0, x.rows, x.cols};
         return x.fmt == Q4MX_FP4 ? few<Q4MX_FP4>(f, w, out, st) : few<Q4MX_FP8>(f, w, out, st);
     }
     return x.fmt == Q4MX_FP4 ? linear<Q4MX_FP4>(x, w, out, ws, st) : linear<Q4MX_FP8>(x, w, out, ws, st);
