@@ -565,7 +565,8 @@ __global__ __launch_bounds__(64 * WC* WD, 2) void k_mx_grad(Gradient a, MxMat m,
     const int64_t cp = m.slices * (FMT == Q4MX_FP4 ? 64 : 128);
     const int crow = tid / LPR, ccol = (tid % LPR) * 8;
     const uint32_t coff = (uint32_t)crow * (uint32_t)cp + (uint32_t)(ccol / 8 * kCode);
-    const uint32_t soff = ((uint32_t)(ccol >> 7) * (uint32_t)m.rows + crow) * 4 + ((ccol >> 5) & 3);
+    const uint32_t soff = ((uint32_t)(ccol >> 7) * (uint32_t)m.rows + crow) * 4;
+    const int sbyte = ((ccol >> 5) & 3) * 8;  // the lane's scale in the slice's word
     const int cf = (crow & 3) | (((crow >> 3) & 1) << 2);
     const int cat = 3 * kD + crow * (BC * 2) + (((tid % LPR) >> 1) ^ cf) * 32 + (tid & 1) * 16;
     uint32_t code[4][kCode / 4];
@@ -585,57 +586,68 @@ __global__ __launch_bounds__(64 * WC* WD, 2) void k_mx_grad(Gradient a, MxMat m,
             ws.open(m.scales + s0 * 4, (m.slices * m.rows - s0) * 4);
             next_left = u.last - u.first;
             next_rows = (int)(depth - k0);
+        } else {
+            // the end: nothing is read, zeros go where nothing is read any more
+            wd.left = wk.left = ws.left = 0;
+            next_left = 0x7FFFFFFF, next_rows = 0;
         }
     };
-    // Loads the stream's next step: codes to registers, the dense operand's
-    // pieces to shared memory.
-    auto load = [&] {
-        const auto b = readable(wk), bs = readable(ws);
-#pragma unroll
-        for (int p = 0; p < 4; ++p) {
+    // Loads the stream's next step in 8 + CD pieces: codes and scales to
+    // registers, the dense operand to shared memory.
+    auto load_piece = [&](int n) {
+        if (n < 8) {
             // past the last row both read as 0 (the scale there is another
             // row's, which may be a NaN's)
-            const uint32_t o = inside(coff + (uint32_t)(16 * p) * (uint32_t)cp, crow + 16 * p, next_rows);
-            if (FMT == Q4MX_FP4) {
-                code[p][0] = __builtin_amdgcn_raw_buffer_load_b32(b, (int)o, 0, 0);
+            const int p = n >> 1;
+            if (n & 1) {
+                scale[p] = __builtin_amdgcn_raw_buffer_load_b32(
+                    readable(ws), (int)inside(soff + 64 * p, crow + 16 * p, next_rows), 0, 0);
             } else {
-                const u32x2 t = __builtin_amdgcn_raw_buffer_load_b64(b, (int)o, 0, 0);
-                code[p][0] = t[0];
-                code[p][kCode / 4 - 1] = t[1];
+                const uint32_t o = inside(coff + (uint32_t)(16 * p) * (uint32_t)cp, crow + 16 * p, next_rows);
+                if (FMT == Q4MX_FP4) {
+                    code[p][0] = __builtin_amdgcn_raw_buffer_load_b32(readable(wk), (int)o, 0, 0);
+                } else {
+                    const u32x2 t = __builtin_amdgcn_raw_buffer_load_b64(readable(wk), (int)o, 0, 0);
+                    code[p][0] = t[0];
+                    code[p][kCode / 4 - 1] = t[1];
+                }
             }
-            scale[p] = __builtin_amdgcn_raw_buffer_load_b8(bs, (int)inside(soff + 64 * p, crow + 16 * p, next_rows), 0, 0);
+        } else if (n < 8 + CD) {
+            const int j = n - 8;
+            copy16(wd.get(), TURNED ? doff[j] : inside(doff[j], dk[j], next_rows), next_at + (j * NW + wave) * 1024);
         }
-        const i32x4 bd = wd.get();
+    };
+    auto load = [&] {
 #pragma unroll
-        for (int j = 0; j < CD; ++j)
-            copy16(bd, TURNED ? doff[j] : inside(doff[j], dk[j], next_rows), next_at + (j * NW + wave) * 1024);
+        for (int n = 0; n < 8 + CD; ++n) load_piece(n);
+    };
+    auto advance = [&] {
         next_at = next_at == base + 2 * kD ? base : next_at + kD;
         if (--next_left == 0) {
             next_unit += gridDim.x;
             open();
-        } else {
+        } else if (next_unit < units) {
             wd.move(TURNED ? 128 * a.ld : 128);
             wk.move(64 * cp);
             ws.move(256);
             next_rows -= 64;
         }
     };
-    // Decodes the step that was loaded last into the ring's buffer `slot`.
+    // Decodes the step that was loaded last into the ring's buffer `slot`, in 8
+    // pieces of 4 values a lane.
+    uint32_t half[2];
+    auto decode_piece = [&](int slot, int n) {
+        const int p = n >> 1;
+        const float f = scale_of((scale[p] >> sbyte) & 0xFF);
+        const uint32_t w = FMT == Q4MX_FP4 ? code[p][0] : code[p][(n & 1) * (kCode / 4 - 1)];
+        const int k = FMT == Q4MX_FP4 ? 2 * (n & 1) : 0;
+        const uint32_t lo = bf16_pair_of(w, f, FMT, k), hi = bf16_pair_of(w, f, FMT, k + 1);
+        if ((n & 1) == 0) half[0] = lo, half[1] = hi;
+        else *reinterpret_cast<uint4*>(lds + cat + slot * kC + p * 16 * (BC * 2)) = make_uint4(half[0], half[1], lo, hi);
+    };
     auto decode = [&](int slot) {
-        char* const at = lds + cat + slot * kC;
 #pragma unroll
-        for (int p = 0; p < 4; ++p) {
-            const float f = scale_of(scale[p]);
-            uint4 v;
-            if (FMT == Q4MX_FP4)
-                v = make_uint4(bf16_pair_of(code[p][0], f, FMT, 0), bf16_pair_of(code[p][0], f, FMT, 1),
-                               bf16_pair_of(code[p][0], f, FMT, 2), bf16_pair_of(code[p][0], f, FMT, 3));
-            else
-                v = make_uint4(bf16_pair_of(code[p][0], f, FMT, 0), bf16_pair_of(code[p][0], f, FMT, 1),
-                               bf16_pair_of(code[p][kCode / 4 - 1], f, FMT, 0),
-                               bf16_pair_of(code[p][kCode / 4 - 1], f, FMT, 1));
-            *reinterpret_cast<uint4*>(at + p * 16 * (BC * 2)) = v;
-        }
+        for (int n = 0; n < 8; ++n) decode_piece(slot, n);
     };
 
     // fragments: lane (r, g) reads rows k = 32 q + 8 g + r / 4 (+ 4) at columns 4 (r % 4)
@@ -663,15 +675,29 @@ __global__ __launch_bounds__(64 * WC* WD, 2) void k_mx_grad(Gradient a, MxMat m,
         for (int i = 0; i < FC; ++i) pin(c[i]);
     };
     constexpr bool kPhases = NW == 8;  // as in linear
-    auto multiply = [&] {
+    // Half a step's products.  With `slot` >= 0 the next step is decoded and the
+    // one after loaded in between, a piece behind each product or two: a
+    // product occupies the matrix core for 16 cycles and the issue for 4, and
+    // the piece's few instructions fit into the rest.
+    auto multiply = [&](int slot) {
+        constexpr int kPieces = 16 + CD, kPer = (kPieces + FC * FD - 1) / (FC * FD);
         __builtin_amdgcn_sched_barrier(0);
         if (kPhases) __builtin_amdgcn_s_setprio(1);
 #pragma unroll
         for (int i = 0; i < FC; ++i)
 #pragma unroll
-            for (int j = 0; j < FD; ++j)
+            for (int j = 0; j < FD; ++j) {
                 acc[i][j] = SWAP ? __builtin_amdgcn_mfma_f32_16x16x32_bf16(d[j], c[i], acc[i][j], 0, 0, 0)
                                  : __builtin_amdgcn_mfma_f32_16x16x32_bf16(c[i], d[j], acc[i][j], 0, 0, 0);
+                if (slot >= 0) {
+#pragma unroll
+                    for (int n = (i * FD + j) * kPer; n < (i * FD + j + 1) * kPer; ++n) {
+                        if (n < 8) decode_piece(slot, n);
+                        else if (n < kPieces) load_piece(n - 8);
+                    }
+                    if ((i * FD + j) * kPer < kPieces) __builtin_amdgcn_sched_barrier(0);
+                }
+            }
 #pragma unroll
         for (int i = 0; i < FC; ++i)
 #pragma unroll
@@ -689,14 +715,14 @@ __global__ __launch_bounds__(64 * WC* WD, 2) void k_mx_grad(Gradient a, MxMat m,
     // Before the products: step 0 decoded, step 1 loaded.
     const bool second = kPhases && wave >= NW / 2;
     int ds = 0, cs = 0;
-    bool more = false;  // a step is loaded and not yet decoded
     if (steps > 0) {
         open();
         load();
+        advance();
         wait_all();
         decode(0);
-        more = next_unit < units;
-        if (more) load();
+        load();
+        advance();
         wait_copies_and_barrier<0>();
         if (second) phase_end();
     }
@@ -707,23 +733,19 @@ __global__ __launch_bounds__(64 * WC* WD, 2) void k_mx_grad(Gradient a, MxMat m,
 #pragma unroll
             for (int j = 0; j < FD; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
         for (int s = u.first; s < u.last; ++s) {
-            // At this point every wavefront is done reading the step before:
-            // the next step's codes and the dense pieces of the one after
-            // take its places.  The next step's dense pieces have arrived
-            // when wait_all returns.
-            if (more) {
-                wait_all();
-                decode(cs ^ 1);
-                more = next_unit < units;
-                if (more) load();
-            }
+            // At the end of the first reads everything of the next step has
+            // arrived here, and every wavefront is done reading the step
+            // before: the next step's codes and the dense pieces of the one
+            // after take its places.
             read(ds, cs, 0);
-            wait_shared_and_barrier();
-            multiply();
+            wait_all();
+            phase_end();
+            multiply(cs ^ 1);
+            advance();
             if (kPhases) phase_end();
             read(ds, cs, 1);
             wait_shared_and_barrier();
-            multiply();
+            multiply(-1);
             if (kPhases && s + 1 < u.last) phase_end();
             ds = ds == 2 ? 0 : ds + 1;
             cs ^= 1;
@@ -748,6 +770,7 @@ __global__ __launch_bounds__(64 * WC* WD, 2) void k_mx_grad(Gradient a, MxMat m,
         if (kPhases && steps > 0) phase_end();
     }
     if (kPhases && !second && steps > 0) phase_end();
+    wait_all();  // the stream's last copies, of nothing, into this work-group's shared memory
 }
 
 // A dense operand whose rows are not 16-byte aligned runs of whole pieces:
