@@ -14,7 +14,7 @@ typedef short s16x2 __attribute__((ext_vector_type(2)));
 // 2^(e-127): the FP32 with that biased exponent, subnormal for e = 0.  For e
 // = 255 the bits are those of an infinity; the conversions read the exponent
 // field alone and give NaN.
-__device__ __forceinline__ float scale_of(uint32_t e) { return __uint_as_float(e == 0 ? 0x00400000u : e << 23); }
+__device__ __forceinline__ float scale_of(uint32_t e) { return __uint_as_float(max(e << 23, 0x00400000u)); }
 
 // The scale byte of a block whose largest magnitude has the bits `top`: the
 // smallest e >= 0 with |x| 2^(127-e) <= 6 = 1.5 2^2 (E2M1) or 448 = 1.75 2^8

@@ -21,7 +21,7 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 #define Q4_LDS __attribute__((address_space(3)))
@@ -476,8 +476,10 @@ template <int XF, int NW> __global__ __launch_bounds__(64 * NW) void k_mx_linear
 // output for wgrad), c over the code matrix's columns; the sum runs over the
 // code matrix's rows k (outputs for dgrad, tokens for wgrad), 64 per step.
 //
-// Codes are read 8 to a lane, decoded to BF16 with their block's scale and
-// written to shared memory as [k][c]; the transposing reads
+// Codes are read a block of 32 to a lane, decoded to BF16 with the block's
+// scale and written to shared memory as [k][c], each lane's four 16-byte
+// pieces in an order that differs between neighbours, so that they lie in
+// different banks; the transposing reads
 // (ds_read_b64_tr_b16) turn them into fragments, 16 columns x 8 k per lane
 // group.  The dense operand is copied straight to shared memory: as [d][k]
 // where k is its row's axis (dgrad), as [k][d] where it is not (TURNED:
@@ -533,8 +535,7 @@ __global__ __launch_bounds__(64 * WC* WD, 2) void k_mx_grad(Gradient a, MxMat m,
     constexpr int NW = WC * WD, BC = WC * FC * 16, BD = WD * FD * 16;
     constexpr int kD = BD * 128, kC = BC * 128;  // bytes of a step
     constexpr int CD = kD / 1024 / NW;
-    constexpr int LPR = BC / 8;  // lanes of a row of codes
-    static_assert(NW * 64 / LPR == 16 && kD % (1024 * NW) == 0, "tile");
+    static_assert(NW * 64 == 64 * (BC / 32) && kD % (1024 * NW) == 0, "tile");
     __shared__ __attribute__((aligned(1024))) char lds[3 * kD + 2 * kC];
 
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -545,7 +546,7 @@ __global__ __launch_bounds__(64 * WC* WD, 2) void k_mx_grad(Gradient a, MxMat m,
 
     // dense: this lane's pieces of the step's copies
     uint32_t doff[CD];
-    int dk[CD];  // first k of the piece within the step (not TURNED)
+    int dk = 0;  // first k of the pieces within the step (not TURNED)
 #pragma unroll
     for (int j = 0; j < CD; ++j) {
         if (TURNED) {
@@ -553,24 +554,29 @@ __global__ __launch_bounds__(64 * WC* WD, 2) void k_mx_grad(Gradient a, MxMat m,
             const int k = (j * NW + wave) * (64 / PPR) + lane / PPR, piece = lane % PPR;
             const int f = (k & 3) | (((k >> 3) & 1) << 2);
             doff[j] = (uint32_t)k * (uint32_t)(a.ld * 2) + (uint32_t)(((piece >> 1) ^ f) * 32 + (piece & 1) * 16);
-            dk[j] = 0;
         } else {
-            const int d = (j * NW + wave) * 8 + lane / 8, piece = (lane & 7) ^ (lane >> 3);
-            doff[j] = (uint32_t)d * (uint32_t)(a.ld * 2) + piece * 16;
-            dk[j] = piece * 8;
+            const int row = (j * NW + wave) * 8 + lane / 8, piece = (lane & 7) ^ (lane >> 3);
+            doff[j] = (uint32_t)row * (uint32_t)(a.ld * 2) + piece * 16;
+            dk = piece * 8;
         }
     }
-    // codes: rows crow + 16 p, columns ccol .. ccol + 7 of the step
-    constexpr int kCode = FMT == Q4MX_FP4 ? 4 : 8;  // bytes of 8 codes
-    const int64_t cp = m.slices * (FMT == Q4MX_FP4 ? 64 : 128);
-    const int crow = tid / LPR, ccol = (tid % LPR) * 8;
-    const uint32_t coff = (uint32_t)crow * (uint32_t)cp + (uint32_t)(ccol / 8 * kCode);
-    const uint32_t soff = ((uint32_t)(ccol >> 7) * (uint32_t)m.rows + crow) * 4;
-    const int sbyte = ((ccol >> 5) & 3) * 8;  // the lane's scale in the slice's word
-    const int cf = (crow & 3) | (((crow >> 3) & 1) << 2);
-    const int cat = 3 * kD + crow * (BC * 2) + (((tid % LPR) >> 1) ^ cf) * 32 + (tid & 1) * 16;
-    uint32_t code[4][kCode / 4];
-    uint32_t scale[4];
+
+    // codes: block cblk of row crow of the step
+    constexpr int kCode = FMT == Q4MX_FP4 ? 16 : 32;  // bytes of a block
+    const int64_t cp = m.slices * (kCode * 4);
+    const int crow = tid / (BC / 32), cblk = tid % (BC / 32);
+    const uint32_t coff = (uint32_t)crow * (uint32_t)cp + cblk * kCode;
+    const uint32_t soff = ((uint32_t)(cblk >> 2) * (uint32_t)m.rows + crow) * 4;
+    const int turn = (lane >> 1) & 3;  // the lane's first piece
+    const uint32_t turn1 = turn & 1 ? ~0u : 0u, turn2 = turn & 2 ? ~0u : 0u;
+    int cat[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const int piece = (q + turn) & 3;
+        cat[q] = 3 * kD + crow * (BC * 2) + ((cblk * 2 + (piece >> 1)) ^ ((crow & 3) | (((crow >> 3) & 1) << 2))) * 32 +
+                 (piece & 1) * 16;
+    }
+    uint32_t code[kCode / 4], scale = 0;
     // the stream, two steps ahead of the products
     uint32_t next_unit = blockIdx.x, next_at = base;
     int next_left = 0, next_rows = 0;  // steps of the unit, rows of the sum
@@ -581,7 +587,7 @@ __global__ __launch_bounds__(64 * WC* WD, 2) void k_mx_grad(Gradient a, MxMat m,
             const int64_t c0 = (int64_t)u.i0 * BC, d0 = (int64_t)u.i1 * BD, k0 = (int64_t)u.first * 64;
             if (TURNED) wd.open(a.p + k0 * a.ld + d0, ((depth - 1 - k0) * a.ld + a.span - d0) * 2);
             else wd.open(a.p + d0 * a.ld + k0, ((a.width - 1 - d0) * a.ld + a.span - k0) * 2);
-            wk.open(m.codes + k0 * cp + c0 / 8 * kCode, (depth - k0) * cp - c0 / 8 * kCode);
+            wk.open(m.codes + k0 * cp + c0 / 32 * kCode, (depth - k0) * cp - c0 / 32 * kCode);
             const int64_t s0 = (c0 / 128) * m.rows + k0;
             ws.open(m.scales + s0 * 4, (m.slices * m.rows - s0) * 4);
             next_left = u.last - u.first;
@@ -592,34 +598,31 @@ __global__ __launch_bounds__(64 * WC* WD, 2) void k_mx_grad(Gradient a, MxMat m,
             next_left = 0x7FFFFFFF, next_rows = 0;
         }
     };
-    // Loads the stream's next step in 8 + CD pieces: codes and scales to
-    // registers, the dense operand to shared memory.
+    // Loads the stream's next step in 2 + CD pieces: a block's codes and scale
+    // to registers, the dense operand to shared memory.
+    constexpr int kLoads = 2 + CD;
     auto load_piece = [&](int n) {
-        if (n < 8) {
-            // past the last row both read as 0 (the scale there is another
-            // row's, which may be a NaN's)
-            const int p = n >> 1;
-            if (n & 1) {
-                scale[p] = __builtin_amdgcn_raw_buffer_load_b32(
-                    readable(ws), (int)inside(soff + 64 * p, crow + 16 * p, next_rows), 0, 0);
-            } else {
-                const uint32_t o = inside(coff + (uint32_t)(16 * p) * (uint32_t)cp, crow + 16 * p, next_rows);
-                if (FMT == Q4MX_FP4) {
-                    code[p][0] = __builtin_amdgcn_raw_buffer_load_b32(readable(wk), (int)o, 0, 0);
-                } else {
-                    const u32x2 t = __builtin_amdgcn_raw_buffer_load_b64(readable(wk), (int)o, 0, 0);
-                    code[p][0] = t[0];
-                    code[p][kCode / 4 - 1] = t[1];
-                }
+        if (n == 0) {
+            const auto b = readable(wk);
+#pragma unroll
+            for (int q = 0; q < kCode / 16; ++q) {
+                const u32x4 t = __builtin_amdgcn_raw_buffer_load_b128(b, (int)coff + 16 * q, 0, 0);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) code[4 * q + i] = t[i];
             }
-        } else if (n < 8 + CD) {
-            const int j = n - 8;
-            copy16(wd.get(), TURNED ? doff[j] : inside(doff[j], dk[j], next_rows), next_at + (j * NW + wave) * 1024);
+        } else if (n == 1) {
+            // past the last row codes read as 0, and so must the scale (what
+            // lies there is another slice's, which may be a NaN's); a word
+            // holds the slice's four
+            scale = __builtin_amdgcn_raw_buffer_load_b32(readable(ws), (int)inside(soff, crow, next_rows), 0, 0);
+        } else {
+            const int j = n - 2;
+            copy16(wd.get(), TURNED ? doff[j] : inside(doff[j], dk, next_rows), next_at + (j * NW + wave) * 1024);
         }
     };
     auto load = [&] {
 #pragma unroll
-        for (int n = 0; n < 8 + CD; ++n) load_piece(n);
+        for (int n = 0; n < kLoads; ++n) load_piece(n);
     };
     auto advance = [&] {
         next_at = next_at == base + 2 * kD ? base : next_at + kD;
@@ -633,21 +636,32 @@ __global__ __launch_bounds__(64 * WC* WD, 2) void k_mx_grad(Gradient a, MxMat m,
             next_rows -= 64;
         }
     };
-    // Decodes the step that was loaded last into the ring's buffer `slot`, in 8
-    // pieces of 4 values a lane.
+    // Decodes the step that was loaded last into the ring's buffer `slot`: 2
+    // pieces turn the lane's four groups of 8 codes to its order, 8 convert
+    // half a group each.
+    constexpr int kDecodes = 10, kGroup = kCode / 16;  // words of a group
     uint32_t half[2];
     auto decode_piece = [&](int slot, int n) {
-        const int p = n >> 1;
-        const float f = scale_of((scale[p] >> sbyte) & 0xFF);
-        const uint32_t w = FMT == Q4MX_FP4 ? code[p][0] : code[p][(n & 1) * (kCode / 4 - 1)];
-        const int k = FMT == Q4MX_FP4 ? 2 * (n & 1) : 0;
-        const uint32_t lo = bf16_pair_of(w, f, FMT, k), hi = bf16_pair_of(w, f, FMT, k + 1);
-        if ((n & 1) == 0) half[0] = lo, half[1] = hi;
-        else *reinterpret_cast<uint4*>(lds + cat + slot * kC + p * 16 * (BC * 2)) = make_uint4(half[0], half[1], lo, hi);
+        if (n < 2) {
+            const uint32_t by = n == 0 ? turn1 : turn2;
+            uint32_t t[kCode / 4];
+#pragma unroll
+            for (int i = 0; i < kCode / 4; ++i) t[i] = code[i];
+#pragma unroll
+            for (int i = 0; i < kCode / 4; ++i) code[i] = (t[(i + (n + 1) * kGroup) % (kCode / 4)] & by) | (t[i] & ~by);
+            return;
+        }
+        const int q = (n - 2) >> 1, h = n & 1;
+        const float s = scale_of((scale >> ((cblk & 3) * 8)) & 0xFF);
+        const uint32_t w = FMT == Q4MX_FP4 ? code[q] : code[q * kGroup + h * (kGroup - 1)];
+        const int k = FMT == Q4MX_FP4 ? 2 * h : 0;
+        const uint32_t lo = bf16_pair_of(w, s, FMT, k), hi = bf16_pair_of(w, s, FMT, k + 1);
+        if (h == 0) half[0] = lo, half[1] = hi;
+        else *reinterpret_cast<uint4*>(lds + cat[q] + slot * kC) = make_uint4(half[0], half[1], lo, hi);
     };
     auto decode = [&](int slot) {
 #pragma unroll
-        for (int n = 0; n < 8; ++n) decode_piece(slot, n);
+        for (int n = 0; n < kDecodes; ++n) decode_piece(slot, n);
     };
 
     // fragments: lane (r, g) reads rows k = 32 q + 8 g + r / 4 (+ 4) at columns 4 (r % 4)
@@ -676,11 +690,12 @@ __global__ __launch_bounds__(64 * WC* WD, 2) void k_mx_grad(Gradient a, MxMat m,
     };
     constexpr bool kPhases = NW == 8;  // as in linear
     // Half a step's products.  With `slot` >= 0 the next step is decoded and the
-    // one after loaded in between, a piece behind each product or two: a
+    // one after loaded in between, a piece behind every product or two: a
     // product occupies the matrix core for 16 cycles and the issue for 4, and
     // the piece's few instructions fit into the rest.
     auto multiply = [&](int slot) {
-        constexpr int kPieces = 16 + CD, kPer = (kPieces + FC * FD - 1) / (FC * FD);
+        constexpr int kPieces = kDecodes + kLoads, kEvery = kPieces * 2 <= FC * FD ? 2 : 1;
+        static_assert(kPieces <= FC * FD, "pieces");
         __builtin_amdgcn_sched_barrier(0);
         if (kPhases) __builtin_amdgcn_s_setprio(1);
 #pragma unroll
@@ -689,13 +704,12 @@ __global__ __launch_bounds__(64 * WC* WD, 2) void k_mx_grad(Gradient a, MxMat m,
             for (int j = 0; j < FD; ++j) {
                 acc[i][j] = SWAP ? __builtin_amdgcn_mfma_f32_16x16x32_bf16(d[j], c[i], acc[i][j], 0, 0, 0)
                                  : __builtin_amdgcn_mfma_f32_16x16x32_bf16(c[i], d[j], acc[i][j], 0, 0, 0);
-                if (slot >= 0) {
-#pragma unroll
-                    for (int n = (i * FD + j) * kPer; n < (i * FD + j + 1) * kPer; ++n) {
-                        if (n < 8) decode_piece(slot, n);
-                        else if (n < kPieces) load_piece(n - 8);
-                    }
-                    if ((i * FD + j) * kPer < kPieces) __builtin_amdgcn_sched_barrier(0);
+                const int n = (i * FD + j) / kEvery;
+                if (slot >= 0 && (i * FD + j) % kEvery == 0 && n < kPieces) {
+                    __builtin_amdgcn_sched_barrier(0);
+                    if (n < kDecodes) decode_piece(slot, n);
+                    else load_piece(n - kDecodes);
+                    __builtin_amdgcn_sched_barrier(0);
                 }
             }
 #pragma unroll
@@ -741,8 +755,8 @@ __global__ __launch_bounds__(64 * WC* WD, 2) void k_mx_grad(Gradient a, MxMat m,
             wait_all();
             phase_end();
             multiply(cs ^ 1);
-            advance();
             if (kPhases) phase_end();
+            advance();
             read(ds, cs, 1);
             wait_shared_and_barrier();
             multiply(-1);
