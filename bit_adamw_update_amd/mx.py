@@ -42,7 +42,10 @@ class MXMatrix:
         if format not in FORMATS:
             raise ValueError(f"unknown format {format!r}; expected one of {sorted(FORMATS)}")
         code = FORMATS[format]
-        ncodes, nscales = api.q4mx_matrix_bytes(code, rows, cols)   # refuses sizes out of range
+        padded = (cols + 127) // 128 * 128
+        if not (0 <= rows < 1 << 31 and 0 <= cols < 1 << 31 and rows * padded < 1 << 34):
+            api.q4mx_matrix_bytes(code, rows, cols)   # refuses them, with the reason
+        ncodes, nscales = rows * padded // (2 if code == api.MX_FP4 else 1), rows * padded // 32
         self.rows, self.cols, self.format = rows, cols, format
         self._codes, self._scales, self._buf = codes, scales, None
         if codes is None and scales is None:
