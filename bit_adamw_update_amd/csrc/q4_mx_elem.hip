@@ -13,32 +13,29 @@ namespace q4 {
 namespace {
 
 // ---- row-wise tiles ---------------------------------------------------------
-// A work-group takes 32 rows x 128 columns: lane s of a 16-lane row on columns
-// 8s .. 8s+7, so a block of 32 is a quad of lanes, and a 128-column slice of a
-// row is read as whole 256-byte (BF16) or 512-byte (FP32) runs.  32 rows of a
-// slice share one 128-byte line of scales, which one work-group writes whole.
+// A work-group takes 32 rows x 128 columns in two passes: lane s of a 16-lane
+// row on columns 8s .. 8s+7, so a block of 32 is a quad of lanes, and a
+// 128-column slice of a row is read as whole 256-byte (BF16) or 512-byte
+// (FP32) runs; the 32 rows' scales of a slice are one 128-byte line.  The
+// passes follow each other: both rows loaded first cost registers and are
+// slower (swiglu 8192 x 5632 forward, backward and restore: 187 us against
+// 172; 16 rows to a work-group: 177).
 constexpr int kTileRows = 32;
 
 struct Lane {
     int64_t row;
-    int64_t col;   // first of the lane's 8 columns
-    int64_t slice;
+    int64_t col;  // first of the lane's 8 columns
 };
 
-__device__ __forceinline__ Lane lane_of(int64_t tile, int64_t slices, int pass) {
-    Lane l;
-    const int64_t rt = tile / slices;
-    l.slice = tile - rt * slices;
-    l.row = rt * kTileRows + pass * 16 + (threadIdx.x >> 4);
-    l.col = l.slice * 128 + (threadIdx.x & 15) * 8;
-    return l;
+__device__ __forceinline__ Lane lane_of(int64_t slices, int pass) {
+    const uint32_t rt = blockIdx.x / (uint32_t)slices, slice = blockIdx.x - rt * (uint32_t)slices;
+    return Lane{(int64_t)rt * kTileRows + pass * 16 + (threadIdx.x >> 4), (int64_t)slice * 128 + (threadIdx.x & 15) * 8};
 }
 
-template <bool BF16>
-__global__ __launch_bounds__(256) void k_mx_quantize(const void* src, int64_t ld, MxMat out) {
+template <bool BF16> __global__ __launch_bounds__(256) void k_mx_quantize(const void* src, int64_t ld, MxMat out) {
 #pragma unroll
     for (int pass = 0; pass < 2; ++pass) {
-        const Lane l = lane_of(blockIdx.x, out.slices, pass);
+        const Lane l = lane_of(out.slices, pass);
         if (l.row >= out.rows) return;
         float v[8];
         load8<BF16>(src, l.row * ld + l.col, out.cols - l.col, v);
@@ -55,8 +52,9 @@ template <bool BF16, int FMT>
 __global__ __launch_bounds__(256) void k_mx_quantize_t(const void* src, int64_t ld, MxMat out, int64_t ctiles) {
     constexpr int kBytes = FMT == Q4MX_FP4 ? 16 : 32;  // codes of a block
     __shared__ __attribute__((aligned(16))) uint8_t lds[64][4 * kBytes + 16];
-    __shared__ uint8_t lds_scale[64][4];
-    const int64_t slice = blockIdx.x / ctiles, c0 = (blockIdx.x - slice * ctiles) * 64;
+    __shared__ __attribute__((aligned(4))) uint8_t lds_scale[64][4];
+    const uint32_t st = blockIdx.x / (uint32_t)ctiles;
+    const int64_t slice = st, c0 = (int64_t)(blockIdx.x - st * (uint32_t)ctiles) * 64;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t r0 = slice * 128 + wave * 32, c = c0 + lane;
     float v[32];
@@ -90,11 +88,10 @@ __global__ __launch_bounds__(256) void k_mx_quantize_t(const void* src, int64_t 
             *reinterpret_cast<const uint32_t*>(lds_scale[threadIdx.x]);
 }
 
-template <bool BF16>
-__global__ __launch_bounds__(256) void k_mx_dequantize(MxMat a, void* dst, int64_t ld) {
+template <bool BF16> __global__ __launch_bounds__(256) void k_mx_dequantize(MxMat a, void* dst, int64_t ld) {
 #pragma unroll
     for (int pass = 0; pass < 2; ++pass) {
-        const Lane l = lane_of(blockIdx.x, a.slices, pass);
+        const Lane l = lane_of(a.slices, pass);
         if (l.row >= a.rows || l.col >= a.cols) return;
         float v[8];
         load_mx8(a, l.row, l.col, v);
@@ -149,7 +146,7 @@ __global__ __launch_bounds__(256) void k_act_forward(const void* x, int64_t ldx,
                                                       MxMat ymx, MxMat kx, MxMat ku) {
 #pragma unroll
     for (int pass = 0; pass < 2; ++pass) {
-        const Lane l = lane_of(blockIdx.x, slices, pass);
+        const Lane l = lane_of(slices, pass);
         if (l.row >= rows) return;
         const int64_t left = cols - l.col;
         float v[8], u[8], r[8];
@@ -173,14 +170,13 @@ __global__ __launch_bounds__(256) void k_act_backward(MxMat kx, MxMat ku, const 
                                                        int64_t lddx, void* dup, int64_t lddup) {
 #pragma unroll
     for (int pass = 0; pass < 2; ++pass) {
-        const Lane l = lane_of(blockIdx.x, kx.slices, pass);
-        if (l.row >= kx.rows || l.col >= kx.cols) return;
+        const Lane l = lane_of(kx.slices, pass);
         const int64_t left = kx.cols - l.col;
-        float g[8], v[8], u[8];
+        if (l.row >= kx.rows || left <= 0) return;
+        float g[8], v[8], u[8], a[8], b[8];
         load8<true>(dy, l.row * lddy + l.col, left, g);
         load_mx8(kx, l.row, l.col, v);
         if (ACT == Q4MX_SWIGLU) load_mx8(ku, l.row, l.col, u);
-        float a[8], b[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const ActValue t = act_value<ACT>(v[i]);

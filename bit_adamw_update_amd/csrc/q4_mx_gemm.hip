@@ -72,8 +72,8 @@ __device__ __forceinline__ Unit unit_of(const Cut& c, uint32_t index, int steps,
     }
     const uint32_t run = id / c.rest, tile = id - run * c.rest;
     tile_at(c, c.full + tile, u.i0, u.i1);
-    u.first = (int)((int64_t)steps * run / c.split);
-    u.last = (int)((int64_t)steps * (run + 1) / c.split);
+    u.first = (int)((uint32_t)steps * run / c.split);  // steps < 2^21, at most 32 runs
+    u.last = (int)((uint32_t)steps * (run + 1) / c.split);
     u.part = c.part + ((int64_t)tile * c.split + run) * frags * blockDim.x;
     return u;
 }
@@ -789,20 +789,27 @@ __global__ __launch_bounds__(64 * WC* WD, 2) void k_mx_grad(Gradient a, MxMat m,
 }
 
 // A dense operand whose rows are not 16-byte aligned runs of whole pieces:
-// copied first into rows of a multiple of 8 elements, 0 past the last.
-__global__ __launch_bounds__(256) void k_align_rows(const uint16_t* src, int64_t ld, int64_t cols, uint4* dst,
-                                                     int64_t pieces, int64_t total) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= total) return;
-    const int64_t row = i / pieces, c = (i - row * pieces) * 8;
-    const uint16_t* p = src + row * ld + c;
-    uint32_t v[4];
+// copied first into rows of a multiple of 8 elements, 0 past the last.  32
+// lanes to a row.
+__global__ __launch_bounds__(256) void k_align_rows(const uint16_t* src, int64_t ld, int64_t rows, int64_t cols,
+                                                     uint4* dst, int64_t pieces) {
+    const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (row >= rows) return;
+    for (int64_t i = threadIdx.x & 31; i < pieces; i += 32) {
+        const uint16_t* p = src + row * ld + i * 8;
+        if (i * 8 + 8 <= cols) {
+            const u32x4_any v = *reinterpret_cast<const u32x4_any*>(p);
+            dst[row * pieces + i] = make_uint4(v[0], v[1], v[2], v[3]);
+            continue;
+        }
+        uint32_t v[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const uint32_t lo = c + 2 * k < cols ? p[2 * k] : 0, hi = c + 2 * k + 1 < cols ? p[2 * k + 1] : 0;
-        v[k] = lo | (hi << 16);
+        for (int k = 0; k < 4; ++k) {
+            const int64_t c = i * 8 + 2 * k;
+            v[k] = (c < cols ? p[2 * k] : 0u) | ((c + 1 < cols ? (uint32_t)p[2 * k + 1] : 0u) << 16);
+        }
+        dst[row * pieces + i] = make_uint4(v[0], v[1], v[2], v[3]);
     }
-    dst[i] = make_uint4(v[0], v[1], v[2], v[3]);
 }
 
 // Joins the runs of split tiles: the sums of one fragment (16 x 16 results of
@@ -919,10 +926,10 @@ template <int XF> hipError_t linear(const MxMat& x, const MxMat& w, const Out& y
 // dy as the products read it: in place, or through the workspace.
 hipError_t aligned_gradient(const Dense& dy, int64_t rows, int64_t cols, void* copy, Gradient* g, hipStream_t st) {
     *g = Gradient{static_cast<const uint16_t*>(dy.p), dy.ld, cols, 0};
-    const int64_t pieces = tiles(cols, 8), total = rows * pieces;
-    if (!dense_needs_copy(dy, rows, cols) || total == 0) return hipSuccess;
-    k_align_rows<<<dim3((unsigned)tiles(total, 256)), dim3(256), 0, st>>>(g->p, dy.ld, cols, static_cast<uint4*>(copy),
-                                                                        pieces, total);
+    const int64_t pieces = tiles(cols, 8);
+    if (!dense_needs_copy(dy, rows, cols) || rows * pieces == 0) return hipSuccess;
+    k_align_rows<<<dim3((unsigned)tiles(rows, 8)), dim3(256), 0, st>>>(g->p, dy.ld, rows, cols,
+                                                                     static_cast<uint4*>(copy), pieces);
     *g = Gradient{static_cast<const uint16_t*>(copy), pieces * 8, pieces * 8, 0};
     return hipGetLastError();
 }

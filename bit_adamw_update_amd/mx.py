@@ -166,6 +166,8 @@ _HERE = _Here()
 def _on(device, stream):
     """The device and stream of a call as a context."""
     if stream is not None:
+        if stream.device != device:
+            raise ValueError(f"the stream is on {stream.device}, the operands on {device}")
         return torch.cuda.stream(stream)   # makes the stream's device current
     if torch._C._cuda_getDevice() == device.index:
         return _HERE

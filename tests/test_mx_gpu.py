@@ -332,6 +332,102 @@ def test_non_finite_values_stay_in_their_rows_and_columns(tokens):
     assert torch.equal(torch.isinf(dw[2, 32:]), ref.values_of(xq)[0, 32:] != 0)
 
 
+@pytest.mark.parametrize("tokens", [16, 40, 70, 300])
+def test_a_nan_block_of_another_slice_stays_there(tokens):
+    """Scales of a 128-column slice are followed by the next slice's: steps
+    that reach past the last row must not take a NaN from there."""
+    cin, cout = 203, 150
+    x = _values(tokens, cin, 61, torch.bfloat16)
+    w0 = _values(cout, cin, 62, scale=0.02)
+    dy = _values(tokens, cout, 63, torch.bfloat16) + 1
+    x[:min(tokens, 60), 130] = math.nan
+    w0[:60, 130] = math.nan
+    xq, w = _matrix(x, "fp8"), _matrix(w0, "fp4")
+    block = (torch.arange(cin) >= 128) & (torch.arange(cin) < 160)
+    dw = torch.isnan(mx.linear_wgrad(dy.to(DEV), xq)).cpu()
+    assert torch.equal(dw, block.expand(cout, cin))
+    dx = torch.isnan(mx.linear_dgrad(dy.to(DEV), w)).cpu()
+    assert torch.equal(dx, block.expand(tokens, cin))
+    y = torch.isnan(mx.linear(xq, w)).cpu()
+    rows, cols = torch.arange(tokens) < 60, torch.arange(cout) < 60
+    assert torch.equal(y, rows[:, None] | cols[None, :])
+
+
+MANY = [(4200, 4100, 200), (70001, 129, 130)]   # more tiles of 256 than compute units; of 128 than twice as many
+
+
+def _some_rows(n):
+    """Rows at both ends and around tile borders."""
+    pick = {0, 1, 127, 128, 255, 256, 257, 1024, n // 2, n - 257, n - 256, n - 2, n - 1}
+    return torch.tensor(sorted(r for r in pick if 0 <= r < n))
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "fp4"])
+@pytest.mark.parametrize("rows,cols,depth", MANY)
+def test_linear_of_many_tiles(rows, cols, depth, fmt):
+    """A work-group forms several tiles in a row; FP32 results take another
+    way out than BF16 ones."""
+    _say("linear", rows, cols, depth, fmt)
+    x = _values(rows, depth, 64, torch.bfloat16)
+    xq = _matrix(x, fmt)
+    w = _matrix(_values(cols, depth, 65, scale=0.02), "fp4")
+    pick = _some_rows(rows)
+    xv, wv = ref.values_of(mx.MXMatrix(rows, depth, fmt, codes=xq.codes, scales=xq.scales))[pick], ref.values_of(w)
+    cut = 0.0 if fmt == "fp4" else _cut_off(xv, wv)
+    for dtype in (torch.bfloat16, torch.float32):
+        y = mx.linear(xq, w, dtype=dtype)
+        _check_product(y[pick.to(DEV)], xv @ wv.t(), xv.abs() @ wv.abs().t(), depth, dtype, cut)
+        assert bool(torch.isfinite(y).all())
+
+
+@pytest.mark.parametrize("rows,cols,depth", MANY)
+def test_gradients_of_many_tiles(rows, cols, depth):
+    _say("gradients", rows, cols, depth)
+    pick = _some_rows(rows)
+    # dgrad: rows tokens, cols inputs
+    dy = _values(rows, depth, 66, torch.bfloat16, 1e-3)
+    w = _matrix(_values(depth, cols, 67, scale=0.02), "fp4")
+    d, wv = dy[pick].double(), ref.values_of(w)
+    dx = mx.linear_dgrad(dy.to(DEV), w)
+    _check_product(dx[pick.to(DEV)], d @ wv, d.abs() @ wv.abs(), depth, torch.bfloat16)
+    assert bool(torch.isfinite(dx).all())
+    # wgrad: rows outputs, cols inputs
+    dy = _values(depth, rows, 68, torch.bfloat16, 1e-3)
+    xq = _matrix(_values(depth, cols, 69, torch.bfloat16), "fp8")
+    d, xv = dy[:, pick].double(), ref.values_of(xq)
+    for transposed in (False, True):
+        dw = mx.linear_wgrad(dy.to(DEV), xq, transposed=transposed)
+        assert bool(torch.isfinite(dw).all())
+        got = dw[:, pick.to(DEV)].t() if transposed else dw[pick.to(DEV)]
+        _check_product(got, d.t() @ xv, d.abs().t() @ xv.abs(), depth, torch.bfloat16)
+
+
+def test_products_do_not_depend_on_what_ran_before():
+    """The same bits again, after other products and with a workspace of
+    arbitrary contents (split sums are joined in one order)."""
+    x = _values(300, 520, 71, torch.bfloat16)
+    dy = _values(300, 257, 72, torch.bfloat16)
+    xq, w = _matrix(x, "fp8"), _matrix(_values(257, 520, 73, scale=0.02), "fp4")
+    dyg = dy.to(DEV)
+    n = api.q4mx_wgrad_workspace_bytes(dyg, 257, 257, xq.desc)
+    first = None
+    for fill in (0, 255, 127):
+        ws = torch.full((max(n, 16),), fill, dtype=torch.uint8, device=DEV)
+        dw = torch.empty(257, 520, dtype=torch.bfloat16, device=DEV)
+        api.q4mx_wgrad(dyg, 257, 257, xq.desc, dw, api.MX_BF16, 520, 0, ws)
+        got = (dw, mx.linear(xq, w), mx.linear_dgrad(dyg, w), mx.linear(xq, w, dtype=torch.float32))
+        if first is None:
+            first = got
+        assert all(torch.equal(a, b) for a, b in zip(first, got))
+
+
+@pytest.mark.parametrize("tokens", [1, 7, 16, 17, 200])
+def test_a_bf16_operand_gives_the_bits_of_its_quantized_form(tokens):
+    x = _values(tokens, 333, 74, torch.bfloat16).to(DEV)
+    w = _matrix(_values(300, 333, 75, scale=0.02), "fp4")
+    assert torch.equal(mx.linear(x, w), mx.linear(mx.quantize(x, "fp8"), w))
+
+
 def test_empty_operands():
     w = _matrix(_values(40, 64, 20), "fp4")
     x = torch.empty(0, 64, dtype=torch.bfloat16, device=DEV)
@@ -496,6 +592,51 @@ def test_layer_on_a_side_stream_and_in_a_graph():
         want = _mlp(masters, x, dy)
         assert all(torch.equal(a, b) for a, b in zip(held, want)), seed
         torch.cuda.synchronize()
+
+
+def test_decoding_step_and_accumulation_in_a_graph():
+    """One token's products, and a gradient added to at every replay."""
+    w = _matrix(_values(500, 640, 76, scale=0.02), "fp4")
+    x = torch.zeros(1, 640, dtype=torch.bfloat16, device=DEV)
+    xq = mx.quantize(_values(333, 640, 77, torch.bfloat16).to(DEV), "fp8")
+    dy = _values(333, 101, 78, torch.bfloat16, 1e-2).to(DEV)
+    g = torch.zeros(101, 640, dtype=torch.float32, device=DEV)
+    graph = torch.cuda.CUDAGraph()
+    mx.linear(x, w)
+    with torch.cuda.graph(graph):
+        y = mx.linear(x, w)
+        mx.linear_wgrad(dy, xq, out=g, accumulate=True)
+    want = torch.zeros_like(g)
+    for seed in (80, 81, 82):
+        x.copy_(_values(1, 640, seed, torch.bfloat16))
+        graph.replay()
+        torch.cuda.synchronize()
+        mx.linear_wgrad(dy, xq, out=want, accumulate=True)
+        assert torch.equal(y, mx.linear(x, w)) and torch.equal(g, want), seed
+        torch.cuda.synchronize()
+
+
+def test_operands_and_results_are_checked():
+    w = _matrix(_values(40, 64, 83), "fp4")
+    x = torch.zeros(5, 64, dtype=torch.bfloat16, device=DEV)
+    for text, call in (
+            ("columns", lambda: mx.linear(x[:, :32].contiguous(), w)),
+            ("shape", lambda: mx.linear(x, w, out=torch.empty(5, 41, device=DEV))),
+            ("float32 or", lambda: mx.linear(x, w, out=torch.empty(5, 40, device=DEV, dtype=torch.float16))),
+            ("different devices", lambda: mx.linear(x.cpu(), w)),
+            ("bfloat16", lambda: mx.linear(x.float(), w)),
+            ("consecutive", lambda: mx.quantize(x.t(), "fp8")),
+            ("overlap", lambda: mx.linear(x, w, out=torch.empty(40, device=DEV).expand(5, 40))),
+            ("accumulate", lambda: mx.linear_wgrad(x, mx.quantize(x, "fp8"), accumulate=True)),
+            ("rows", lambda: mx.linear_wgrad(x[:3], mx.quantize(x, "fp8"))),
+            ("up", lambda: mx.act_forward("swiglu", x)),
+            ("MXMatrix", lambda: mx.quantize(x, "fp8", out=w))):
+        with pytest.raises(ValueError, match=text):
+            call()
+    with pytest.raises(api.Q4Error, match="FP4"):
+        mx.linear(x, mx.quantize(x, "fp8"))
+    with pytest.raises(api.Q4Error, match="stride"):
+        mx.quantize(x[:1].expand(5, 64), "fp8")
 
 
 def test_training_steps_with_the_optimizer():
