@@ -640,21 +640,28 @@ __global__ __launch_bounds__(64 * WC* WD, 2) void k_mx_grad(Gradient a, MxMat m,
     // Decodes the step that was loaded last into the ring's buffer `slot`: 2
     // pieces turn the lane's four groups of 8 codes to its order, 8 convert
     // half a group each.
-    constexpr int kDecodes = 10, kGroup = kCode / 16;  // words of a group
-    uint32_t half[2];
+    constexpr int kTurns = 2, kConverts = 8, kGroup = kCode / 16;  // words of a group
+    uint32_t turned[kCode / 4], half[2];
+    float block_scale = 0;
     auto decode_piece = [&](int slot, int n) {
-        if (n < 2) {
-            const uint32_t by = n == 0 ? turn1 : turn2;
+        if (n == 0) {
+            block_scale = scale_of((scale >> ((cblk & 3) * 8)) & 0xFF);
+#pragma unroll
+            for (int i = 0; i < kCode / 4; ++i) turned[i] = (code[(i + kGroup) % (kCode / 4)] & turn1) | (code[i] & ~turn1);
+            return;
+        }
+        if (n == 1) {
             uint32_t t[kCode / 4];
 #pragma unroll
-            for (int i = 0; i < kCode / 4; ++i) t[i] = code[i];
+            for (int i = 0; i < kCode / 4; ++i) t[i] = turned[i];
 #pragma unroll
-            for (int i = 0; i < kCode / 4; ++i) code[i] = (t[(i + (n + 1) * kGroup) % (kCode / 4)] & by) | (t[i] & ~by);
+            for (int i = 0; i < kCode / 4; ++i)
+                turned[i] = (t[(i + 2 * kGroup) % (kCode / 4)] & turn2) | (t[i] & ~turn2);
             return;
         }
         const int q = (n - 2) >> 1, h = n & 1;
-        const float s = scale_of((scale >> ((cblk & 3) * 8)) & 0xFF);
-        const uint32_t w = FMT == Q4MX_FP4 ? code[q] : code[q * kGroup + h * (kGroup - 1)];
+        const float s = block_scale;
+        const uint32_t w = FMT == Q4MX_FP4 ? turned[q] : turned[q * kGroup + h * (kGroup - 1)];
         const int k = FMT == Q4MX_FP4 ? 2 * h : 0;
         const uint32_t lo = bf16_pair_of(w, s, FMT, k), hi = bf16_pair_of(w, s, FMT, k + 1);
         if (h == 0) half[0] = lo, half[1] = hi;
@@ -662,7 +669,7 @@ __global__ __launch_bounds__(64 * WC* WD, 2) void k_mx_grad(Gradient a, MxMat m,
     };
     auto decode = [&](int slot) {
 #pragma unroll
-        for (int n = 0; n < kDecodes; ++n) decode_piece(slot, n);
+        for (int n = 0; n < kTurns + kConverts; ++n) decode_piece(slot, n);
     };
 
     // fragments: lane (r, g) reads rows k = 32 q + 8 g + r / 4 (+ 4) at columns 4 (r % 4)
@@ -695,7 +702,7 @@ __global__ __launch_bounds__(64 * WC* WD, 2) void k_mx_grad(Gradient a, MxMat m,
     // product occupies the matrix core for 16 cycles and the issue for 4, and
     // the piece's few instructions fit into the rest.
     auto multiply = [&](int slot) {
-        constexpr int kPieces = kDecodes + kLoads, kEvery = kPieces * 2 <= FC * FD ? 2 : 1;
+        constexpr int kPieces = kTurns + kLoads + kConverts, kEvery = kPieces * 2 <= FC * FD ? 2 : 1;
         static_assert(kPieces <= FC * FD, "pieces");
         __builtin_amdgcn_sched_barrier(0);
         if (kPhases) __builtin_amdgcn_s_setprio(1);
@@ -708,8 +715,12 @@ __global__ __launch_bounds__(64 * WC* WD, 2) void k_mx_grad(Gradient a, MxMat m,
                 const int n = (i * FD + j) / kEvery;
                 if (slot >= 0 && (i * FD + j) % kEvery == 0 && n < kPieces) {
                     __builtin_amdgcn_sched_barrier(0);
-                    if (n < kDecodes) decode_piece(slot, n);
-                    else load_piece(n - kDecodes);
+                    // E4M3: loads before the conversions (wgrad 16384: 723 us,
+                    // behind them 740); E2M1: behind (dgrad 8192: 352, before 363)
+                    constexpr int kBefore = FMT == Q4MX_FP4 ? kTurns + kConverts : kTurns;
+                    if (n < kBefore) decode_piece(slot, n);
+                    else if (n < kBefore + kLoads) load_piece(n - kBefore);
+                    else decode_piece(slot, n - kLoads);
                     __builtin_amdgcn_sched_barrier(0);
                 }
             }
