@@ -1,7 +1,10 @@
 // q4_mx_elem.hip -- quantization to and from the microscaled formats, and
 // the activation functions that keep their input in 8 bits (gfx950).
 //
-// All of it streams memory: a few conversions per element, so HBM bounds it.
+// All of it streams memory: a few conversions per element, so HBM bounds it
+// (checkpoint and restore of 8192 x 5632: 49 us, 280 MB at 5.7 TB/s; swiglu
+// forward, backward and restore there: 172 us, 839 MB at 4.9 TB/s; a large
+// copy 5.2).
 // The conversions are the hardware's (v_cvt_scalef32_*): they divide or
 // multiply by the block's power of two and round to nearest even in one
 // instruction, exactly the format's definition.
@@ -47,7 +50,8 @@ template <bool BF16> __global__ __launch_bounds__(256) void k_mx_quantize(const 
 // takes 128 source rows x 64 source columns: lane c of wave b holds the 32
 // rows of block b in column c (one block in registers, no exchange), reads 64
 // consecutive elements a row, and the four blocks of a column leave together
-// through shared memory as one run of a result row.
+// through shared memory as one run of a result row.  2560 x 10240 FP32 masters
+// to E2M1: 19 us, 119 MB at 6.2 TB/s (part of it from the last-level cache).
 template <bool BF16, int FMT>
 __global__ __launch_bounds__(256) void k_mx_quantize_t(const void* src, int64_t ld, MxMat out, int64_t ctiles) {
     constexpr int kBytes = FMT == Q4MX_FP4 ? 16 : 32;  // codes of a block

@@ -6,8 +6,12 @@
 // the format itself.  dgrad and wgrad multiply BF16 gradients by codes whose
 // blocks run across the sum, so the codes are decoded to BF16 (exactly: E2M1
 // has one fraction bit, E4M3 three, and scales are powers of two) once per
-// tile on their way into shared memory.  All sums are FP32 in the matrix
-// cores' accumulators.
+// tile on their way into shared memory; only values below 2^-126 round there,
+// to BF16's subnormals.  All sums are FP32 in the matrix cores' accumulators.
+// With an E4M3 operand the block-scaled instruction adds each 8 neighbouring
+// products on a grid of 2^-13 of the largest before that.  It is taken for its
+// rate, twice that of products of decoded BF16: the error it adds to 8192 x
+// 2560 x 10240 results is 2e-4 of them (2-norm), their rounding to BF16 1.7e-3.
 
 #include <algorithm>
 
@@ -109,7 +113,8 @@ __device__ __forceinline__ uint32_t inside(uint32_t off, int i, int n) { return 
 
 // A wavefront copies 64 x 16 (or 4) bytes into shared memory from byte `lds`
 // on, lane i's piece at lds + 16 i (4 i), without passing through registers.
-// No register is written, so the only thing to wait for is vmcnt.
+// No register is written, so the only thing to wait for is vmcnt.  (m0 is not
+// the compiler's to keep values in: it sets it where it needs it.)
 __device__ __forceinline__ void copy16(const i32x4& b, uint32_t off, uint32_t lds) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(off), "s"(b)
                  : "memory");
@@ -191,6 +196,12 @@ Out result(const Dense& d, int64_t rows, int64_t cols, bool add) {
 // Rows of w are dealt to fragments in fours: rows 8 q .. 8 q + 3 of 32 to an
 // even fragment's rows 4 q .., 8 q + 4 .. 8 q + 7 to the next one's, so that a
 // lane's 2 x 4 results are 8 neighbouring outputs, one 16-byte store.
+//
+// 8192 tokens x 2560 x 10240, FP8: 167 us, 2.57 PFLOP/s (matrix instructions
+// alone on the same data 107 us; on zeros, which draw less power, the kernel
+// takes 128).  Copies, products and the results' stores share the rest.
+// Before the phases, with a barrier a step: 200 us; with 8-byte stores of a
+// lane's 4 results: 193.
 //
 // The instruction's lane (r, g), r = lane % 16, g = lane / 16, holds of row r
 // the E2M1 codes of columns 32 g .. 32 g + 31, or the E4M3 codes of columns 16
@@ -381,7 +392,8 @@ __global__ __launch_bounds__(64 * WN* WT, 2) void k_mx_linear(MxMat x, MxMat w, 
 // Up to 16 tokens (a decoding step) are one fragment, and the weights' bytes
 // are all that counts: a work-group takes 16 outputs, its NW wavefronts every
 // NW-th slice of 128 columns, straight from memory into registers, and their
-// sums meet in shared memory.  The weights of two slices per wavefront are on
+// sums meet in shared memory (2048 -> 5632, one token: 4.2 us; its 6.1 MB at
+// the copy's rate are 1.2, the rest is a launch's and a load's latency).  The weights of two slices per wavefront are on
 // their way before x is looked at.  A BF16 x is quantized by the work-group, 8
 // columns to a lane, into shared memory (a slice of 16 rows x 128 codes, its
 // 16-byte pieces permuted by the row as in the large product); x in codes
@@ -491,8 +503,13 @@ template <int XF, int NW> __global__ __launch_bounds__(64 * NW) void k_mx_linear
 //
 // The steps of a work-group's units form one stream, as in linear, and half of
 // the wavefronts run a phase behind: while one wavefront of a SIMD multiplies
-// (half a step), the other decodes, copies and reads fragments.  Three steps
-// of the dense operand and two of the codes are in rings.
+// (half a step), the other reads fragments.  Three steps of the dense operand
+// and two of the codes are in rings (160 KB in all).
+//
+// dgrad 8192 x 2560 x 10240: 342 us, 1.25 PFLOP/s; wgrad over 16384 tokens 735
+// us, 1.17 PFLOP/s (the library's BF16 product of these shapes, from operands
+// in BF16, reaches 1.15 and 0.89).  Matrix instructions alone take 70% of
+// that time; decoding and its loads cost 90 and 110 us of wgrad's.
 __device__ __forceinline__ bf16x8 read_turned(const char* p, int pitch) {
     union {
         s16x4 h[2];
@@ -847,16 +864,21 @@ __global__ __launch_bounds__(64 * W0* W1) void k_mx_join(Cut cut, Out out) {
 // ---- how a product is cut ---------------------------------------------------------
 //
 // Two tiles: 256 x 256 by 8 wavefronts, one work-group per compute unit, and
-// 128 x 128 by 4, two per unit (their step costs less than half as much, but
-// more per result).  Where the last round of tiles would leave most units
-// idle, its tiles are split along the sum.  The choice minimizes an estimate
-// of the time: rounds of work-groups times steps, plus what the runs' sums
-// cost to write, read and join.
+// 128 x 128 by 4, two per unit (a step of one costs less than half as much,
+// but a result more: wgrad 4096 x 2048 x 5632 117 us in large tiles, 130 in
+// small ones; dgrad 2048 x 2048 x 2048, 64 large tiles for 256 units, 43 and
+// 32).  Where the last round of tiles would leave most units idle, its tiles
+// are split along the sum (wgrad of 256 outputs over 8192 tokens 93 us whole,
+// 28 split; dgrad 8192 x 2560 x 10240, 320 large tiles, 536 and 380 when it
+// was made), unless the join costs more than that saves (linear 512 x 2048 x
+// 2048: 13.7 us whole, 19.0 split).  The choice minimizes an estimate of the
+// time: rounds of work-groups times steps, plus what the runs' sums cost to
+// write, read and join.  The constants are fits to such measurements.
 struct TileCost {
     double step;  // microseconds of a step with every unit busy
     double ends;  // of a work-group's start and end
 };
-constexpr double kPartBytesPerUs = 4.0e6, kJoinUs = 4.0;
+constexpr double kPartBytesPerUs = 4.0e6, kJoinUs = 6.0;
 
 struct Plan {
     bool big;
@@ -891,8 +913,8 @@ Plan plan_of(int64_t n0, int64_t n1, int64_t steps, const TileCost& big, const T
 }
 
 Plan linear_plan(const MxMat& x, const MxMat& w) {
-    return x.fmt == Q4MX_FP4 ? plan_of(w.rows, x.rows, w.slices, TileCost{1.2, 4}, TileCost{0.8, 3})
-                             : plan_of(w.rows, x.rows, w.slices, TileCost{1.9, 4}, TileCost{1.2, 3});
+    return x.fmt == Q4MX_FP4 ? plan_of(w.rows, x.rows, w.slices, TileCost{1.0, 4}, TileCost{0.65, 4})
+                             : plan_of(w.rows, x.rows, w.slices, TileCost{1.5, 4}, TileCost{0.95, 4});
 }
 Plan grad_plan(const MxMat& m, int64_t width) {
     return plan_of(m.cols, width, tiles(m.rows, 64), TileCost{1.7, 4}, TileCost{1.1, 3});
@@ -946,7 +968,9 @@ hipError_t aligned_gradient(const Dense& dy, int64_t rows, int64_t cols, void* c
 }
 
 // Wavefronts of a work-group: as many as give each two slices, up to 16, but
-// no more than fill the chip (8 a compute unit).
+// no more than fill the chip (8 a compute unit).  One token, 4, 8 and 16
+// wavefronts: 2048 -> 5632 4.6, 4.2, 5.6 us (8 taken); 10240 -> 2560 9.3, 7.5,
+// 7.0 (16); 2560 -> 10240 5.7, 6.0, 8.3 (4).
 template <int XF> hipError_t few(const Few& x, const MxMat& w, const Out& y, hipStream_t st) {
     const int64_t groups = tiles(w.rows, 16);
     int waves = 4;
