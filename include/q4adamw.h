@@ -386,7 +386,10 @@ q4_status q4adamw_dequant_state(const q4_config* cfg, const q4_tensor* t, float*
  * dense result's rows x cols elements is written.  A call whose result has
  * no elements does nothing; a product over no elements is 0.  The calls take
  * no upload and allocate nothing, so they may be captured in a HIP graph;
- * the operands' pointers must live on the current device. */
+ * the operands' pointers must live on the current device, and a workspace
+ * must not be used by two calls that overlap there.  The products take in and
+ * out widths, and row strides, below 2^23, and results below 2^38 elements.
+ * The result of a call depends on its operands alone, bit for bit. */
 
 typedef enum { Q4MX_FP4 = 0, Q4MX_FP8 = 1 } q4mx_format;
 typedef enum { Q4MX_F32 = 0, Q4MX_BF16 = 1 } q4mx_dtype;
@@ -434,7 +437,9 @@ q4_status q4mx_linear_bf16(const uint16_t* x, int64_t ldx, int64_t tokens, const
 q4_status q4mx_linear_bf16_workspace_bytes(int64_t tokens, const q4mx_matrix* w, size_t* bytes);
 
 /* dx (tokens x w->cols, dtype) <- dy w, dy BF16 (tokens x w->rows), w in
- * Q4MX_FP4. */
+ * Q4MX_FP4.  The codes' values enter as BF16, exactly but below 2^-126; sums
+ * in FP32.  This and q4mx_wgrad copy a dy whose rows are not 16-byte aligned
+ * runs of a multiple of 8 elements into the workspace first. */
 q4_status q4mx_dgrad(const uint16_t* dy, int64_t lddy, int64_t tokens, const q4mx_matrix* w, void* dx, int32_t dtype,
                      int64_t lddx, void* ws, size_t ws_bytes, void* stream);
 q4_status q4mx_dgrad_workspace_bytes(const uint16_t* dy, int64_t lddy, int64_t tokens, const q4mx_matrix* w,
@@ -469,7 +474,7 @@ q4_status q4mx_act_forward(int32_t act, const uint16_t* x, int64_t ldx, const ui
 
 /* Backward from the checkpoints: dx <- dy f'(x) (times up), and dup <- dy
  * f(x) for Q4MX_SWIGLU, with x and up the kept values; all BF16, rows x cols
- * of kept_x.  dx may be dy. */
+ * of kept_x.  dx may be dy (with its row stride). */
 q4_status q4mx_act_backward(int32_t act, const q4mx_matrix* kept_x, const q4mx_matrix* kept_up, const uint16_t* dy,
                             int64_t lddy, uint16_t* dx, int64_t lddx, uint16_t* dup, int64_t lddup, void* stream);
 
