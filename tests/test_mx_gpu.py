@@ -265,6 +265,32 @@ def test_wgrad(tokens, cin, cout, fmt, transposed):
         _check_product(out, want + g.double(), terms + g.double().abs(), tokens + 1, dtype)
 
 
+def test_gradients_against_differences():
+    """L = sum(dy * (x w^T)) is linear in each operand, so (L(v + h) - L(v -
+    h)) / 2h in 64 bits is its derivative for any h, to 2^-52 of the terms
+    over h; dgrad and wgrad give it to a product's tolerance."""
+    tokens, cin, cout, h = 37, 150, 61, 2.0 ** -4
+    x, w = _matrix(_values(tokens, cin, 90, torch.bfloat16), "fp8"), _matrix(_values(cout, cin, 91, scale=0.1), "fp4")
+    dy = _values(tokens, cout, 92, torch.bfloat16, 0.1)
+    xv, wv, d = ref.values_of(x), ref.values_of(w), dy.double()
+    loss = lambda a, b: (d * (a @ b.t())).sum().item()  # noqa: E731
+    dx = mx.linear_dgrad(dy.to(DEV), w, dtype=torch.float32).cpu().double()
+    dw = mx.linear_wgrad(dy.to(DEV), x, dtype=torch.float32).cpu().double()
+    slack = 2.0 ** -52 * (d.abs() * (xv.abs() @ wv.abs().t())).sum().item() * tokens * cout / h
+    for r, c in ((0, 0), (36, 149), (17, 64), (5, 128)):
+        e = torch.zeros_like(xv)
+        e[r, c] = h
+        diff = (loss(xv + e, wv) - loss(xv - e, wv)) / (2 * h)
+        terms = (d[r].abs() * wv[:, c].abs()).sum().item()
+        assert abs(dx[r, c].item() - diff) <= abs(diff) * 2.0 ** -24 + (cout + 16) * 2.0 ** -23 * terms + slack
+    for r, c in ((0, 0), (60, 149), (33, 31), (7, 128)):
+        e = torch.zeros_like(wv)
+        e[r, c] = h
+        diff = (loss(xv, wv + e) - loss(xv, wv - e)) / (2 * h)
+        terms = (d[:, r].abs() * xv[:, c].abs()).sum().item()
+        assert abs(dw[r, c].item() - diff) <= abs(diff) * 2.0 ** -24 + (tokens + 16) * 2.0 ** -23 * terms + slack
+
+
 @pytest.mark.parametrize("gap,shift", [(0, 1), (3, 0), (8, 8), (8, 5)])
 def test_products_take_strided_and_misaligned_operands(gap, shift):
     """Rows with gaps of NaN between them, bases off by one element; results
