@@ -102,26 +102,26 @@ _SIGNATURES = {
                            C.c_void_p], C.c_int),
     "q4adamw_grad_norm": ([C.c_void_p, C.c_size_t, C.POINTER(C.c_double), C.c_void_p], C.c_int),
     "q4mx_matrix_bytes": ([C.c_int32, C.c_int64, C.c_int64, C.POINTER(C.c_size_t), C.POINTER(C.c_size_t)], C.c_int),
-    "q4mx_quantize": ([C.c_void_p, C.c_int32, C.c_int64, C.c_int32, C.POINTER(Q4MXMatrix), C.c_void_p], C.c_int),
-    "q4mx_dequantize": ([C.POINTER(Q4MXMatrix), C.c_void_p, C.c_int32, C.c_int64, C.c_void_p], C.c_int),
-    "q4mx_linear": ([C.POINTER(Q4MXMatrix), C.POINTER(Q4MXMatrix), C.c_void_p, C.c_int32, C.c_int64, C.c_void_p,
+    "q4mx_quantize": ([C.c_void_p, C.c_int32, C.c_int64, C.c_int32, C.c_void_p, C.c_void_p], C.c_int),
+    "q4mx_dequantize": ([C.c_void_p, C.c_void_p, C.c_int32, C.c_int64, C.c_void_p], C.c_int),
+    "q4mx_linear": ([C.c_void_p, C.c_void_p, C.c_void_p, C.c_int32, C.c_int64, C.c_void_p,
                      C.c_size_t, C.c_void_p], C.c_int),
-    "q4mx_linear_workspace_bytes": ([C.POINTER(Q4MXMatrix), C.POINTER(Q4MXMatrix), C.POINTER(C.c_size_t)], C.c_int),
-    "q4mx_linear_bf16": ([C.c_void_p, C.c_int64, C.c_int64, C.POINTER(Q4MXMatrix), C.c_void_p, C.c_int32, C.c_int64,
+    "q4mx_linear_workspace_bytes": ([C.c_void_p, C.c_void_p, C.POINTER(C.c_size_t)], C.c_int),
+    "q4mx_linear_bf16": ([C.c_void_p, C.c_int64, C.c_int64, C.c_void_p, C.c_void_p, C.c_int32, C.c_int64,
                           C.c_void_p, C.c_size_t, C.c_void_p], C.c_int),
-    "q4mx_linear_bf16_workspace_bytes": ([C.c_int64, C.POINTER(Q4MXMatrix), C.POINTER(C.c_size_t)], C.c_int),
-    "q4mx_dgrad": ([C.c_void_p, C.c_int64, C.c_int64, C.POINTER(Q4MXMatrix), C.c_void_p, C.c_int32, C.c_int64,
+    "q4mx_linear_bf16_workspace_bytes": ([C.c_int64, C.c_void_p, C.POINTER(C.c_size_t)], C.c_int),
+    "q4mx_dgrad": ([C.c_void_p, C.c_int64, C.c_int64, C.c_void_p, C.c_void_p, C.c_int32, C.c_int64,
                     C.c_void_p, C.c_size_t, C.c_void_p], C.c_int),
-    "q4mx_dgrad_workspace_bytes": ([C.c_void_p, C.c_int64, C.c_int64, C.POINTER(Q4MXMatrix),
+    "q4mx_dgrad_workspace_bytes": ([C.c_void_p, C.c_int64, C.c_int64, C.c_void_p,
                                     C.POINTER(C.c_size_t)], C.c_int),
-    "q4mx_wgrad": ([C.c_void_p, C.c_int64, C.c_int64, C.POINTER(Q4MXMatrix), C.c_void_p, C.c_int32, C.c_int64,
+    "q4mx_wgrad": ([C.c_void_p, C.c_int64, C.c_int64, C.c_void_p, C.c_void_p, C.c_int32, C.c_int64,
                     C.c_int32, C.c_void_p, C.c_size_t, C.c_void_p], C.c_int),
-    "q4mx_wgrad_workspace_bytes": ([C.c_void_p, C.c_int64, C.c_int64, C.POINTER(Q4MXMatrix), C.c_int32,
+    "q4mx_wgrad_workspace_bytes": ([C.c_void_p, C.c_int64, C.c_int64, C.c_void_p, C.c_int32,
                                     C.POINTER(C.c_size_t)], C.c_int),
     "q4mx_act_forward": ([C.c_int32, C.c_void_p, C.c_int64, C.c_void_p, C.c_int64, C.c_int64, C.c_int64, C.c_void_p,
-                          C.c_int64, C.POINTER(Q4MXMatrix), C.POINTER(Q4MXMatrix), C.POINTER(Q4MXMatrix),
+                          C.c_int64, C.c_void_p, C.c_void_p, C.c_void_p,
                           C.c_void_p], C.c_int),
-    "q4mx_act_backward": ([C.c_int32, C.POINTER(Q4MXMatrix), C.POINTER(Q4MXMatrix), C.c_void_p, C.c_int64,
+    "q4mx_act_backward": ([C.c_int32, C.c_void_p, C.c_void_p, C.c_void_p, C.c_int64,
                            C.c_void_p, C.c_int64, C.c_void_p, C.c_int64, C.c_void_p], C.c_int),
 }
 
@@ -295,7 +295,8 @@ def q4adamw_grad_norm(ws, ws_bytes: int | None = None, stream=None) -> float:
 # ---- microscaled matrices (dense operands as pointer, row stride) -----------
 
 def _mx(m):
-    return C.byref(m) if m is not None else None
+    """An MX matrix for a call: a Q4MXMatrix, or its bytes as they are."""
+    return m if m is None or type(m) is bytes else C.byref(m)
 
 
 def _ws(ws, ws_bytes):

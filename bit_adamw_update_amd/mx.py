@@ -20,6 +20,8 @@ calls are the layer's backward pass.
 """
 from __future__ import annotations
 
+import struct
+
 import torch
 
 from . import api
@@ -27,6 +29,8 @@ from . import api
 FORMATS = {"fp4": api.MX_FP4, "fp8": api.MX_FP8}
 ACTIVATIONS = {"gelu": api.MX_GELU, "gelu_erf": api.MX_GELU_ERF, "swiglu": api.MX_SWIGLU}
 _DTYPES = {torch.float32: api.MX_F32, torch.bfloat16: api.MX_BF16}
+_BOTH = tuple(_DTYPES)
+_PACK = struct.Struct("@iiqqPP").pack   # a q4mx_matrix
 
 
 class MXMatrix:
@@ -36,7 +40,7 @@ class MXMatrix:
             a multiple of 128;
     scales: uint8 [P / 128, rows, 4].
     """
-    __slots__ = ("rows", "cols", "format", "device", "desc", "_codes", "_scales", "_buf")
+    __slots__ = ("rows", "cols", "format", "device", "packed", "_codes", "_scales", "_buf")
 
     def __init__(self, rows: int, cols: int, format: str, codes=None, scales=None, device="cuda"):
         if format not in FORMATS:
@@ -69,7 +73,12 @@ class MXMatrix:
                 raise ValueError("codes and scales must be on one device")
             self.device = codes.device
             pointers = (codes.data_ptr(), scales.data_ptr())
-        self.desc = api.Q4MXMatrix(code, 0, rows, cols, *pointers)
+        self.packed = _PACK(code, 0, rows, cols, *pointers)   # for the calls
+
+    @property
+    def desc(self) -> api.Q4MXMatrix:
+        """The C description of the matrix."""
+        return api.Q4MXMatrix.from_buffer_copy(self.packed)
 
     def _code_shape(self) -> tuple:
         return (self.rows, (self.cols + 127) // 128 * (64 if self.format == "fp4" else 128))
@@ -109,10 +118,11 @@ def _dense(name, t, dtypes=(torch.bfloat16,)):
     if not t.is_cuda:
         raise ValueError(f"{name} must be on a GPU")
     rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
+    ld, step = t.stride()
+    if cols > 1 and step != 1:
         raise ValueError(f"{name} must have consecutive columns (stride 1)")
     # the stride of a single row, or of an empty matrix, means nothing
-    return t.stride(0) if rows > 1 and cols > 0 else max(1, cols)
+    return ld if rows > 1 and cols > 0 else max(1, cols)
 
 
 def _matrix(name, m):
@@ -122,11 +132,12 @@ def _matrix(name, m):
 
 
 def _result(out, shape, dtype, device):
+    """(result, its dtype code, its row stride)."""
     if out is None:
         if dtype not in _DTYPES:
             raise ValueError(f"dtype must be torch.float32 or torch.bfloat16, not {dtype}")
-        out = torch.empty(shape, dtype=dtype, device=device)
-    ld = _dense("out", out, tuple(_DTYPES))
+        return torch.empty(shape, dtype=dtype, device=device), _DTYPES[dtype], max(1, shape[1])
+    ld = _dense("out", out, _BOTH)
     if tuple(out.shape) != tuple(shape):
         raise ValueError(f"out must have shape {tuple(shape)}, not {tuple(out.shape)}")
     if out.shape[0] > 1 and ld < out.shape[1]:
@@ -150,28 +161,18 @@ def _same_device(first, *others):
     return device
 
 
-class _Here:
-    """The current device and stream: nothing to enter."""
-
-    def __enter__(self):
-        return None
-
-    def __exit__(self, *exc):
-        return None
-
-
-_HERE = _Here()
+def _elsewhere(device, stream) -> bool:
+    """Whether a call has to enter its device or stream first."""
+    return stream is not None or torch._C._cuda_getDevice() != device.index
 
 
 def _on(device, stream):
     """The device and stream of a call as a context."""
-    if stream is not None:
-        if stream.device != device:
-            raise ValueError(f"the stream is on {stream.device}, the operands on {device}")
-        return torch.cuda.stream(stream)   # makes the stream's device current
-    if torch._C._cuda_getDevice() == device.index:
-        return _HERE
-    return torch.cuda.device(device)
+    if stream is None:
+        return torch.cuda.device(device)
+    if stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the operands on {device}")
+    return torch.cuda.stream(stream)   # makes the stream's device current
 
 
 def _raw(device) -> int:
@@ -187,23 +188,31 @@ def quantize(src, format: str, transpose: bool = False, out: MXMatrix | None = N
     """src (float32 or bfloat16) in a microscaled format, blocks along its
     columns; transpose: the quantized transpose, blocks along its rows (a
     weight whose master is stored [in, out])."""
-    ld = _dense("src", src, tuple(_DTYPES))
+    ld = _dense("src", src, _BOTH)
     if format not in FORMATS:
         raise ValueError(f"unknown format {format!r}; expected one of {sorted(FORMATS)}")
+    device = src.device
+    if out is not None:
+        _same_device(src, out)
+    if _elsewhere(device, stream):
+        with _on(device, stream):
+            return quantize(src, format, transpose, out)
     rows, cols = src.shape[::-1] if transpose else src.shape
-    device = _same_device(src, out)
-    with _on(device, stream):
-        out = _mx_result(out, rows, cols, format, device)
-        api.q4mx_quantize(src, _DTYPES[src.dtype], ld, transpose, out.desc, _raw(device))
+    out = _mx_result(out, rows, cols, format, device)
+    api.q4mx_quantize(src.data_ptr(), _DTYPES[src.dtype], ld, transpose, out.packed, _raw(device))
     return out
 
 
 def dequantize(a: MXMatrix, dtype=torch.bfloat16, out=None, stream=None) -> torch.Tensor:
     """The values of a."""
-    device = _same_device(_matrix("a", a), out)
-    with _on(device, stream):
-        out, code, ld = _result(out, a.shape, dtype, device)
-        api.q4mx_dequantize(a.desc, out, code, ld, _raw(device))
+    device = _matrix("a", a).device
+    if out is not None:
+        _same_device(a, out)
+    if _elsewhere(device, stream):
+        with _on(device, stream):
+            return dequantize(a, dtype, out)
+    out, code, ld = _result(out, (a.rows, a.cols), dtype, device)
+    api.q4mx_dequantize(a.packed, out.data_ptr(), code, ld, _raw(device))
     return out
 
 
@@ -211,24 +220,25 @@ def linear(x, w: MXMatrix, out=None, dtype=torch.bfloat16, stream=None) -> torch
     """x w^T: x an MXMatrix [tokens, in] or a bfloat16 tensor (quantized to
     "fp8" on the way), w an MXMatrix [out, in] in "fp4"."""
     device = _same_device(x, _matrix("w", w), out)
-    if isinstance(x, MXMatrix):
+    coded = isinstance(x, MXMatrix)
+    if not coded:
+        ldx = _dense("x", x)
+        if x.shape[1] != w.cols:
+            raise ValueError(f"x has {x.shape[1]} columns, w has {w.cols}")
+    if _elsewhere(device, stream):
         with _on(device, stream):
-            out, code, ld = _result(out, (x.rows, w.rows), dtype, device)
-            ws = None
-            if x.rows > api.MX_FEW_TOKENS:
-                ws = _workspace(api.q4mx_linear_workspace_bytes(x.desc, w.desc), device)
-            api.q4mx_linear(x.desc, w.desc, out, code, ld, ws, stream=_raw(device))
-        return out
-    ldx = _dense("x", x)
-    if x.shape[1] != w.cols:
-        raise ValueError(f"x has {x.shape[1]} columns, w has {w.cols}")
-    tokens = x.shape[0]
-    with _on(device, stream):
-        out, code, ld = _result(out, (tokens, w.rows), dtype, device)
-        ws = None
-        if tokens > api.MX_FEW_TOKENS:
-            ws = _workspace(api.q4mx_linear_bf16_workspace_bytes(tokens, w.desc), device)
-        api.q4mx_linear_bf16(x, ldx, tokens, w.desc, out, code, ld, ws, stream=_raw(device))
+            return linear(x, w, out, dtype)
+    tokens = x.rows if coded else x.shape[0]
+    out, code, ld = _result(out, (tokens, w.rows), dtype, device)
+    need = 0
+    if tokens > api.MX_FEW_TOKENS:
+        need = (api.q4mx_linear_workspace_bytes(x.packed, w.packed) if coded
+                else api.q4mx_linear_bf16_workspace_bytes(tokens, w.packed))
+    ws = _workspace(need, device)
+    if coded:
+        api.q4mx_linear(x.packed, w.packed, out.data_ptr(), code, ld, ws, need, _raw(device))
+    else:
+        api.q4mx_linear_bf16(x.data_ptr(), ldx, tokens, w.packed, out.data_ptr(), code, ld, ws, need, _raw(device))
     return out
 
 
@@ -236,13 +246,16 @@ def linear_dgrad(dy, w: MXMatrix, out=None, dtype=torch.bfloat16, stream=None) -
     """dy w: the gradient of linear's x, dy bfloat16 [tokens, out]."""
     lddy = _dense("dy", dy)
     device = _same_device(dy, _matrix("w", w), out)
-    if dy.shape[1] != w.rows:
-        raise ValueError(f"dy has {dy.shape[1]} columns, w has {w.rows} rows")
-    tokens = dy.shape[0]
-    with _on(device, stream):
-        out, code, ld = _result(out, (tokens, w.cols), dtype, device)
-        ws = _workspace(api.q4mx_dgrad_workspace_bytes(dy, lddy, tokens, w.desc), device)
-        api.q4mx_dgrad(dy, lddy, tokens, w.desc, out, code, ld, ws, stream=_raw(device))
+    tokens, n = dy.shape
+    if n != w.rows:
+        raise ValueError(f"dy has {n} columns, w has {w.rows} rows")
+    if _elsewhere(device, stream):
+        with _on(device, stream):
+            return linear_dgrad(dy, w, out, dtype)
+    out, code, ld = _result(out, (tokens, w.cols), dtype, device)
+    at = dy.data_ptr()
+    need = api.q4mx_dgrad_workspace_bytes(at, lddy, tokens, w.packed)
+    api.q4mx_dgrad(at, lddy, tokens, w.packed, out.data_ptr(), code, ld, _workspace(need, device), need, _raw(device))
     return out
 
 
@@ -252,16 +265,19 @@ def linear_wgrad(dy, x: MXMatrix, out=None, transposed: bool = False, accumulate
     checkpoint x: the gradient of linear's w.  accumulate: added to out."""
     lddy = _dense("dy", dy)
     device = _same_device(dy, _matrix("x", x), out)
-    if dy.shape[0] != x.rows:
-        raise ValueError(f"dy has {dy.shape[0]} rows, x has {x.rows}")
+    tokens, n = dy.shape
+    if tokens != x.rows:
+        raise ValueError(f"dy has {tokens} rows, x has {x.rows}")
     if accumulate and out is None:
         raise ValueError("accumulate needs out")
-    n = dy.shape[1]
+    if _elsewhere(device, stream):
+        with _on(device, stream):
+            return linear_wgrad(dy, x, out, transposed, accumulate, dtype)
     flags = (api.MX_WGRAD_TRANSPOSED if transposed else 0) | (api.MX_WGRAD_ADD if accumulate else 0)
-    with _on(device, stream):
-        out, code, ld = _result(out, (x.cols, n) if transposed else (n, x.cols), dtype, device)
-        ws = _workspace(api.q4mx_wgrad_workspace_bytes(dy, lddy, n, x.desc, flags), device)
-        api.q4mx_wgrad(dy, lddy, n, x.desc, out, code, ld, flags, ws, stream=_raw(device))
+    out, code, ld = _result(out, (x.cols, n) if transposed else (n, x.cols), dtype, device)
+    at = dy.data_ptr()
+    need = api.q4mx_wgrad_workspace_bytes(at, lddy, n, x.packed, flags)
+    api.q4mx_wgrad(at, lddy, n, x.packed, out.data_ptr(), code, ld, flags, _workspace(need, device), need, _raw(device))
     return out
 
 
@@ -277,32 +293,33 @@ def act_forward(kind: str, x, up=None, out_format: str | None = None, stream=Non
     MXMatrix (the next linear layer's operand); kept is what act_backward
     needs, the inputs in 8 bits."""
     act = _activation(kind)
-    ldx = _dense("x", x)
+    ldx, ldup, up_at = _dense("x", x), 0, None
     if (up is not None) != (kind == "swiglu"):
         raise ValueError('"swiglu" takes up, the others do not')
-    ldup = 0
+    device = x.device
     if up is not None:
-        ldup = _dense("up", up)
+        ldup, up_at = _dense("up", up), up.data_ptr()
         if up.shape != x.shape:
             raise ValueError("x and up must have one shape")
+        _same_device(x, up)
     if out_format is not None and out_format not in FORMATS:
         raise ValueError(f"unknown format {out_format!r}; expected one of {sorted(FORMATS)}")
-    device = _same_device(x, up)
+    if _elsewhere(device, stream):
+        with _on(device, stream):
+            return act_forward(kind, x, up, out_format)
     rows, cols = x.shape
-    with _on(device, stream):
-        y = y_mx = kept_up = None
-        ldy = 0
-        if out_format is None:
-            y = torch.empty((rows, cols), dtype=torch.bfloat16, device=device)
-            ldy = max(1, cols)
-        else:
-            y_mx = MXMatrix(rows, cols, out_format, device=device)
-        kept_x = MXMatrix(rows, cols, "fp8", device=device)
-        if up is not None:
-            kept_up = MXMatrix(rows, cols, "fp8", device=device)
-        api.q4mx_act_forward(act, x, ldx, up, ldup, rows, cols, y, ldy, y_mx.desc if y_mx is not None else None,
-                             kept_x.desc, kept_up.desc if kept_up is not None else None, _raw(device))
-    return (y if y_mx is None else y_mx), (kept_x, kept_up)
+    y_at = y_mx = None
+    if out_format is None:
+        y = torch.empty((rows, cols), dtype=torch.bfloat16, device=device)
+        y_at = y.data_ptr()
+    else:
+        y = MXMatrix(rows, cols, out_format, device=device)
+        y_mx = y.packed
+    kept_x = MXMatrix(rows, cols, "fp8", device=device)
+    kept_up = None if up is None else MXMatrix(rows, cols, "fp8", device=device)
+    api.q4mx_act_forward(act, x.data_ptr(), ldx, up_at, ldup, rows, cols, y_at, max(1, cols), y_mx, kept_x.packed,
+                         None if up is None else kept_up.packed, _raw(device))
+    return y, (kept_x, kept_up)
 
 
 def act_backward(kind: str, kept, dy, stream=None) -> tuple:
@@ -313,13 +330,16 @@ def act_backward(kind: str, kept, dy, stream=None) -> tuple:
     if (kept_up is not None) != (kind == "swiglu"):
         raise ValueError('"swiglu" keeps up, the others do not')
     lddy = _dense("dy", dy)
-    if tuple(dy.shape) != kept_x.shape:
-        raise ValueError(f"dy must have shape {kept_x.shape}, not {tuple(dy.shape)}")
+    shape = (kept_x.rows, kept_x.cols)
+    if tuple(dy.shape) != shape:
+        raise ValueError(f"dy must have shape {shape}, not {tuple(dy.shape)}")
     device = _same_device(dy, kept_x, kept_up)
-    ld = max(1, dy.shape[1])
-    with _on(device, stream):
-        dx = torch.empty(dy.shape, dtype=torch.bfloat16, device=device)
-        dup = torch.empty_like(dx) if kept_up is not None else None
-        api.q4mx_act_backward(act, kept_x.desc, kept_up.desc if kept_up is not None else None, dy, lddy, dx, ld, dup,
-                              ld, _raw(device))
+    if _elsewhere(device, stream):
+        with _on(device, stream):
+            return act_backward(kind, kept, dy)
+    ld = max(1, shape[1])
+    dx = torch.empty(shape, dtype=torch.bfloat16, device=device)
+    dup = None if kept_up is None else torch.empty(shape, dtype=torch.bfloat16, device=device)
+    api.q4mx_act_backward(act, kept_x.packed, None if dup is None else kept_up.packed, dy.data_ptr(), lddy,
+                          dx.data_ptr(), ld, None if dup is None else dup.data_ptr(), ld, _raw(device))
     return (dx,) if dup is None else (dx, dup)
