@@ -1,17 +1,16 @@
 // q4_mx_gemm.hip -- the three products of the microscaled linear layer
 // (gfx950).
 //
-// linear multiplies codes by codes: the block-scaled matrix instructions take
-// E4M3 or E2M1 operands with a power of two per row and 32 columns, which is
-// the format itself.  dgrad and wgrad multiply BF16 gradients by codes whose
-// blocks run across the sum, so the codes are decoded to BF16 (exactly: E2M1
-// has one fraction bit, E4M3 three, and scales are powers of two) once per
-// tile on their way into shared memory; only values below 2^-126 round there,
-// to BF16's subnormals.  All sums are FP32 in the matrix cores' accumulators.
-// With an E4M3 operand the block-scaled instruction adds each 8 neighbouring
-// products on a grid of 2^-13 of the largest before that.  It is taken for its
-// rate, twice that of products of decoded BF16: the error it adds to 8192 x
-// 2560 x 10240 results is 2e-4 of them (2-norm), their rounding to BF16 1.7e-3.
+// linear with an E2M1 x multiplies codes by codes: the block-scaled matrix
+// instruction takes operands with a power of two per row and 32 columns, which
+// is the format itself, and E2M1 products and their sums lose nothing in it.
+// With an E4M3 operand the same instruction adds each 8 neighbouring products
+// on a grid of 2^-13 of the largest, fewer bits than FP32, so a linear with an
+// E4M3 x, and dgrad and wgrad (BF16 gradients by codes whose blocks run across
+// the sum), are products of BF16: codes are decoded to it exactly (E2M1 has one
+// fraction bit, E4M3 three, and scales are powers of two); only values below
+// 2^-126 round there, to BF16's subnormals.  All sums are FP32 in the matrix
+// cores' accumulators.
 
 #include <algorithm>
 
@@ -138,6 +137,39 @@ __device__ __forceinline__ uint32_t lds_base(const void* p) {
     return (uint32_t) reinterpret_cast<uintptr_t>((Q4_LDS const char*)p);
 }
 
+// ---- decoding -----------------------------------------------------------------
+
+__device__ __forceinline__ uint32_t bf16_pair_of(uint32_t w, float s, int fmt, int k) {
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    union {
+        bf16x2 v;
+        uint32_t u;
+    } t;
+    if (fmt == Q4MX_FP4) {
+        switch (k) {
+        case 0: t.v = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 0); break;
+        case 1: t.v = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 1); break;
+        case 2: t.v = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 2); break;
+        default: t.v = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3); break;
+        }
+    } else {
+        t.v = k == 0 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, s, false)
+                     : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, s, true);
+    }
+    return t.u;
+}
+// 8 neighbouring codes of a block with scale s: a word of E2M1, two of E4M3.
+__device__ __forceinline__ bf16x8 bf16_of_e2m1(uint32_t w, float s) {
+    const u32x4 t = {bf16_pair_of(w, s, Q4MX_FP4, 0), bf16_pair_of(w, s, Q4MX_FP4, 1), bf16_pair_of(w, s, Q4MX_FP4, 2),
+                     bf16_pair_of(w, s, Q4MX_FP4, 3)};
+    return __builtin_bit_cast(bf16x8, t);
+}
+__device__ __forceinline__ bf16x8 bf16_of_e4m3(uint32_t lo, uint32_t hi, float s) {
+    const u32x4 t = {bf16_pair_of(lo, s, Q4MX_FP8, 0), bf16_pair_of(lo, s, Q4MX_FP8, 1), bf16_pair_of(hi, s, Q4MX_FP8, 0),
+                     bf16_pair_of(hi, s, Q4MX_FP8, 1)};
+    return __builtin_bit_cast(bf16x8, t);
+}
+
 // ---- results -------------------------------------------------------------------
 
 // A result whose element (r, c) is p[r * ld + c]; `add`: added to what is
@@ -184,28 +216,32 @@ Out result(const Dense& d, int64_t rows, int64_t cols, bool add) {
     return Out{d.p, d.ld, rows, cols, d.dtype == Q4MX_BF16, add};
 }
 
-// ---- linear: codes by codes -------------------------------------------------------
+// ---- linear ---------------------------------------------------------------------
 //
 // A work-group of WN x WT wavefronts forms BN outputs x BT tokens; a wavefront
-// FN x FT tiles of 16 x 16, 128 columns of the sum per instruction.  Both
-// operands are copied straight into shared memory, three steps of 128 columns
-// in a ring: while one is multiplied, the next two are on their way.  A row of
-// a step is 64 bytes (E2M1) or 128 (E4M3); its 16-byte pieces are permuted by
-// the row's low bits, so that the 16 rows of a fragment read different banks.
+// FN x FT tiles of 16 x 16, 128 columns of the sum per step.  Both operands'
+// codes are copied straight into shared memory, three steps of 128 columns in a
+// ring: while one is multiplied, the next two are on their way.  A row of a
+// step is 64 bytes (E2M1) or 128 (E4M3); its 16-byte pieces are permuted by the
+// row's low bits, so that the 16 rows of a fragment read different banks.
 //
 // Rows of w are dealt to fragments in fours: rows 8 q .. 8 q + 3 of 32 to an
 // even fragment's rows 4 q .., 8 q + 4 .. 8 q + 7 to the next one's, so that a
 // lane's 2 x 4 results are 8 neighbouring outputs, one 16-byte store.
 //
-// 8192 tokens x 2560 x 10240, FP8: 167 us, 2.57 PFLOP/s (matrix instructions
-// alone on the same data 107 us; on zeros, which draw less power, the kernel
-// takes 128).  Copies, products and the results' stores share the rest.
-// Before the phases, with a barrier a step: 200 us; with 8-byte stores of a
-// lane's 4 results: 193.
+// Lane (r, g), r = lane % 16, g = lane / 16, holds of row r the codes of
+// columns 32 g .. 32 g + 31, one block, and its scale byte: what the
+// block-scaled instruction wants for E2M1.  For E4M3 it decodes 8 columns of
+// each operand at a time, columns 32 g + 8 q .. + 7 for the q-th of four BF16
+// products: the order of the columns does not matter to a sum, as long as both
+// operands have the same.  Every wavefront decodes the fragments that it
+// multiplies (twice or four times what the tile has): the conversions take
+// issue slots that 16-cycle products leave free, and codes are a half or a
+// quarter of BF16's bytes in shared memory.
 //
-// The instruction's lane (r, g), r = lane % 16, g = lane / 16, holds of row r
-// the E2M1 codes of columns 32 g .. 32 g + 31, or the E4M3 codes of columns 16
-// g .. +15 and 64 + 16 g .. +15, and the scale byte of columns 32 g .. +31.
+// 8192 tokens x 2560 x 10240, E4M3: 286-291 us, 1.48 PFLOP/s (the library's product
+// of BF16 operands reaches 1.36 at 8192 cubed; the block-scaled instruction
+// takes 168 us, with the coarser sums).  E2M1: 128 us.
 template <int XF, int WN, int WT, int FN, int FT>
 __global__ __launch_bounds__(64 * WN* WT, 2) void k_mx_linear(MxMat x, MxMat w, Out y, Cut cut) {
     constexpr int NW = WN * WT, BN = WN * FN * 16, BT = WT * FT * 16;
@@ -275,8 +311,8 @@ __global__ __launch_bounds__(64 * WN* WT, 2) void k_mx_linear(MxMat x, MxMat w, 
     const int r = lane & 15, g = lane >> 4, wn = wave % WN, wt = wave / WN;
     const int wrow = wn * FN * 16 + (r >> 2) * 8 + (r & 3), xrow = wt * FT * 16 + r;
     const int wat = wrow * 64 + ((g ^ (((r >> 1) & 1) | (((r >> 2) & 1) << 1))) * 16);
-    const int xat = kW + xrow * XB + (XF == Q4MX_FP4 ? (g ^ ((r >> 1) & 3)) * 16 : (g ^ (r & 7)) * 16);
-    const int xat2 = kW + xrow * XB + ((4 + g) ^ (r & 7)) * 16;
+    const int xat = kW + xrow * XB + (XF == Q4MX_FP4 ? (g ^ ((r >> 1) & 3)) * 16 : ((2 * g) ^ (r & 7)) * 16);
+    const int xat2 = kW + xrow * XB + ((2 * g + 1) ^ (r & 7)) * 16;
     const int wsat = kW + kX + wrow * 4 + g, xsat = kW + kX + BN * 4 + xrow * 4 + g;
 
     f32x4 acc[FN][FT] = {};
@@ -305,14 +341,32 @@ __global__ __launch_bounds__(64 * WN* WT, 2) void k_mx_linear(MxMat x, MxMat w, 
     };
     auto multiply = [&] {
         const i32x4 none = {0, 0, 0, 0};
+        if (XF == Q4MX_FP4) {
 #pragma unroll
-        for (int i = 0; i < FN; ++i)
+            for (int i = 0; i < FN; ++i)
 #pragma unroll
-            for (int j = 0; j < FT; ++j)
-                acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                    __builtin_shufflevector(a[i], none, 0, 1, 2, 3, 4, 5, 6, 7),
-                    __builtin_shufflevector(blo[j], XF == Q4MX_FP4 ? none : bhi[j], 0, 1, 2, 3, 4, 5, 6, 7), acc[i][j], 4,
-                    XF == Q4MX_FP4 ? 4 : 0, 0, sa[i], 0, sb[j]);
+                for (int j = 0; j < FT; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                        __builtin_shufflevector(a[i], none, 0, 1, 2, 3, 4, 5, 6, 7),
+                        __builtin_shufflevector(blo[j], none, 0, 1, 2, 3, 4, 5, 6, 7), acc[i][j], 4, 4, 0, sa[i], 0, sb[j]);
+        } else {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                bf16x8 xv[FT];
+#pragma unroll
+                for (int j = 0; j < FT; ++j) {
+                    const i32x4 b = q < 2 ? blo[j] : bhi[j];
+                    xv[j] = bf16_of_e4m3((uint32_t)b[2 * (q & 1)], (uint32_t)b[2 * (q & 1) + 1], scale_of((uint32_t)sb[j]));
+                }
+#pragma unroll
+                for (int i = 0; i < FN; ++i) {
+                    const bf16x8 wv = bf16_of_e2m1((uint32_t)a[i][q], scale_of((uint32_t)sa[i]));
+#pragma unroll
+                    for (int j = 0; j < FT; ++j)
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv, xv[j], acc[i][j], 0, 0, 0);
+                }
+            }
+        }
 #pragma unroll
         for (int i = 0; i < FN; ++i)
 #pragma unroll
@@ -392,9 +446,10 @@ __global__ __launch_bounds__(64 * WN* WT, 2) void k_mx_linear(MxMat x, MxMat w, 
 // Up to 16 tokens (a decoding step) are one fragment, and the weights' bytes
 // are all that counts: a work-group takes 16 outputs, its NW wavefronts every
 // NW-th slice of 128 columns, straight from memory into registers, and their
-// sums meet in shared memory (2048 -> 5632, one token: 4.2 us; its 6.1 MB at
-// the copy's rate are 1.2, the rest is a launch's and a load's latency).  The weights of two slices per wavefront are on
-// their way before x is looked at.  A BF16 x is quantized by the work-group, 8
+// sums meet in shared memory (2048 -> 5632, one token: 4.5 us; its 6.1 MB at
+// the copy's rate are 1.2, the rest is a launch's and a load's latency).  The
+// weights of two slices per wavefront are on their way before x is looked at.
+// E4M3 is multiplied as BF16, as above.  A BF16 x is quantized by the work-group, 8
 // columns to a lane, into shared memory (a slice of 16 rows x 128 codes, its
 // 16-byte pieces permuted by the row as in the large product); x in codes
 // comes from memory as the weights do.
@@ -433,11 +488,11 @@ template <int XF, int NW> __global__ __launch_bounds__(64 * NW) void k_mx_linear
                 const int n = r < x.tokens ? slices : 0;
                 const auto bx = readable(x.mx.codes, x.mx.rows * x.mx.slices * kRow);
                 const auto bxs = readable(x.mx.scales, x.mx.slices * x.mx.rows * 4);
-                const uint32_t o = (uint32_t)(r * x.mx.slices + s) * kRow + g * 16;
+                const uint32_t o = (uint32_t)(r * x.mx.slices + s) * kRow + g * (kRow / 4);
                 lo[k] = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(bx, (int)inside(o, s, n), 0, 0));
                 hi[k] = none;
                 if (XF == Q4MX_FP8)
-                    hi[k] = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(bx, (int)inside(o + 64, s, n), 0, 0));
+                    hi[k] = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(bx, (int)inside(o + 16, s, n), 0, 0));
                 sx[k] = __builtin_amdgcn_raw_buffer_load_b8(
                     bxs, (int)inside(((uint32_t)s * (uint32_t)x.mx.rows + r) * 4 + g, s, n), 0, 0);
             }
@@ -463,17 +518,28 @@ template <int XF, int NW> __global__ __launch_bounds__(64 * NW) void k_mx_linear
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) {
                 const char* const p = xcodes + (k * NW + wave) * 2048 + r * 128;
-                lo[k] = *reinterpret_cast<const i32x4*>(p + ((g ^ (r & 7)) * 16));
-                hi[k] = *reinterpret_cast<const i32x4*>(p + (((4 + g) ^ (r & 7)) * 16));
+                lo[k] = *reinterpret_cast<const i32x4*>(p + (((2 * g) ^ (r & 7)) * 16));
+                hi[k] = *reinterpret_cast<const i32x4*>(p + (((2 * g + 1) ^ (r & 7)) * 16));
                 sx[k] = xscales[((k * NW + wave) * 16 + r) * 4 + g];
             }
         }
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k)
-            acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                __builtin_shufflevector(a[k], none, 0, 1, 2, 3, 4, 5, 6, 7),
-                __builtin_shufflevector(lo[k], hi[k], 0, 1, 2, 3, 4, 5, 6, 7), acc, 4, XF == Q4MX_FP4 ? 4 : 0, 0, sa[k],
-                0, sx[k]);
+        for (int k = 0; k < kAhead; ++k) {
+            if (XF == Q4MX_FP4) {
+                acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                    __builtin_shufflevector(a[k], none, 0, 1, 2, 3, 4, 5, 6, 7),
+                    __builtin_shufflevector(lo[k], none, 0, 1, 2, 3, 4, 5, 6, 7), acc, 4, 4, 0, sa[k], 0, sx[k]);
+                continue;
+            }
+            const float sw = scale_of((uint32_t)sa[k] & 0xFFu), sv = scale_of((uint32_t)sx[k] & 0xFFu);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const i32x4 b = q < 2 ? lo[k] : hi[k];
+                acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                    bf16_of_e2m1((uint32_t)a[k][q], sw),
+                    bf16_of_e4m3((uint32_t)b[2 * (q & 1)], (uint32_t)b[2 * (q & 1) + 1], sv), acc, 0, 0, 0);
+            }
+        }
     }
     sums[wave][lane] = acc;
     __syncthreads();
@@ -518,26 +584,6 @@ __device__ __forceinline__ bf16x8 read_turned(const char* p, int pitch) {
     t.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Q4_LDS s16x4*)p);
     t.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Q4_LDS s16x4*)(p + 4 * pitch));
     return t.v;
-}
-
-__device__ __forceinline__ uint32_t bf16_pair_of(uint32_t w, float s, int fmt, int k) {
-    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-    union {
-        bf16x2 v;
-        uint32_t u;
-    } t;
-    if (fmt == Q4MX_FP4) {
-        switch (k) {
-        case 0: t.v = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 0); break;
-        case 1: t.v = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 1); break;
-        case 2: t.v = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 2); break;
-        default: t.v = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3); break;
-        }
-    } else {
-        t.v = k == 0 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, s, false)
-                     : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, s, true);
-    }
-    return t.u;
 }
 
 // The dense operand: dgrad's rows d, or wgrad's (TURNED) rows k, 16-byte
@@ -875,10 +921,11 @@ __global__ __launch_bounds__(64 * W0* W1) void k_mx_join(Cut cut, Out out) {
 // time: rounds of work-groups times steps, plus what the runs' sums cost to
 // write, read and join.  The constants are fits to such measurements.
 struct TileCost {
-    double step;  // microseconds of a step with every unit busy
-    double ends;  // of a work-group's start and end
+    double step;   // microseconds of a step with every slot taken
+    double alone;  // with one work-group on a unit
+    double ends;   // of a work-group's start and end
 };
-constexpr double kPartBytesPerUs = 4.0e6, kJoinUs = 6.0;
+constexpr double kPartBytesPerUs = 4.0e6;
 
 struct Plan {
     bool big;
@@ -888,7 +935,7 @@ struct Plan {
 
 int64_t tiles(int64_t n, int64_t b) { return (n + b - 1) / b; }
 
-Plan plan_of(int64_t n0, int64_t n1, int64_t steps, const TileCost& big, const TileCost& small) {
+Plan plan_of(int64_t n0, int64_t n1, int64_t steps, const TileCost& big, const TileCost& small, double join_us) {
     Plan best{};
     double best_us = 0;
     for (int k = 0; k < 2; ++k) {
@@ -900,8 +947,8 @@ Plan plan_of(int64_t n0, int64_t n1, int64_t steps, const TileCost& big, const T
             const int64_t rounds = tiles(rest * split, slots);
             const size_t bytes = split == 1 ? 0 : (size_t)(rest * split * b * b * 4);
             double us = (double)(full / slots) * ((double)steps * c.step + c.ends) +
-                        (double)rounds * ((double)tiles(steps, split) * c.step + c.ends);
-            if (split > 1) us += kJoinUs + 2.0 * (double)bytes / kPartBytesPerUs;
+                        (double)rounds * ((double)tiles(steps, split) * (rest * split <= 256 ? c.alone : c.step) + c.ends);
+            if (split > 1) us += join_us + 2.0 * (double)bytes / kPartBytesPerUs;
             if (best.cut.n0 == 0 || us < best_us) {
                 best_us = us;
                 best = Plan{k == 0, Cut{(uint32_t)t0, (uint32_t)t1, (uint32_t)full, (uint32_t)rest, (uint32_t)split, nullptr},
@@ -913,11 +960,12 @@ Plan plan_of(int64_t n0, int64_t n1, int64_t steps, const TileCost& big, const T
 }
 
 Plan linear_plan(const MxMat& x, const MxMat& w) {
-    return x.fmt == Q4MX_FP4 ? plan_of(w.rows, x.rows, w.slices, TileCost{1.0, 4}, TileCost{0.65, 4})
-                             : plan_of(w.rows, x.rows, w.slices, TileCost{1.5, 4}, TileCost{0.95, 4});
+    return x.fmt == Q4MX_FP4
+               ? plan_of(w.rows, x.rows, w.slices, TileCost{1.0, 1.0, 4}, TileCost{0.65, 0.65, 4}, 6.0)
+               : plan_of(w.rows, x.rows, w.slices, TileCost{2.6, 2.6, 6}, TileCost{1.45, 1.05, 5}, 3.0);
 }
 Plan grad_plan(const MxMat& m, int64_t width) {
-    return plan_of(m.cols, width, tiles(m.rows, 64), TileCost{1.7, 4}, TileCost{1.1, 3});
+    return plan_of(m.cols, width, tiles(m.rows, 64), TileCost{1.7, 1.7, 4}, TileCost{1.1, 1.1, 3}, 6.0);
 }
 
 template <bool TURNED, int FMT, bool SWAP>
