@@ -11,6 +11,9 @@ namespace {
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef short s16x2 __attribute__((ext_vector_type(2)));
 
+// The work-group's number in a grid_of grid.
+__device__ __forceinline__ uint32_t group_index() { return blockIdx.y * gridDim.x + blockIdx.x; }
+
 // 2^(e-127): the FP32 with that biased exponent, subnormal for e = 0.  For e
 // = 255 the bits are those of an infinity; the conversions read the exponent
 // field alone and give NaN.

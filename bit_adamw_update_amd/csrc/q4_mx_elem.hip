@@ -31,7 +31,7 @@ struct Lane {
 };
 
 __device__ __forceinline__ Lane lane_of(int64_t slices, int pass) {
-    const uint32_t rt = blockIdx.x / (uint32_t)slices, slice = blockIdx.x - rt * (uint32_t)slices;
+    const uint32_t id = group_index(), rt = id / (uint32_t)slices, slice = id - rt * (uint32_t)slices;
     return Lane{(int64_t)rt * kTileRows + pass * 16 + (threadIdx.x >> 4), (int64_t)slice * 128 + (threadIdx.x & 15) * 8};
 }
 
@@ -57,8 +57,9 @@ __global__ __launch_bounds__(256) void k_mx_quantize_t(const void* src, int64_t 
     constexpr int kBytes = FMT == Q4MX_FP4 ? 16 : 32;  // codes of a block
     __shared__ __attribute__((aligned(16))) uint8_t lds[64][4 * kBytes + 16];
     __shared__ __attribute__((aligned(4))) uint8_t lds_scale[64][4];
-    const uint32_t st = blockIdx.x / (uint32_t)ctiles;
-    const int64_t slice = st, c0 = (int64_t)(blockIdx.x - st * (uint32_t)ctiles) * 64;
+    const uint32_t id = group_index(), st = id / (uint32_t)ctiles;
+    const int64_t slice = st, c0 = (int64_t)(id - st * (uint32_t)ctiles) * 64;
+    if (slice >= out.slices) return;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t r0 = slice * 128 + wave * 32, c = c0 + lane;
     float v[32];
@@ -200,21 +201,21 @@ hipError_t launch_mx_quantize(const Dense& src, bool transpose, const MxMat& out
     const bool bf = src.dtype == Q4MX_BF16;
     if (transpose) {
         const int64_t ctiles = (out.rows + 63) / 64;
-        const dim3 g((unsigned)(ctiles * out.slices)), b(256);
+        const dim3 g = grid_of(ctiles * out.slices), b(256);
         if (bf && out.fmt == Q4MX_FP4) k_mx_quantize_t<true, Q4MX_FP4><<<g, b, 0, st>>>(src.p, src.ld, out, ctiles);
         else if (bf) k_mx_quantize_t<true, Q4MX_FP8><<<g, b, 0, st>>>(src.p, src.ld, out, ctiles);
         else if (out.fmt == Q4MX_FP4) k_mx_quantize_t<false, Q4MX_FP4><<<g, b, 0, st>>>(src.p, src.ld, out, ctiles);
         else k_mx_quantize_t<false, Q4MX_FP8><<<g, b, 0, st>>>(src.p, src.ld, out, ctiles);
         return hipGetLastError();
     }
-    const dim3 g((unsigned)row_tiles(out.rows, out.slices)), b(256);
+    const dim3 g = grid_of(row_tiles(out.rows, out.slices)), b(256);
     if (bf) k_mx_quantize<true><<<g, b, 0, st>>>(src.p, src.ld, out);
     else k_mx_quantize<false><<<g, b, 0, st>>>(src.p, src.ld, out);
     return hipGetLastError();
 }
 
 hipError_t launch_mx_dequantize(const MxMat& a, const Dense& dst, hipStream_t st) {
-    const dim3 g((unsigned)row_tiles(a.rows, a.slices)), b(256);
+    const dim3 g = grid_of(row_tiles(a.rows, a.slices)), b(256);
     if (dst.dtype == Q4MX_BF16) k_mx_dequantize<true><<<g, b, 0, st>>>(a, dst.p, dst.ld);
     else k_mx_dequantize<false><<<g, b, 0, st>>>(a, dst.p, dst.ld);
     return hipGetLastError();
@@ -223,7 +224,7 @@ hipError_t launch_mx_dequantize(const MxMat& a, const Dense& dst, hipStream_t st
 hipError_t launch_act_forward(int act, const Dense& x, const Dense& up, int64_t rows, int64_t cols, const Dense& y,
                               const MxMat& y_mx, const MxMat& kx, const MxMat& ku, hipStream_t st) {
     const int64_t slices = (cols + kMxPad - 1) / kMxPad;
-    const dim3 g((unsigned)row_tiles(rows, slices)), b(256);
+    const dim3 g = grid_of(row_tiles(rows, slices)), b(256);
 #define Q4_ACT_FWD(A) \
     k_act_forward<A><<<g, b, 0, st>>>(x.p, x.ld, up.p, up.ld, rows, cols, slices, y.p, y.ld, y_mx, kx, ku)
     if (act == Q4MX_GELU) Q4_ACT_FWD(Q4MX_GELU);
@@ -235,7 +236,7 @@ hipError_t launch_act_forward(int act, const Dense& x, const Dense& up, int64_t 
 
 hipError_t launch_act_backward(int act, const MxMat& kx, const MxMat& ku, const Dense& dy, const Dense& dx,
                                const Dense& dup, hipStream_t st) {
-    const dim3 g((unsigned)row_tiles(kx.rows, kx.slices)), b(256);
+    const dim3 g = grid_of(row_tiles(kx.rows, kx.slices)), b(256);
 #define Q4_ACT_BWD(A) k_act_backward<A><<<g, b, 0, st>>>(kx, ku, dy.p, dy.ld, dx.p, dx.ld, dup.p, dup.ld)
     if (act == Q4MX_GELU) Q4_ACT_BWD(Q4MX_GELU);
     else if (act == Q4MX_GELU_ERF) Q4_ACT_BWD(Q4MX_GELU_ERF);

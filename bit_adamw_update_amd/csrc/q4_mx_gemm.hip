@@ -216,6 +216,19 @@ Out result(const Dense& d, int64_t rows, int64_t cols, bool add) {
     return Out{d.p, d.ld, rows, cols, d.dtype == Q4MX_BF16, add};
 }
 
+// A product over no columns.
+__global__ __launch_bounds__(256) void k_mx_zero(Out o) {
+    for (int64_t r = blockIdx.y; r < o.rows; r += gridDim.y)
+        for (int64_t c = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; c < o.cols; c += (int64_t)gridDim.x * 1024)
+            put4(o, r, c, f32x4{0, 0, 0, 0});
+}
+
+hipError_t zero(const Out& o, hipStream_t st) {
+    const int64_t along = std::min((o.cols + 1023) / 1024, int64_t(2048));
+    k_mx_zero<<<dim3((unsigned)along, (unsigned)std::min(o.rows, int64_t(1024))), dim3(256), 0, st>>>(o);
+    return hipGetLastError();
+}
+
 // ---- linear ---------------------------------------------------------------------
 //
 // A work-group of WN x WT wavefronts forms BN outputs x BT tokens; a wavefront
@@ -867,7 +880,7 @@ __global__ __launch_bounds__(64 * WC* WD, 2) void k_mx_grad(Gradient a, MxMat m,
 // lanes to a row.
 __global__ __launch_bounds__(256) void k_align_rows(const uint16_t* src, int64_t ld, int64_t rows, int64_t cols,
                                                      uint4* dst, int64_t pieces) {
-    const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int64_t row = (int64_t)group_index() * 8 + (threadIdx.x >> 5);
     if (row >= rows) return;
     for (int64_t i = threadIdx.x & 31; i < pieces; i += 32) {
         const uint16_t* p = src + row * ld + i * 8;
@@ -985,18 +998,13 @@ hipError_t grad(const Gradient& a, const MxMat& m, const Out& out, void* ws, hip
 }
 
 template <int XF> hipError_t linear(const MxMat& x, const MxMat& w, const Out& y, void* ws, hipStream_t st) {
-    Plan p = linear_plan(x, w);
-    if (w.slices == 0) p.cut = Cut{p.cut.n0, p.cut.n1, 0, p.cut.n0 * p.cut.n1, 0, nullptr};  // joins no runs: zeros
+    const Plan p = linear_plan(x, w);
     Cut cut = p.cut;
     cut.part = static_cast<f32x4*>(ws);
     const uint32_t units = cut.full + cut.rest * cut.split;
     const dim3 joins(cut.rest * (p.big ? 32 : 16));
-    if (units == 0) {
-    } else if (p.big) {
-        k_mx_linear<XF, 2, 4, 8, 4><<<dim3(std::min(units, 256u)), dim3(512), 0, st>>>(x, w, y, cut);
-    } else {
-        k_mx_linear<XF, 2, 2, 4, 4><<<dim3(std::min(units, 512u)), dim3(256), 0, st>>>(x, w, y, cut);
-    }
+    if (p.big) k_mx_linear<XF, 2, 4, 8, 4><<<dim3(std::min(units, 256u)), dim3(512), 0, st>>>(x, w, y, cut);
+    else k_mx_linear<XF, 2, 2, 4, 4><<<dim3(std::min(units, 512u)), dim3(256), 0, st>>>(x, w, y, cut);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || cut.split == 1) return e;
     if (p.big) k_mx_join<2, 4, 8, 4, false, true><<<joins, dim3(512), 0, st>>>(cut, y);
@@ -1009,8 +1017,7 @@ hipError_t aligned_gradient(const Dense& dy, int64_t rows, int64_t cols, void* c
     *g = Gradient{static_cast<const uint16_t*>(dy.p), dy.ld, cols, 0};
     const int64_t pieces = tiles(cols, 8);
     if (!dense_needs_copy(dy, rows, cols) || rows * pieces == 0) return hipSuccess;
-    k_align_rows<<<dim3((unsigned)tiles(rows, 8)), dim3(256), 0, st>>>(g->p, dy.ld, rows, cols,
-                                                                     static_cast<uint4*>(copy), pieces);
+    k_align_rows<<<grid_of(tiles(rows, 8)), dim3(256), 0, st>>>(g->p, dy.ld, rows, cols, static_cast<uint4*>(copy), pieces);
     *g = Gradient{static_cast<const uint16_t*>(copy), pieces * 8, pieces * 8, 0};
     return hipGetLastError();
 }
@@ -1023,7 +1030,7 @@ template <int XF> hipError_t few(const Few& x, const MxMat& w, const Out& y, hip
     const int64_t groups = tiles(w.rows, 16);
     int waves = 4;
     while (waves < 16 && w.slices >= 4 * waves && groups * waves < 2048) waves *= 2;
-    const dim3 g((unsigned)groups);
+    const dim3 g((unsigned)groups);  // w.rows < 2^27: at most 2^31 threads
     if (waves == 4) k_mx_linear_few<XF, 4><<<g, dim3(256), 0, st>>>(x, w, y);
     else if (waves == 8) k_mx_linear_few<XF, 8><<<g, dim3(512), 0, st>>>(x, w, y);
     else k_mx_linear_few<XF, 16><<<g, dim3(1024), 0, st>>>(x, w, y);
@@ -1043,12 +1050,14 @@ size_t linear_workspace(const MxMat& x, const MxMat& w) {
 size_t grad_workspace(const MxMat& m, int64_t width) { return grad_plan(m, width).bytes; }
 
 hipError_t launch_linear_few(const Dense& x, int64_t tokens, const MxMat& w, const Dense& y, hipStream_t st) {
-    return few<kFromBf16>(Few{MxMat{}, static_cast<const uint16_t*>(x.p), x.ld, tokens, w.cols}, w,
-                          result(y, tokens, w.rows, false), st);
+    const Out out = result(y, tokens, w.rows, false);
+    if (w.slices == 0) return zero(out, st);
+    return few<kFromBf16>(Few{MxMat{}, static_cast<const uint16_t*>(x.p), x.ld, tokens, w.cols}, w, out, st);
 }
 
 hipError_t launch_linear(const MxMat& x, const MxMat& w, const Dense& y, void* ws, hipStream_t st) {
     const Out out = result(y, x.rows, w.rows, false);
+    if (w.slices == 0) return zero(out, st);
     if (x.rows <= Q4MX_FEW_TOKENS) {
         const Few f{x, nullptr, 0, x.rows, x.cols};
         return x.fmt == Q4MX_FP4 ? few<Q4MX_FP4>(f, w, out, st) : few<Q4MX_FP8>(f, w, out, st);

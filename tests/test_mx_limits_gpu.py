@@ -1,0 +1,166 @@
+"""The microscaled calls at the ends of their ranges: more work-groups than one
+launch dimension takes (2^32 threads), results over no inputs, operands past 4
+GiB.  Values are such that every result is exact, or are compared with the same
+call on pieces, whose sizes other tests cover."""
+import pytest
+import torch
+
+from bit_adamw_update_amd import mx
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+def _room(gib):
+    torch.cuda.empty_cache()
+    free = torch.cuda.mem_get_info()[0] >> 30
+    if free < gib:
+        pytest.skip(f"{gib} GiB of GPU memory needed, {free} free")
+
+
+def _bits(shape, seed):
+    """BF16 values of random sign and mantissa, exponents 2^-3 .. 2^4 (any
+    16-bit pattern built in place: no wide copies)."""
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    u = torch.randint(0, 1 << 11, shape, dtype=torch.int16, device=DEV, generator=g)   # sign, 3 exponent, 7 mantissa bits
+    u = ((u & 0x400) << 5) | ((u & 0x3FF) + (124 << 7))
+    return u.view(torch.bfloat16)
+
+
+def test_input_gradient_of_many_rows():
+    """2^27 + 5 tokens through a 1 x 1 weight: dy's rows are copied to 16 bytes
+    each first, 8 rows to a work-group."""
+    _room(8)
+    print("dgrad 2^27 + 5", flush=True)
+    dy = _bits(((1 << 27) + 5, 1), 1)
+    w = mx.quantize(torch.tensor([[1.5]], device=DEV), "fp4")
+    dx = mx.linear_dgrad(dy, w)
+    assert torch.equal(dx, (dy.float() * 1.5).to(torch.bfloat16))
+
+
+ONE_ROW = (1 << 31) - 64   # 2^24 slices of 128 columns, 256 threads each
+
+
+def _same(m, part, at):
+    n = part.codes.shape[1]
+    return (torch.equal(m.codes[:, at:at + n], part.codes)
+            and torch.equal(m.scales[at // 128:at // 128 + part.scales.shape[0]], part.scales))
+
+
+def test_one_row_of_2_31_columns():
+    _room(40)
+    print("one row", flush=True)
+    x = _bits((1, ONE_ROW), 2)
+    m = mx.quantize(x, "fp8")
+    turned = mx.quantize(x.view(-1, 1), "fp8", transpose=True)
+    assert torch.equal(m.codes, turned.codes) and torch.equal(m.scales, turned.scales)
+    del turned
+    back = mx.dequantize(m)
+    y, kept = mx.act_forward("gelu", x)
+    assert torch.equal(kept[0].codes, m.codes) and torch.equal(kept[0].scales, m.scales)
+    dx = mx.act_backward("gelu", kept, x)[0]
+    step = 1 << 29
+    for at in range(0, ONE_ROW, step):
+        piece = x[:, at:at + step]
+        part = mx.quantize(piece, "fp8")
+        assert _same(m, part, at), at
+        assert torch.equal(back[:, at:at + step], mx.dequantize(part)), at
+        yp, kp = mx.act_forward("gelu", piece)
+        assert torch.equal(y[:, at:at + step], yp), at
+        assert torch.equal(dx[:, at:at + step], mx.act_backward("gelu", kp, piece)[0]), at
+
+
+@pytest.mark.parametrize("tokens,outs", [(1, 1 << 28), (17, 1 << 27), (3, 5), (40, 300)])
+def test_products_over_no_inputs(tokens, outs):
+    """Zeros, from either form of x, whatever the result held."""
+    _room(20)
+    print("no inputs", tokens, outs, flush=True)
+    w = mx.MXMatrix(outs, 0, "fp4")
+    e = torch.empty(tokens, 0, dtype=torch.bfloat16, device=DEV)
+    y = torch.full((tokens, outs), 5.0, dtype=torch.bfloat16, device=DEV)
+    mx.linear(e, w, out=y)
+    assert not bool(y.any())
+    y.fill_(5.0)
+    mx.linear(mx.quantize(e, "fp8"), w, out=y)
+    assert not bool(y.any())
+
+
+def test_zeros_leave_the_gaps_of_a_result():
+    buf = torch.full((21, 40), 7.0, device=DEV)
+    mx.linear(torch.empty(21, 0, dtype=torch.bfloat16, device=DEV), mx.MXMatrix(33, 0, "fp4"), out=buf[:, 2:35])
+    assert not bool(buf[:, 2:35].any()) and bool((buf[:, :2] == 7).all()) and bool((buf[:, 35:] == 7).all())
+
+
+# ---- operands past 4 GiB -------------------------------------------------------
+
+def _some(n):
+    return torch.tensor(sorted({0, 1, 127, 128, 255, 256, n // 3, n // 2, n - 257, n - 129, n - 2, n - 1}), device=DEV)
+
+
+def _exact_codes(rows, cols, fmt, seed):
+    """A matrix of codes 0, +-1, +-2 (scale 1): products and sums are whole numbers."""
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    m = mx.MXMatrix(rows, cols, fmt)
+    table = (torch.tensor([0, 2, 4, 10, 12], dtype=torch.uint8) if fmt == "fp4"
+             else torch.tensor([0, 0x38, 0x40, 0xB8, 0xC0], dtype=torch.uint8)).to(DEV)
+    step = max(1, (1 << 28) // m.codes.shape[1])
+    for at in range(0, rows, step):
+        part = m.codes[at:at + step]
+        c = table[torch.randint(0, 5, part.shape, device=DEV, generator=g)]
+        if fmt == "fp4":
+            c |= table[torch.randint(0, 5, part.shape, device=DEV, generator=g)] << 4
+        part.copy_(c)
+    m.scales.fill_(127)
+    assert cols % 128 == 0
+    return m
+
+
+def _rows_of(m, rows):
+    """Those rows of m as FP32 values, decoded apart."""
+    part = mx.MXMatrix(len(rows), m.cols, m.format, codes=m.codes[rows].contiguous(),
+                       scales=m.scales[:, rows].contiguous())
+    return mx.dequantize(part, torch.float32)
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "fp4"])
+def test_linear_past_4_gib(fmt):
+    """Codes of x past 2^32 bytes, w small, and the other way round (w is E2M1)."""
+    _room(40)
+    print("linear past 4 GiB", fmt, flush=True)
+    tokens, cin = (1 << 32) // (8192 if fmt == "fp8" else 4096) + 300, 8192
+    x, w = _exact_codes(tokens, cin, fmt, 3), _exact_codes(40, cin, "fp4", 4)
+    assert x.codes.numel() > 1 << 32
+    y = mx.linear(x, w, dtype=torch.float32)
+    pick = _some(tokens)
+    want = _rows_of(x, pick) @ mx.dequantize(w, torch.float32).t()
+    assert torch.equal(y[pick], want)
+    if fmt == "fp4":
+        few = _exact_codes(5, cin, "fp8", 5)
+        for a in (few, w):
+            y = mx.linear(a, x, dtype=torch.float32)
+            assert torch.equal(y[:, pick], mx.dequantize(a, torch.float32) @ _rows_of(x, pick).t())
+
+
+def test_gradients_past_4_gib():
+    """dy and the code matrix past 2^32 bytes."""
+    _room(60)
+    print("gradients past 4 GiB", flush=True)
+    cin, cout = 8192, 256
+    tokens = (1 << 32) // 8192 + 300
+    x, w = _exact_codes(tokens, cin, "fp8", 6), _exact_codes(cout, 384, "fp4", 7)
+    g = torch.Generator(device=DEV).manual_seed(8)
+    # 2^23 columns' worth of row stride is not needed: rows of 4608 elements, 4.8 GB
+    buf = torch.zeros(tokens, 4608, dtype=torch.bfloat16, device=DEV)
+    dy = buf[:, 8:8 + cout]
+    # few rows are not zero, so that the sums over tokens are small whole numbers
+    pick = _some(tokens)
+    dy[pick] = torch.randint(-3, 4, (len(pick), cout), device=DEV, generator=g).to(torch.bfloat16)
+    assert buf.numel() * 2 > 1 << 32
+    dx = mx.linear_dgrad(dy, w, dtype=torch.float32)
+    assert torch.equal(dx[pick], dy[pick].float() @ mx.dequantize(w, torch.float32))
+    dx[pick] = 0
+    assert not bool(dx.any())
+    want = dy[pick].float().t() @ _rows_of(x, pick)
+    for transposed in (False, True):
+        dw = mx.linear_wgrad(dy, x, transposed=transposed, dtype=torch.float32)
+        assert torch.equal(dw.t() if transposed else dw, want)
