@@ -14,9 +14,18 @@ A linear layer beside ``Q4State``, for a master stored [in, out]::
     dx = mx.linear_dgrad(dy, w)
     mx.linear_wgrad(dy, xq, out=grad, transposed=True)   # the BF16 gradient
 
-The calls run on ``stream`` (a torch stream), or on the current stream of
-their operands' device.  They are not recorded by autograd: the backward
-calls are the layer's backward pass.
+The calls run on the current stream of their operands' device, or on
+``stream`` (a torch stream of that device).  As with ``torch.cuda.stream``,
+nothing is ordered: the caller lets ``stream`` wait for whatever made the
+operands (``stream.wait_stream(torch.cuda.current_stream())``), and lets other
+streams wait for it before they use the results.  Memory is held: operands may
+be dropped as soon as the call returns, and results as soon as the work that
+uses them is queued on ``stream`` or on the stream that was current at the
+call.  For any other stream, ``record_stream`` of the tensors and of
+``MXMatrix`` tells the allocator.
+
+The calls are not recorded by autograd: the backward calls are the layer's
+backward pass.
 """
 from __future__ import annotations
 
@@ -105,6 +114,13 @@ class MXMatrix:
     def shape(self) -> tuple:
         return (self.rows, self.cols)
 
+    def record_stream(self, stream) -> None:
+        """torch.Tensor.record_stream of the codes and scales: their memory,
+        once freed, is not used again before the work queued on stream by then
+        is done."""
+        for t in (self._codes, self._scales) if self._buf is None else (self._buf,):
+            t.record_stream(stream)
+
     def __repr__(self) -> str:
         return f"MXMatrix({self.rows} x {self.cols}, {self.format!r}, device='{self.device}')"
 
@@ -166,13 +182,28 @@ def _elsewhere(device, stream) -> bool:
     return stream is not None or torch._C._cuda_getDevice() != device.index
 
 
-def _on(device, stream):
-    """The device and stream of a call as a context."""
+def _entered(device, stream, operands, call, *args):
+    """call(*args) on `device`, or on `stream`.  The allocator knows the stream
+    a tensor was made on; the other one that uses it is recorded."""
     if stream is None:
-        return torch.cuda.device(device)
+        with torch.cuda.device(device):
+            return call(*args)
     if stream.device != device:
         raise ValueError(f"the stream is on {stream.device}, the operands on {device}")
-    return torch.cuda.stream(stream)   # makes the stream's device current
+    caller = torch.cuda.current_stream(device)
+    with torch.cuda.stream(stream):   # makes the stream's device current
+        results = call(*args)
+    _hold(operands, stream)
+    _hold(results, caller)
+    return results
+
+
+def _hold(held, stream):
+    if isinstance(held, tuple):
+        for h in held:
+            _hold(h, stream)
+    elif held is not None:
+        held.record_stream(stream)
 
 
 def _raw(device) -> int:
@@ -195,8 +226,7 @@ def quantize(src, format: str, transpose: bool = False, out: MXMatrix | None = N
     if out is not None:
         _same_device(src, out)
     if _elsewhere(device, stream):
-        with _on(device, stream):
-            return quantize(src, format, transpose, out)
+        return _entered(device, stream, (src, out), quantize, src, format, transpose, out)
     rows, cols = src.shape[::-1] if transpose else src.shape
     out = _mx_result(out, rows, cols, format, device)
     api.q4mx_quantize(src.data_ptr(), _DTYPES[src.dtype], ld, transpose, out.packed, _raw(device))
@@ -209,8 +239,7 @@ def dequantize(a: MXMatrix, dtype=torch.bfloat16, out=None, stream=None) -> torc
     if out is not None:
         _same_device(a, out)
     if _elsewhere(device, stream):
-        with _on(device, stream):
-            return dequantize(a, dtype, out)
+        return _entered(device, stream, (a, out), dequantize, a, dtype, out)
     out, code, ld = _result(out, (a.rows, a.cols), dtype, device)
     api.q4mx_dequantize(a.packed, out.data_ptr(), code, ld, _raw(device))
     return out
@@ -226,8 +255,7 @@ def linear(x, w: MXMatrix, out=None, dtype=torch.bfloat16, stream=None) -> torch
         if x.shape[1] != w.cols:
             raise ValueError(f"x has {x.shape[1]} columns, w has {w.cols}")
     if _elsewhere(device, stream):
-        with _on(device, stream):
-            return linear(x, w, out, dtype)
+        return _entered(device, stream, (x, w, out), linear, x, w, out, dtype)
     tokens = x.rows if coded else x.shape[0]
     out, code, ld = _result(out, (tokens, w.rows), dtype, device)
     need = 0
@@ -250,8 +278,7 @@ def linear_dgrad(dy, w: MXMatrix, out=None, dtype=torch.bfloat16, stream=None) -
     if n != w.rows:
         raise ValueError(f"dy has {n} columns, w has {w.rows} rows")
     if _elsewhere(device, stream):
-        with _on(device, stream):
-            return linear_dgrad(dy, w, out, dtype)
+        return _entered(device, stream, (dy, w, out), linear_dgrad, dy, w, out, dtype)
     out, code, ld = _result(out, (tokens, w.cols), dtype, device)
     at = dy.data_ptr()
     need = api.q4mx_dgrad_workspace_bytes(at, lddy, tokens, w.packed)
@@ -271,8 +298,7 @@ def linear_wgrad(dy, x: MXMatrix, out=None, transposed: bool = False, accumulate
     if accumulate and out is None:
         raise ValueError("accumulate needs out")
     if _elsewhere(device, stream):
-        with _on(device, stream):
-            return linear_wgrad(dy, x, out, transposed, accumulate, dtype)
+        return _entered(device, stream, (dy, x, out), linear_wgrad, dy, x, out, transposed, accumulate, dtype)
     flags = (api.MX_WGRAD_TRANSPOSED if transposed else 0) | (api.MX_WGRAD_ADD if accumulate else 0)
     out, code, ld = _result(out, (x.cols, n) if transposed else (n, x.cols), dtype, device)
     at = dy.data_ptr()
@@ -305,8 +331,7 @@ def act_forward(kind: str, x, up=None, out_format: str | None = None, stream=Non
     if out_format is not None and out_format not in FORMATS:
         raise ValueError(f"unknown format {out_format!r}; expected one of {sorted(FORMATS)}")
     if _elsewhere(device, stream):
-        with _on(device, stream):
-            return act_forward(kind, x, up, out_format)
+        return _entered(device, stream, (x, up), act_forward, kind, x, up, out_format)
     rows, cols = x.shape
     y_at = y_mx = None
     if out_format is None:
@@ -335,8 +360,7 @@ def act_backward(kind: str, kept, dy, stream=None) -> tuple:
         raise ValueError(f"dy must have shape {shape}, not {tuple(dy.shape)}")
     device = _same_device(dy, kept_x, kept_up)
     if _elsewhere(device, stream):
-        with _on(device, stream):
-            return act_backward(kind, kept, dy)
+        return _entered(device, stream, (kept_x, kept_up, dy), act_backward, kind, kept, dy)
     ld = max(1, shape[1])
     dx = torch.empty(shape, dtype=torch.bfloat16, device=device)
     dup = None if kept_up is None else torch.empty(shape, dtype=torch.bfloat16, device=device)
