@@ -25,13 +25,17 @@ call.  For any other stream, ``record_stream`` of the tensors and of
 ``MXMatrix`` tells the allocator.
 
 The calls are not recorded by autograd: the backward calls are the layer's
-backward pass.
+backward pass.  A dense operand or result whose gradient would be lost (it
+requires one and gradients are recorded, or it carries a forward tangent) is
+refused, except by ``quantize``: call under ``torch.no_grad()``, from a
+``torch.autograd.Function``, or with ``x.detach()``.
 """
 from __future__ import annotations
 
 import struct
 
 import torch
+from torch.autograd import forward_ad
 
 from . import api
 
@@ -125,12 +129,21 @@ class MXMatrix:
         return f"MXMatrix({self.rows} x {self.cols}, {self.format!r}, device='{self.device}')"
 
 
-def _dense(name, t, dtypes=(torch.bfloat16,)):
+def _lost_gradient(t) -> bool:
+    """Whether autograd expects to see what is done with t."""
+    if t.requires_grad and torch.is_grad_enabled():
+        return True
+    return forward_ad._current_level >= 0 and forward_ad.unpack_dual(t).tangent is not None
+
+
+def _dense(name, t, dtypes=(torch.bfloat16,), recorded=True):
     """A 2-D GPU tensor with consecutive columns; returns its row stride."""
     if not isinstance(t, torch.Tensor) or t.dim() != 2:
         raise ValueError(f"{name} must be a 2-D tensor")
     if t.dtype not in dtypes:
         raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, not {t.dtype}")
+    if recorded and _lost_gradient(t):
+        raise ValueError(f"{name} has a gradient, which autograd would lose here; call under torch.no_grad() or detach it")
     if not t.is_cuda:
         raise ValueError(f"{name} must be on a GPU")
     rows, cols = t.shape
@@ -219,7 +232,7 @@ def quantize(src, format: str, transpose: bool = False, out: MXMatrix | None = N
     """src (float32 or bfloat16) in a microscaled format, blocks along its
     columns; transpose: the quantized transpose, blocks along its rows (a
     weight whose master is stored [in, out])."""
-    ld = _dense("src", src, _BOTH)
+    ld = _dense("src", src, _BOTH, recorded=False)   # codes have no gradient; the products' calls give that of src
     if format not in FORMATS:
         raise ValueError(f"unknown format {format!r}; expected one of {sorted(FORMATS)}")
     device = src.device
