@@ -88,6 +88,10 @@ class MXMatrix:
             pointers = (codes.data_ptr(), scales.data_ptr())
         self.packed = _PACK(code, 0, rows, cols, *pointers)   # for the calls
 
+    def __reduce__(self):
+        # a copy or a pickled matrix describes its own memory, not this one's
+        return MXMatrix, (self.rows, self.cols, self.format, self.codes, self.scales)
+
     @property
     def desc(self) -> api.Q4MXMatrix:
         """The C description of the matrix."""
