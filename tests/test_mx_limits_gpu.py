@@ -164,3 +164,64 @@ def test_gradients_past_4_gib():
     for transposed in (False, True):
         dw = mx.linear_wgrad(dy, x, transposed=transposed, dtype=torch.float32)
         assert torch.equal(dw.t() if transposed else dw, want)
+
+
+# ---- the widest products, the largest results --------------------------------------
+# Sums of 2^23 products of at most 6 and random sign stay far below 2^24 (their
+# standard deviation is below 2^23.5 / 2 * 2.4 < 2^13): whole numbers, exact.
+
+WIDEST = (1 << 23) - 128
+
+
+def _small(rows, cols, seed):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    return torch.randint(-3, 4, (rows, cols), device=DEV, generator=g, dtype=torch.int8).to(torch.bfloat16)
+
+
+@pytest.mark.parametrize("fmt,tokens", [("fp8", 140), ("fp4", 140), ("fp8", 5), ("fp4", 5)])
+def test_linear_of_the_widest_inputs(fmt, tokens):
+    _room(40)
+    print("widest linear", fmt, tokens, flush=True)
+    x, w = _exact_codes(tokens, WIDEST, fmt, 10), _exact_codes(40, WIDEST, "fp4", 11)
+    want = mx.dequantize(x, torch.float32) @ mx.dequantize(w, torch.float32).t()
+    assert torch.equal(mx.linear(x, w, dtype=torch.float32), want)
+
+
+def test_gradients_of_the_widest():
+    _room(60)
+    print("widest gradients", flush=True)
+    w = _exact_codes(WIDEST, 128, "fp4", 12)
+    dy = _small(140, WIDEST, 13)
+    want = dy.float() @ mx.dequantize(w, torch.float32)
+    assert torch.equal(mx.linear_dgrad(dy, w, dtype=torch.float32), want)
+    del w, want
+    x = _exact_codes(140, 128, "fp8", 14)
+    want = dy.float().t() @ mx.dequantize(x, torch.float32)
+    assert torch.equal(mx.linear_wgrad(dy, x, dtype=torch.float32), want)
+    assert torch.equal(mx.linear_wgrad(dy, x, transposed=True, dtype=torch.float32), want.t())
+    del dy, want
+    x, dy = _exact_codes(140, WIDEST, "fp8", 15), _small(140, 40, 16)
+    want = dy.float().t() @ mx.dequantize(x, torch.float32)
+    for transposed in (False, True):
+        got = mx.linear_wgrad(dy, x, transposed=transposed, dtype=torch.float32)
+        assert torch.equal(got.t() if transposed else got, want)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_results_past_2_32_elements(dtype):
+    _room(60)
+    print("large results", dtype, flush=True)
+    rows, cols = 70001, 65536
+    pick, across = _some(rows), _some(cols)
+
+    def check(got, a, b):
+        assert got.numel() > 1 << 32
+        assert torch.equal(got[pick].float(), (a[pick] @ b.t()).to(dtype).float())
+        assert torch.equal(got[:, across].float(), (a @ b[across].t()).to(dtype).float())
+
+    x, w = _exact_codes(rows, 128, "fp8", 17), _exact_codes(cols, 128, "fp4", 18)
+    check(mx.linear(x, w, dtype=dtype), mx.dequantize(x, torch.float32), mx.dequantize(w, torch.float32))
+    dy, w = _small(rows, 64, 19), _exact_codes(64, cols, "fp4", 20)
+    check(mx.linear_dgrad(dy, w, dtype=dtype), dy.float(), mx.dequantize(w, torch.float32).t().contiguous())
+    dy, x = _small(64, rows, 21), _exact_codes(64, cols, "fp8", 22)
+    check(mx.linear_wgrad(dy, x, dtype=dtype), dy.float().t().contiguous(), mx.dequantize(x, torch.float32).t().contiguous())
