@@ -47,8 +47,9 @@ struct Unit {
 };
 
 // Tile number -> tile, in bands of 16 along the first axis: the 32 tiles that
-// run together on an XCD share rows of both operands (bands of 2, 4, 8 and 16:
-// dgrad 8192 342, 341, 339 and 334 us).
+// run together on an XCD share rows of both operands (bands of 2, 4, 8 and 16
+// differ by less than the runs do, 2%: linear, dgrad and wgrad of 8192 x 2560 x
+// 10240, 8192 x 10240 x 2560 and 4096 x 2048 x 5632).
 __device__ __forceinline__ void tile_at(const Cut& c, uint32_t id, uint32_t& i0, uint32_t& i1) {
     constexpr uint32_t kBand = 16;
     const uint32_t band = id / (kBand * c.n1), first = band * kBand, h = min(c.n0 - first, kBand);
@@ -275,10 +276,14 @@ __global__ __launch_bounds__(64 * WN* WT, 2) void k_mx_linear(MxMat x, MxMat w, 
         woff[j] = (uint32_t)((j * NW + wave) * 16 + lane / 4) * (uint32_t)wp +
                   ((lane & 3) ^ (((lane >> 3) & 1) | ((lane >> 5) << 1))) * 16;
 #pragma unroll
-    for (int j = 0; j < CX; ++j)
+    for (int j = 0; j < CX; ++j) {
+        // E4M3: first the even pieces of a row, then the odd ones, so that a
+        // lane's two (2 g and 2 g + 1) are read as pieces g and 4 + g
+        const int slot = (lane & 7) ^ (lane >> 3);
         xoff[j] = XF == Q4MX_FP4
                       ? (uint32_t)((j * NW + wave) * 16 + lane / 4) * (uint32_t)xp + ((lane & 3) ^ ((lane >> 3) & 3)) * 16
-                      : (uint32_t)((j * NW + wave) * 8 + lane / 8) * (uint32_t)xp + ((lane & 7) ^ (lane >> 3)) * 16;
+                      : (uint32_t)((j * NW + wave) * 8 + lane / 8) * (uint32_t)xp + ((slot & 3) * 2 + (slot >> 2)) * 16;
+    }
     // wavefronts 0 .. BN/64-1 copy the scales of w, the others those of x
     const bool xs = wave >= BN / 64;
     const int64_t srows = xs ? x.rows : w.rows;
@@ -324,8 +329,8 @@ __global__ __launch_bounds__(64 * WN* WT, 2) void k_mx_linear(MxMat x, MxMat w, 
     const int r = lane & 15, g = lane >> 4, wn = wave % WN, wt = wave / WN;
     const int wrow = wn * FN * 16 + (r >> 2) * 8 + (r & 3), xrow = wt * FT * 16 + r;
     const int wat = wrow * 64 + ((g ^ (((r >> 1) & 1) | (((r >> 2) & 1) << 1))) * 16);
-    const int xat = kW + xrow * XB + (XF == Q4MX_FP4 ? (g ^ ((r >> 1) & 3)) * 16 : ((2 * g) ^ (r & 7)) * 16);
-    const int xat2 = kW + xrow * XB + ((2 * g + 1) ^ (r & 7)) * 16;
+    const int xat = kW + xrow * XB + (XF == Q4MX_FP4 ? (g ^ ((r >> 1) & 3)) * 16 : (g ^ (r & 7)) * 16);
+    const int xat2 = kW + xrow * XB + ((4 + g) ^ (r & 7)) * 16;
     const int wsat = kW + kX + wrow * 4 + g, xsat = kW + kX + BN * 4 + xrow * 4 + g;
 
     f32x4 acc[FN][FT] = {};
@@ -585,10 +590,12 @@ template <int XF, int NW> __global__ __launch_bounds__(64 * NW) void k_mx_linear
 // (half a step), the other reads fragments.  Three steps of the dense operand
 // and two of the codes are in rings (160 KB in all).
 //
-// dgrad 8192 x 2560 x 10240: 342 us, 1.25 PFLOP/s; wgrad over 16384 tokens 735
-// us, 1.17 PFLOP/s (the library's BF16 product of these shapes, from operands
-// in BF16, reaches 1.15 and 0.89).  Matrix instructions alone take 70% of
-// that time; decoding and its loads cost 90 and 110 us of wgrad's.
+// dgrad 8192 x 2560 x 10240: 337-341 us, 1.27 PFLOP/s; wgrad over 16384 tokens
+// 725-736 us, 1.18 PFLOP/s (the library's BF16 product of these shapes, from
+// operands in BF16, reaches 1.15 and 0.89); under sustained load, when power
+// holds the clock, 5% more.  The matrix cores are busy for 54% of it: a step's
+// codes and its dense operand are waited for together, a step after they were
+// asked for.
 __device__ __forceinline__ bf16x8 read_turned(const char* p, int pitch) {
     union {
         s16x4 h[2];
@@ -791,8 +798,8 @@ __global__ __launch_bounds__(64 * WC* WD, 2) void k_mx_grad(Gradient a, MxMat m,
                 const int n = (i * FD + j) / kEvery;
                 if (slot >= 0 && (i * FD + j) % kEvery == 0 && n < kPieces) {
                     __builtin_amdgcn_sched_barrier(0);
-                    // E4M3: loads before the conversions (wgrad 16384: 723 us,
-                    // behind them 740); E2M1: behind (dgrad 8192: 352, before 363)
+                    // E4M3: loads before the conversions (wgrad 16384: 2% faster than
+                    // behind them); E2M1: behind (dgrad 8192: 3% faster than before)
                     constexpr int kBefore = FMT == Q4MX_FP4 ? kTurns + kConverts : kTurns;
                     if (n < kBefore) decode_piece(slot, n);
                     else if (n < kBefore + kLoads) load_piece(n - kBefore);
