@@ -105,6 +105,9 @@ template <bool BF16> __global__ __launch_bounds__(256) void k_mx_dequantize(MxMa
 }
 
 // ---- activation functions ---------------------------------------------------
+// 8192 x 5632, forward and backward: SwiGLU 73 and 76 us, GELU (tanh) 41 and 45
+// (memory); GELU (erf) 71 and 83 (arithmetic: erfcf and an exponential).
+//
 // f(x) and f'(x).  With s = 1 / (1 + e^-t): x s for the gated unit (t = x) and
 // for the tanh form, since 0.5 (1 + tanh u) = 1 / (1 + e^-2u).
 struct ActValue {

@@ -383,7 +383,8 @@ q4_status q4adamw_dequant_state(const q4_config* cfg, const q4_tensor* t, float*
  * row's length) and pointers aligned to the element; 16-byte aligned pointers
  * with rows a multiple of 16 bytes apart are read and written fastest.
  * Codes, scales and workspaces are 16-byte aligned.  Nothing outside a
- * dense result's rows x cols elements is written.  A call whose result has
+ * dense result's rows x cols elements is written; a result shares no element
+ * with an operand unless the call says so.  A call whose result has
  * no elements does nothing; a product over no elements is 0.  The calls take
  * no upload and allocate nothing, so they may be captured in a HIP graph;
  * the operands' pointers must live on the current device, and a workspace

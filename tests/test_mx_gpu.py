@@ -9,9 +9,11 @@ products in FP32; each of its at most K additions is off by at most one step
 |error| <= (K + 16) 2^-23 S, plus half a step of the result's type, 2^-8 |y|
 for BF16 and 2^-24 |y| for FP32.
 
-The block-scaled matrix instruction with an E4M3 operand adds 8 neighbouring
-products on a grid of 2^-13 of the largest one's power of two first, cutting
-off what lies below (one instruction with two products of chosen sizes shows
+test_mx_sums_gpu.py holds linear from "fp8" to that; the tests here allow it
+what a product by the block-scaled matrix instruction would need.  With an
+E4M3 operand that one adds 8 neighbouring products on a grid of 2^-13 of the
+largest one's power of two first, cutting off what lies below (one
+instruction with two products of chosen sizes shows
 it: 256 + 2^-5 is exact within 8 neighbours, 256 + 2^-6 gives 256, and across
 them FP32 decides).  Each of the 8 loses less than 2^-13 of the largest, so
 linear from "fp8" is allowed 8 * 2^-13 of the largest product of each 8
@@ -379,7 +381,7 @@ def test_a_nan_block_of_another_slice_stays_there(tokens):
     assert torch.equal(y, rows[:, None] | cols[None, :])
 
 
-MANY = [(4200, 4100, 200), (70001, 129, 130)]   # more tiles of 256 than compute units; of 128 than twice as many
+MANY = [(4200, 4100, 200), (70001, 129, 130)]   # more tiles of 256 than compute units, shallow sums
 
 
 def _some_rows(n):
