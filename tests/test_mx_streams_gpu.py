@@ -146,3 +146,15 @@ def test_recording_empty_and_given_matrices():
     mx.MXMatrix(5, 64, "fp4", codes=m.codes, scales=m.scales).record_stream(side)
     m.record_stream(side)
     assert mx.linear(torch.empty(0, 64, dtype=torch.bfloat16, device=DEV), m, stream=side).shape == (0, 5)
+
+
+def test_a_stream_of_another_device_is_refused():
+    class Other:
+        device = torch.device("cuda", torch.cuda.current_device() + 1)
+
+    x = _normal(5, 64, 12)
+    m = mx.quantize(x, "fp4")
+    for call in (lambda s: mx.quantize(x, "fp8", stream=s), lambda s: mx.dequantize(m, stream=s),
+                 lambda s: mx.linear(x, m, stream=s), lambda s: mx.act_forward("gelu", x, stream=s)):
+        with pytest.raises(ValueError, match="the stream is on"):
+            call(Other())
