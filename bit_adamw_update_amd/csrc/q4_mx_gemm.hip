@@ -253,9 +253,10 @@ hipError_t zero(const Out& o, hipStream_t st) {
 // issue slots that 16-cycle products leave free, and codes are a half or a
 // quarter of BF16's bytes in shared memory.
 //
-// 8192 tokens x 2560 x 10240, E4M3: 285-297 us, 1.48 PFLOP/s (the library's product
-// of BF16 operands reaches 1.36 at 8192 cubed; the block-scaled instruction
-// takes 168 us, with the coarser sums).  E2M1: 128 us.
+// 8192 tokens x 2560 x 10240, E4M3: 285-319 us on several cards, 1.35-1.5
+// PFLOP/s (the library's product of BF16 operands reaches 1.36 at 8192 cubed;
+// the block-scaled instruction takes 168 us, with the coarser sums).  E2M1: 128
+// us.
 template <int XF, int WN, int WT, int FN, int FT>
 __global__ __launch_bounds__(64 * WN* WT, 2) void k_mx_linear(MxMat x, MxMat w, Out y, Cut cut) {
     constexpr int NW = WN * WT, BN = WN * FN * 16, BT = WT * FT * 16;
@@ -590,8 +591,8 @@ template <int XF, int NW> __global__ __launch_bounds__(64 * NW) void k_mx_linear
 // (half a step), the other reads fragments.  Three steps of the dense operand
 // and two of the codes are in rings (160 KB in all).
 //
-// dgrad 8192 x 2560 x 10240: 337-343 us, 1.26 PFLOP/s; wgrad over 16384 tokens
-// 725-736 us, 1.18 PFLOP/s (the library's BF16 product of these shapes, from
+// dgrad 8192 x 2560 x 10240: 337-369 us on several cards, 1.16-1.27 PFLOP/s;
+// wgrad over 16384 tokens 725-790 us, 1.09-1.18 PFLOP/s (the library's BF16 product of these shapes, from
 // operands in BF16, reaches 1.15 and 0.89); under sustained load, when power
 // holds the clock, 5% more.  The matrix cores are busy for 54% of it: a step's
 // codes and its dense operand are waited for together, a step after they were
