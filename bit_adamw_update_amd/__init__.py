@@ -25,5 +25,11 @@ from .api import (  # noqa: F401
     q4mx_wgrad_workspace_bytes, q4mx_act_forward, q4mx_act_backward, MX_FP4, MX_FP8, MX_F32, MX_BF16, MX_GELU,
     MX_GELU_ERF, MX_SWIGLU, MX_WGRAD_TRANSPOSED, MX_WGRAD_ADD, MX_FEW_TOKENS,
 )
+from .api import (  # noqa: F401
+    Q4NNHeads, Q4NNRope, q4nn_embedding, q4nn_embedding_mx, q4nn_embedding_grad, q4nn_embedding_grad_workspace_bytes,
+    q4nn_head_norm_rope, q4nn_head_norm_rope_backward, q4nn_head_norm_rope_backward_workspace_bytes, q4nn_dropout,
+    NN_I32, NN_I64, NN_ADD,
+)
 from .state import Q4State, RECIPE_BY_NAME  # noqa: F401
 from . import mx  # noqa: F401
+from . import layers  # noqa: F401

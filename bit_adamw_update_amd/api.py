@@ -24,6 +24,8 @@ MX_F32, MX_BF16 = range(2)
 MX_GELU, MX_GELU_ERF, MX_SWIGLU = range(3)
 MX_WGRAD_TRANSPOSED, MX_WGRAD_ADD = 1, 2
 MX_FEW_TOKENS = 16
+NN_I32, NN_I64 = range(2)
+NN_ADD = 1
 
 STATUS = {0: "Q4_OK", 1: "Q4_ERR_INVALID_ARG", 2: "Q4_ERR_SHAPE", 3: "Q4_ERR_ALIGNMENT", 4: "Q4_ERR_CONFLICT",
           5: "Q4_ERR_STATE_FORMAT", 6: "Q4_ERR_DEVICE", 7: "Q4_ERR_WORKSPACE", 8: "Q4_ERR_HIP"}
@@ -64,6 +66,18 @@ class Q4StateHeader(C.Structure):
 class Q4MXMatrix(C.Structure):
     _fields_ = [("format", C.c_int32), ("reserved", C.c_int32), ("rows", C.c_int64), ("cols", C.c_int64),
                 ("codes", C.c_void_p), ("scales", C.c_void_p)]
+
+
+class Q4NNHeads(C.Structure):
+    _fields_ = [("p", C.c_void_p), ("batch", C.c_int64), ("token", C.c_int64), ("head", C.c_int64)]
+
+
+class Q4NNRope(C.Structure):
+    _fields_ = [("batches", C.c_int64), ("tokens", C.c_int64), ("q_heads", C.c_int32), ("k_heads", C.c_int32),
+                ("dim", C.c_int32), ("rotary", C.c_int32), ("interleaved", C.c_int32), ("gain_dtype", C.c_int32),
+                ("position_type", C.c_int32), ("eps", C.c_float), ("q_gain", C.c_void_p), ("k_gain", C.c_void_p),
+                ("positions", C.c_void_p), ("position_batch", C.c_int64), ("position_token", C.c_int64),
+                ("frequencies", C.c_void_p)]
 
 
 class Q4Error(RuntimeError):
@@ -123,6 +137,21 @@ _SIGNATURES = {
                           C.c_void_p], C.c_int),
     "q4mx_act_backward": ([C.c_int32, C.c_void_p, C.c_void_p, C.c_void_p, C.c_int64,
                            C.c_void_p, C.c_int64, C.c_void_p, C.c_int64, C.c_void_p], C.c_int),
+    "q4nn_embedding": ([C.c_void_p, C.c_int32, C.c_int64, C.c_void_p, C.c_int32, C.c_int64, C.c_int64, C.c_int64,
+                        C.c_float, C.c_void_p, C.c_int32, C.c_int64, C.c_void_p], C.c_int),
+    "q4nn_embedding_mx": ([C.c_void_p, C.c_int32, C.c_int64, C.c_void_p, C.c_float, C.c_void_p, C.c_int32, C.c_int64,
+                           C.c_void_p], C.c_int),
+    "q4nn_embedding_grad": ([C.c_void_p, C.c_int32, C.c_int64, C.c_void_p, C.c_int64, C.c_float, C.c_int64, C.c_int64,
+                             C.c_void_p, C.c_int32, C.c_int64, C.c_int32, C.c_void_p, C.c_size_t, C.c_void_p], C.c_int),
+    "q4nn_embedding_grad_workspace_bytes": ([C.c_int64, C.c_int64, C.c_int64, C.POINTER(C.c_size_t)], C.c_int),
+    "q4nn_head_norm_rope": ([C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p], C.c_int),
+    "q4nn_head_norm_rope_backward": ([C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p,
+                                      C.c_void_p, C.c_void_p, C.c_void_p, C.c_int32, C.c_int32, C.c_void_p, C.c_size_t,
+                                      C.c_void_p], C.c_int),
+    "q4nn_head_norm_rope_backward_workspace_bytes": ([C.c_void_p, C.POINTER(C.c_size_t)], C.c_int),
+    "q4nn_dropout": ([C.c_double, C.c_uint64, C.c_uint64, C.c_void_p, C.c_uint32, C.c_int64, C.c_void_p, C.c_int64,
+                      C.c_void_p, C.c_int64, C.c_int64, C.c_int64, C.c_void_p, C.c_int64, C.c_int32, C.c_void_p],
+                     C.c_int),
 }
 
 
@@ -375,3 +404,54 @@ def q4mx_act_backward(act: int, kept_x: Q4MXMatrix, kept_up, dy, lddy: int, dx, 
                       stream=None) -> None:
     _check(load_library().q4mx_act_backward(act, _mx(kept_x), _mx(kept_up), _ptr(dy), lddy, _ptr(dx), lddx,
                                             _ptr(dup), lddup, _stream(stream)))
+
+
+# ---- beside the products: embedding, head norms, dropout --------------------
+
+def q4nn_embedding(ids, id_type: int, tokens: int, table, dtype: int, rows: int, cols: int, ld: int, scale: float, out,
+                   out_dtype: int, ldo: int, stream=None) -> None:
+    _check(load_library().q4nn_embedding(_ptr(ids), id_type, tokens, _ptr(table), dtype, rows, cols, ld, scale,
+                                         _ptr(out), out_dtype, ldo, _stream(stream)))
+
+
+def q4nn_embedding_mx(ids, id_type: int, tokens: int, table: Q4MXMatrix, scale: float, out, out_dtype: int, ldo: int,
+                      stream=None) -> None:
+    _check(load_library().q4nn_embedding_mx(_ptr(ids), id_type, tokens, _mx(table), scale, _ptr(out), out_dtype, ldo,
+                                            _stream(stream)))
+
+
+def q4nn_embedding_grad_workspace_bytes(tokens: int, rows: int, cols: int) -> int:
+    out = C.c_size_t()
+    _check(load_library().q4nn_embedding_grad_workspace_bytes(tokens, rows, cols, C.byref(out)))
+    return out.value
+
+
+def q4nn_embedding_grad(ids, id_type: int, tokens: int, dy, lddy: int, scale: float, rows: int, cols: int, grad,
+                        dtype: int, ldg: int, flags: int = 0, ws=None, ws_bytes: int | None = None, stream=None) -> None:
+    _check(load_library().q4nn_embedding_grad(_ptr(ids), id_type, tokens, _ptr(dy), lddy, scale, rows, cols, _ptr(grad),
+                                              dtype, ldg, flags, _ptr(ws), _ws(ws, ws_bytes), _stream(stream)))
+
+
+def q4nn_head_norm_rope(rope: Q4NNRope, q: Q4NNHeads, k: Q4NNHeads, q_out: Q4NNHeads, k_out: Q4NNHeads,
+                        stream=None) -> None:
+    _check(load_library().q4nn_head_norm_rope(_mx(rope), _mx(q), _mx(k), _mx(q_out), _mx(k_out), _stream(stream)))
+
+
+def q4nn_head_norm_rope_backward_workspace_bytes(rope: Q4NNRope) -> int:
+    out = C.c_size_t()
+    _check(load_library().q4nn_head_norm_rope_backward_workspace_bytes(_mx(rope), C.byref(out)))
+    return out.value
+
+
+def q4nn_head_norm_rope_backward(rope: Q4NNRope, q: Q4NNHeads, k: Q4NNHeads, dq: Q4NNHeads, dk: Q4NNHeads,
+                                 dq_in: Q4NNHeads, dk_in: Q4NNHeads, dq_gain, dk_gain, dtype: int, flags: int = 0,
+                                 ws=None, ws_bytes: int | None = None, stream=None) -> None:
+    _check(load_library().q4nn_head_norm_rope_backward(_mx(rope), _mx(q), _mx(k), _mx(dq), _mx(dk), _mx(dq_in),
+                                                       _mx(dk_in), _ptr(dq_gain), _ptr(dk_gain), dtype, flags, _ptr(ws),
+                                                       _ws(ws, ws_bytes), _stream(stream)))
+
+
+def q4nn_dropout(p: float, seed: int, step: int, step_at, layer: int, offset: int, x, ldx: int, residual, ldr: int,
+                 rows: int, cols: int, out, ldo: int, dtype: int, stream=None) -> None:
+    _check(load_library().q4nn_dropout(p, seed, step, _ptr(step_at), layer, offset, _ptr(x), ldx, _ptr(residual), ldr,
+                                       rows, cols, _ptr(out), ldo, dtype, _stream(stream)))

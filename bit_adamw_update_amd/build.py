@@ -19,10 +19,12 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(BUILD_DIR, "libq4adamw.so")
 SOURCES = [os.path.join(CSRC, f) for f in ("q4_kernels.hip", "q4_abi.cpp", "q4_mx_elem.hip", "q4_mx_gemm.hip",
-                                           "q4_mx_abi.cpp")]
+                                           "q4_mx_abi.cpp", "q4_nn_embed.hip", "q4_nn_heads.hip", "q4_nn_dropout.hip",
+                                           "q4_nn_abi.cpp")]
 DEPS = SOURCES + [os.path.join(CSRC, "q4_internal.h"), os.path.join(CSRC, "q4_exact.h"),
                   os.path.join(CSRC, "q4_quant.h"), os.path.join(CSRC, "q4_codebooks.inc"),
                   os.path.join(CSRC, "q4_mx.h"), os.path.join(CSRC, "q4_mx_dev.h"),
+                  os.path.join(CSRC, "q4_nn.h"), os.path.join(CSRC, "q4_check.h"),
                   os.path.join(ROOT, "include", "q4adamw.h")]
 PROBE_PATH = os.path.join(BUILD_DIR, "libq4probe.so")
 PROBE_SOURCES = [os.path.join(CSRC, "q4_probe.hip")]

@@ -477,6 +477,105 @@ q4_status q4mx_act_forward(int32_t act, const uint16_t* x, int64_t ldx, const ui
 q4_status q4mx_act_backward(int32_t act, const q4mx_matrix* kept_x, const q4mx_matrix* kept_up, const uint16_t* dy,
                             int64_t lddy, uint16_t* dx, int64_t lddx, uint16_t* dup, int64_t lddup, void* stream);
 
+/* ---- beside the products: embedding, head norms, dropout ---------------
+ * The rest of what a training step does with its masters and gradients
+ * outside of products and attention: rows of the embedding table and their
+ * gradient, the norm of queries and keys with the rotation by position, and
+ * dropout.  Dense operands are as above (row stride `ld`, pointers aligned to
+ * the element, types Q4MX_F32 and Q4MX_BF16), and so are the rules on what is
+ * written, captured and shared.  Results have fewer than 2^38 elements, and
+ * every sum is in FP32 and in an order that the operands alone decide: the
+ * result of a call is the same bit for bit. */
+
+typedef enum { Q4NN_I32 = 0, Q4NN_I64 = 1 } q4nn_int; /* integers in device memory */
+
+/* out (tokens x cols, out_dtype) <- scale * table[ids[t]], the product in
+ * FP32 and rounded once.  ids (device, type id_type): tokens consecutive
+ * integers.  A token below 0 is padding: its row is 0.  A token of `rows` or
+ * more names no row: its row is NaN.  table: rows x cols, dtype, or an MX
+ * matrix in either format (the w of a tied q4mx_linear). */
+q4_status q4nn_embedding(const void* ids, int32_t id_type, int64_t tokens, const void* table, int32_t dtype,
+                         int64_t rows, int64_t cols, int64_t ld, float scale, void* out, int32_t out_dtype, int64_t ldo,
+                         void* stream);
+q4_status q4nn_embedding_mx(const void* ids, int32_t id_type, int64_t tokens, const q4mx_matrix* table, float scale,
+                            void* out, int32_t out_dtype, int64_t ldo, void* stream);
+
+#define Q4NN_ADD 1 /* a gradient is added to what its buffer holds, with one rounding */
+
+/* grad (rows x cols, dtype) <- scale * the sum of dy[t] over the tokens with
+ * ids[t] = row, dy BF16 (tokens x cols): the gradient of the table, every row
+ * of it (0 where no token read it; with Q4NN_ADD such rows are not touched).
+ * Tokens outside [0, rows) count for no row.  The tokens are sorted by id and
+ * position, and a row's gradients are summed in that order, in pieces of
+ * fixed places joined in FP32.  A tensor's BF16 gradient (q4_tensor.grad) is a
+ * grad of dtype Q4MX_BF16. */
+q4_status q4nn_embedding_grad(const void* ids, int32_t id_type, int64_t tokens, const uint16_t* dy, int64_t lddy,
+                              float scale, int64_t rows, int64_t cols, void* grad, int32_t dtype, int64_t ldg,
+                              int32_t flags, void* ws, size_t ws_bytes, void* stream);
+q4_status q4nn_embedding_grad_workspace_bytes(int64_t tokens, int64_t rows, int64_t cols, size_t* bytes);
+
+/* Queries or keys, BF16: element i of head h of token t of batch b at
+ * p[b batch + t token + h head + i]. */
+typedef struct {
+    uint16_t* p;
+    int64_t batch, token, head; /* strides in elements, each in [0, 2^40) */
+} q4nn_heads;
+
+/* n = x / sqrt(mean of x^2 over the head + eps), y = n gain, and the first
+ * `rotary` elements of y turned by position: pair i is (y_a, y_b) <-
+ * (y_a c - y_b s, y_b c + y_a s), c and s the cosine and sine of position *
+ * frequencies[i], where (a, b) = (i, i + rotary/2), or (2i, 2i + 1) with
+ * `interleaved`.  Angles are formed and reduced in FP64, the rest is FP32
+ * (squares too: a mean past its range normalizes to 0), one rounding. */
+typedef struct {
+    int64_t batches, tokens;   /* per batch; batches * tokens < 2^31 */
+    int32_t q_heads, k_heads;  /* each in [0, 4096] */
+    int32_t dim, rotary;       /* even; 2 <= dim <= 1024, 0 <= rotary <= dim */
+    int32_t interleaved;       /* 0 or 1 */
+    int32_t gain_dtype;        /* q4mx_dtype of the gains */
+    int32_t position_type;     /* q4nn_int */
+    float eps;                 /* normal and positive */
+    const void* q_gain;        /* device, dim elements each */
+    const void* k_gain;
+    const void* positions;     /* device: of token t of batch b at [b position_batch + t position_token] */
+    int64_t position_batch, position_token; /* strides in elements, each in [0, 2^31) */
+    const double* frequencies; /* device, rotary / 2 angles per position */
+} q4nn_rope;
+
+/* q_out, k_out <- the above of q and k.  An output may be its input, with the
+ * same strides. */
+q4_status q4nn_head_norm_rope(const q4nn_rope* r, const q4nn_heads* q, const q4nn_heads* k, const q4nn_heads* q_out,
+                              const q4nn_heads* k_out, void* stream);
+
+/* Its gradients from the inputs q and k and the results' gradients dq and dk:
+ * those of q and k in dq_in and dk_in (each may be dq or dk, with the same
+ * strides), and those of the gains (dim elements, dtype; with Q4NN_ADD added
+ * to what they hold).  A q4_tensor's grad is one of dtype Q4MX_BF16. */
+q4_status q4nn_head_norm_rope_backward(const q4nn_rope* r, const q4nn_heads* q, const q4nn_heads* k,
+                                       const q4nn_heads* dq, const q4nn_heads* dk, const q4nn_heads* dq_in,
+                                       const q4nn_heads* dk_in, void* dq_gain, void* dk_gain, int32_t dtype,
+                                       int32_t flags, void* ws, size_t ws_bytes, void* stream);
+q4_status q4nn_head_norm_rope_backward_workspace_bytes(const q4nn_rope* r, size_t* bytes);
+
+/* out <- x / (1 - p) where kept and 0 where dropped (also for a NaN or
+ * infinite x), plus residual if it is not NULL; all rows x cols of one dtype,
+ * FP32 arithmetic, one rounding.  out may be x or residual (with its row
+ * stride).
+ * The mask is not stored.  Element i (of the row-major matrix, counted from
+ * `offset`: a shard's first element, a multiple of 8, so that a matrix in
+ * several calls gets the mask that it gets in one) is dropped if its 16 random
+ * bits are below p 2^16, p rounded to a multiple of 2^-16 first, which is also
+ * the p of the scale.  The bits are half i mod 8 (the low half of a word
+ * first) of Philox4x32-10 under the key `seed` with the counter (i / 8, step,
+ * layer, 2): the step's generator, on a stream that the optimizer's draws do
+ * not use.  Backward: the same call on the gradient, without residual.
+ * step_at, if not NULL: one 64-bit step count in device memory that is used
+ * in place of `step`, so that a captured graph can draw anew at each replay.
+ * Steps are taken modulo 2^32; offset + rows * cols <= 2^35. */
+q4_status q4nn_dropout(double p, uint64_t seed, uint64_t step, const uint64_t* step_at, uint32_t layer, int64_t offset,
+                       const void* x, int64_t ldx, const void* residual, int64_t ldr, int64_t rows, int64_t cols,
+                       void* out, int64_t ldo, int32_t dtype, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
