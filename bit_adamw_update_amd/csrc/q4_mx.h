@@ -29,12 +29,13 @@ struct Dense {
     int dtype;  // q4mx_dtype
 };
 
-// The grid of n work-groups of up to 512 threads.  A launch takes fewer than
-// 2^32 threads along a dimension (it refuses 2^32 and drops what is above), so
-// groups past 2^22 go into rows; the last row may have more than n groups.
-inline dim3 grid_of(int64_t n) {
-    constexpr int64_t kRow = int64_t(1) << 22;
-    return n <= kRow ? dim3((unsigned)n) : dim3((unsigned)kRow, (unsigned)((n + kRow - 1) / kRow));
+// The grid of n work-groups of up to 512 threads, or of `threads`.  A launch
+// takes fewer than 2^32 threads along a dimension (it refuses 2^32 and drops
+// what is above), so groups past 2^22 (of 512) go into rows; the last row may
+// have more than n groups.
+inline dim3 grid_of(int64_t n, int threads = 512) {
+    const int64_t row = (int64_t(1) << 31) / threads;
+    return n <= row ? dim3((unsigned)n) : dim3((unsigned)row, (unsigned)((n + row - 1) / row));
 }
 
 hipError_t launch_mx_quantize(const Dense& src, bool transpose, const MxMat& out, hipStream_t st);

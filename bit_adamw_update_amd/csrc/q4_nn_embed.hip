@@ -46,114 +46,143 @@ __global__ __launch_bounds__(256) void k_embedding(Ids ids, Dense table, MxMat m
 // summed in one order:
 //   1. tiles of 1024 tokens are sorted in shared memory, and the gradient is
 //      filled with zeros by the work-groups behind them: the sort is over long
-//      before the fill of a large vocabulary's table is;
-//   2. up to 16 sorted runs at a time are merged: an element's place is its
-//      place in its own run plus the number of smaller ones in each other;
-//   3. pieces of 32 sorted tokens are summed, a wave to 512 columns of a piece.
-//      A row that lies within a piece is finished; one that crosses a piece's
-//      end leaves FP32 sums in the workspace;
+//      before the fill of a large vocabulary's table is, and writes alone run
+//      at 7.9 TB/s where reads and writes together reach 5.1;
+//   2. up to 16 sorted runs at a time are merged: an element's place is the
+//      number of smaller ones in all of them;
+//   3. a wave takes the rows that begin in a piece of 16 sorted tokens, 512
+//      columns of them.  A row of up to 32 tokens is summed whole, past the
+//      piece's end where it has to; of a longer one every piece that it touches
+//      leaves an FP32 sum in the workspace;
 //   4. those are joined, in the order of the pieces.
 // Keys are (id << 32) | position; a token that counts for no row has the id
 // kNone and lies behind all others.
-constexpr int kSortTile = 1024, kMergeRuns = 16, kPiece = 32, kSlab = 512, kJoinCols = 256, kJoinPieces = 16;
-constexpr uint32_t kNone = 0xFFFFFFFFu;
-constexpr int64_t kFillBytes = 64 << 10;  // zeros of a work-group
+constexpr int kSortTile = 1024, kMergeRuns = 16, kPiece = 16, kShort = 32, kSlab = 512;
+constexpr int kJoinCols = 256, kJoinPieces = 16;
+constexpr uint32_t kNone = 0x80000000u;   // above every id; one more is a number too
+constexpr int kFillPieces = 8 * kSortTile;  // 16 bytes of zeros each, of a work-group
 
 __device__ __forceinline__ uint32_t id_of(uint64_t key) { return (uint32_t)(key >> 32); }
 
-// Zeros into part `block` of grad (rows x cols elements of `unit` bytes).
+// Zeros into part `block` of grad: 16-byte pieces, the last of a row shorter.
 struct Fill {
-    void* p;
-    int64_t rows, row_bytes, pitch;  // one row if the rows follow each other
-    int64_t row_blocks;              // parts of a row
+    char* p;
+    int64_t row_bytes, pitch;  // one row if the rows follow each other
+    int64_t pieces, row_pieces;
     int64_t blocks;
 };
 __device__ __forceinline__ void fill_zero(const Fill& f, int64_t block) {
-    if (block >= f.blocks) return;
-    const int64_t row = block / f.row_blocks, from = (block - row * f.row_blocks) * kFillBytes;
-    const int64_t size = f.row_bytes - from < kFillBytes ? f.row_bytes - from : kFillBytes;
-    char* p = static_cast<char*>(f.p) + row * f.pitch + from;
-    for (int64_t i = threadIdx.x * 16; i < size; i += 256 * 16) {
-        if (size - i >= 16) {
-            *reinterpret_cast<u32x4_any*>(p + i) = u32x4_any{0, 0, 0, 0};
+    const int64_t first = block * kFillPieces, row = first / f.row_pieces;
+    const uint32_t at = (uint32_t)(first - row * f.row_pieces);
+#pragma unroll
+    for (int k = 0; k < kFillPieces; k += kSortTile) {
+        if (first + k + threadIdx.x >= f.pieces) return;
+        int64_t r = 0, i = first + k + threadIdx.x;
+        if (f.pieces != f.row_pieces) {
+            const uint32_t local = at + k + threadIdx.x, rows = local / (uint32_t)f.row_pieces;
+            r = row + rows, i = local - rows * (uint32_t)f.row_pieces;
+        }
+        char* p = f.p + r * f.pitch + i * 16;
+        const int64_t size = f.row_bytes - i * 16;
+        if (size >= 16) {
+            *reinterpret_cast<u32x4_any*>(p) = u32x4_any{0, 0, 0, 0};
         } else {
-            for (int64_t k = i; k < size; k += 2) *reinterpret_cast<uint16_t*>(p + k) = 0;
+            for (int64_t n = 0; n < size; n += 2) *reinterpret_cast<uint16_t*>(p + n) = 0;
         }
     }
 }
 
-__global__ __launch_bounds__(256) void k_sort_tiles(Ids ids, int64_t rows, uint64_t* keys, int64_t tiles, Fill fill) {
-    __shared__ uint64_t lds[kSortTile];
+// A wave ranks its 64 ids by comparing each with each (equal ones by their
+// position), which leaves 16 sorted runs in shared memory; then a key's place
+// is its place in its own run and the numbers of ids before it in the others,
+// found by 16 binary searches side by side.
+__global__ __launch_bounds__(kSortTile) void k_sort_tiles(Ids ids, int64_t rows, uint64_t* keys, int64_t tiles,
+                                                           Fill fill) {
+    __shared__ uint32_t run_id[kSortTile], run_token[kSortTile];
     const int64_t tile = group_index();
-    if (tile >= tiles) return fill_zero(fill, tile - tiles);
-    const int64_t first = tile * kSortTile;
-#pragma unroll
-    for (int j = 0; j < kSortTile / 256; ++j) {
-        const int64_t t = first + j * 256 + threadIdx.x;
-        uint64_t key = ~uint64_t(0);
-        if (t < ids.n) {
-            const int64_t id = load_id(ids, t);
-            key = (uint64_t)(id >= 0 && id < rows ? (uint32_t)id : kNone) << 32 | (uint32_t)t;
-        }
-        lds[j * 256 + threadIdx.x] = key;
+    if (tile >= tiles) {
+        if (tile - tiles < fill.blocks) fill_zero(fill, tile - tiles);
+        return;
     }
-    // bitonic: blocks of `size` alternate in direction
-    for (int size = 2; size <= kSortTile; size *= 2)
-        for (int step = size / 2; step > 0; step /= 2) {
-            __syncthreads();
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int64_t t = tile * kSortTile + tid;
+    uint32_t id = kNone;
+    if (t < ids.n) {
+        const int64_t v = load_id(ids, t);
+        if (v >= 0 && v < rows) id = (uint32_t)v;
+    }
+    int rank = 0;
 #pragma unroll
-            for (int j = 0; j < kSortTile / 512; ++j) {
-                const int i = j * 256 + threadIdx.x, lo = 2 * i - (i & (step - 1)), hi = lo + step;
-                const uint64_t a = lds[lo], b = lds[hi];
-                if ((a > b) == ((lo & size) == 0)) lds[lo] = b, lds[hi] = a;
-            }
-        }
+    for (int j = 0; j < 64; ++j) {
+        const uint32_t other = (uint32_t)__builtin_amdgcn_readlane((int)id, j);
+        rank += other < id + (j < lane ? 1u : 0u) ? 1 : 0;
+    }
+    run_id[wave * 64 + rank] = id;
+    run_token[wave * 64 + rank] = (uint32_t)t;
     __syncthreads();
+    id = run_id[tid];
+    int place = lane;
+    int pos[16];
 #pragma unroll
-    for (int j = 0; j < kSortTile / 256; ++j) {
-        const int64_t t = first + j * 256 + threadIdx.x;
-        if (t < ids.n) keys[t] = lds[j * 256 + threadIdx.x];
+    for (int r = 0; r < 16; ++r) pos[r] = 0;
+#pragma unroll
+    for (int step = 32; step > 0; step /= 2)
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+            if (run_id[r * 64 + pos[r] + step - 1] < id + (r < wave ? 1u : 0u)) pos[r] += step;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+        const int found = pos[r] + (run_id[r * 64 + pos[r]] < id + (r < wave ? 1u : 0u) ? 1 : 0);
+        if (r != wave) place += found;
     }
+    // past the last token: ids of kNone from the end of the tile, so they are the last
+    if (tile * kSortTile + place < ids.n) keys[tile * kSortTile + place] = (uint64_t)id << 32 | run_token[tid];
 }
 
-// Runs of `run` keys, the last one shorter: each kMergeRuns neighbours become one.
+// Runs of `run` keys, the last one shorter: each kMergeRuns neighbours become
+// one.  16 lanes to a key, a run to each.
 __global__ __launch_bounds__(256) void k_merge_runs(const uint64_t* src, uint64_t* dst, int64_t n, int64_t run) {
-    const int64_t i = (int64_t)group_index() * 256 + threadIdx.x;
+    const int64_t i = (int64_t)group_index() * 16 + (threadIdx.x >> 4);
     if (i >= n) return;
     const uint64_t key = src[i];
     const int64_t group = i / (run * kMergeRuns) * (run * kMergeRuns);
-    int64_t place = i;
-    for (int r = 0; r < kMergeRuns; ++r) {
-        const int64_t begin = group + r * run;
-        if (begin >= n) break;
-        const int64_t end = begin + run < n ? begin + run : n;
-        if (i >= begin && i < end) continue;
-        int64_t lo = begin, hi = end;  // the first of this run that is larger (no two are equal)
-        while (lo < hi) {
-            const int64_t mid = lo + (hi - lo) / 2;
-            if (src[mid] < key) lo = mid + 1;
-            else hi = mid;
-        }
-        place += begin < i ? lo - end : lo - begin;  // those of a run before it that are larger move behind it
+    const int64_t begin = group + (threadIdx.x & 15) * run, end = begin + run < n ? begin + run : n;
+    int64_t lo = begin, hi = end > begin ? end : begin;  // the first of this run that is not smaller (no two are equal)
+    if (i >= lo && i < hi) lo = hi = i;
+    while (lo < hi) {
+        const int64_t mid = lo + (hi - lo) / 2;
+        if (src[mid] < key) lo = mid + 1;
+        else hi = mid;
     }
-    dst[place] = key;
+    int smaller = (int)(lo - begin);
+    smaller += __builtin_amdgcn_update_dpp(0, smaller, 0xB1, 0xF, 0xF, true);
+    smaller += __builtin_amdgcn_update_dpp(0, smaller, 0x4E, 0xF, 0xF, true);
+    smaller += __builtin_amdgcn_update_dpp(0, smaller, 0x141, 0xF, 0xF, true);
+    smaller += __builtin_amdgcn_update_dpp(0, smaller, 0x140, 0xF, 0xF, true);
+    if ((threadIdx.x & 15) == 0) dst[group + (uint32_t)smaller] = key;
 }
 
-// scale * sum into 8 columns of a row, or added to what is there; the first
-// `left` of them exist.
+// scale * sum into N columns of a row from col on, or added to what is there;
+// those before `skip` and from `left` on are another lane's, or do not exist.
 template <bool BF16, bool ADD, int N>
-__device__ __forceinline__ void store_grad(const Dense& grad, int64_t row, int64_t col, int64_t left, float scale,
-                                           const float* sum) {
+__device__ __forceinline__ void store_grad(const Dense& grad, int64_t row, int64_t col, int skip, int64_t left,
+                                           float scale, const float* sum) {
     const int64_t at = row * grad.ld + col;
-    float v[8] = {};
-    if (ADD) {
-        if (N == 8) load8<BF16>(grad.p, at, left, v);
-        else
-            for (int k = 0; k < N; ++k) v[k] = k < left ? load1<BF16>(grad.p, at + k) : 0.0f;
+    if (N == 8 && skip == 0 && left >= 8) {
+        float v[8];
+        if (ADD) load8<BF16>(grad.p, at, 8, v);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = ADD ? __builtin_fmaf(scale, sum[k], v[k]) : scale * sum[k];
+        store8<BF16>(grad.p, at, 8, v);
+        return;
     }
 #pragma unroll
-    for (int k = 0; k < N; ++k) v[k] = ADD ? __builtin_fmaf(scale, sum[k], v[k]) : scale * sum[k];
-    store8<BF16>(grad.p, at, left < N ? left : N, v);
+    for (int k = 0; k < N; ++k) {
+        if (k < skip || k >= left) continue;
+        const float v = ADD ? __builtin_fmaf(scale, sum[k], load1<BF16>(grad.p, at + k)) : scale * sum[k];
+        if (BF16) static_cast<uint16_t*>(grad.p)[at + k] = bf16_bits(v);
+        else static_cast<float*>(grad.p)[at + k] = v;
+    }
 }
 
 struct GradArgs {
@@ -161,89 +190,120 @@ struct GradArgs {
     int64_t n, pieces, slabs;
     const uint16_t* dy;
     int64_t lddy, cols, part_ld;
-    float* part;  // [pieces][2][part_ld]: a row that the piece begins with and does not finish, and one that it ends with
+    float* part;     // [pieces][2][part_ld]: of a long row that the piece begins with, and of one that begins behind that
+    uint32_t* long_begins;  // [pieces]: 0, or 1 + the place in part of the long row that begins in this piece
     float scale;
     Dense grad;
 };
 
-template <bool BF16, bool ADD> __global__ __launch_bounds__(256) void k_grad_pieces(GradArgs a) {
+// NARROW: fewer than 8 columns.  Else a lane whose 8 columns pass the end takes
+// the last 8, and stores those that are its own.
+template <bool BF16, bool ADD, bool NARROW> __global__ __launch_bounds__(256) void k_grad_pieces(GradArgs a) {
     const int lane = threadIdx.x & 63;
     const int64_t unit = (int64_t)group_index() * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t piece = unit / a.slabs;
+    const int64_t piece = unit / a.slabs, slab = unit - piece * a.slabs;
     if (piece >= a.pieces) return;
-    const int64_t col = (unit - piece * a.slabs) * kSlab + lane * 8, left = a.cols - col;
     const int64_t begin = piece * kPiece;
-    const int count = (int)(a.n - begin < kPiece ? a.n - begin : kPiece);
-    const uint64_t key = lane < count ? a.keys[begin + lane] : ~uint64_t(0);
+    // the piece and the 48 tokens behind it; the 32 before it
+    const uint64_t key = begin + lane < a.n ? a.keys[begin + lane] : ~uint64_t(0);
     const uint32_t id = id_of(key), token = (uint32_t)key;
-    const uint32_t before = begin > 0 ? id_of(a.keys[begin - 1]) : kNone;
-    const uint32_t behind = begin + count < a.n ? id_of(a.keys[begin + count]) : kNone;
+    const uint32_t before = lane < kShort && begin - kShort + lane >= 0 ? id_of(a.keys[begin - kShort + lane]) : ~0u;
+    const int real = __builtin_popcountll(__builtin_amdgcn_ballot_w64(id < kNone));
+    const int count = real < kPiece ? real : kPiece;
+    int from = 0, end = 0;
+    bool first_long = false, last_long = false;
+    if (count > 0) {
+        const uint32_t first = (uint32_t)__builtin_amdgcn_readlane((int)id, 0);
+        const int back = __builtin_popcountll(__builtin_amdgcn_ballot_w64(before == first));
+        const int ahead = __builtin_popcountll(__builtin_amdgcn_ballot_w64(id == first));
+        first_long = back > 0 && back + ahead > kShort;
+        from = back > 0 && !first_long ? ahead : 0;  // a short row that began before is another wave's
+    }
+    if (from < count) {
+        const uint32_t last = (uint32_t)__builtin_amdgcn_readlane((int)id, count - 1);
+        const uint64_t mask = __builtin_amdgcn_ballot_w64(id == last);
+        const int start = __builtin_ctzll(mask), length = __builtin_popcountll(mask);
+        last_long = (start > 0 || !first_long) && length > kShort;  // begins here, and more than 32 follow
+        end = last_long || (start == 0 && first_long) ? (start + length < kPiece ? start + length : kPiece) : start + length;
+        if (slab == 0 && lane == 0) a.long_begins[piece] = last_long ? (start == 0 ? 1 : 2) : 0;
+    } else {
+        if (slab == 0 && lane == 0) a.long_begins[piece] = 0;
+        return;
+    }
+    const int64_t col = slab * kSlab + lane * 8, left = a.cols - col;
+    const int64_t at = NARROW ? 0 : left >= 8 ? col : left > 0 ? a.cols - 8 : 0;
+    const int skip = left >= 8 || NARROW ? 0 : left > 0 ? (int)(8 - left) : 8;
+    const int64_t here = NARROW ? (lane == 0 ? a.cols : 0) : 8;  // of the 8 columns from `at` on
     float sum[8] = {};
-    uint32_t current = (uint32_t)__builtin_amdgcn_readlane((int)id, 0);
-    int from = 0;
+    uint32_t current = (uint32_t)__builtin_amdgcn_readlane((int)id, from);
+    int begun = from;
     auto finish = [&](int to) {
-        const bool begun = from == 0 && before == current, goes_on = to == count && behind == current;
-        if (left <= 0) return;
-        if (!begun && !goes_on) {
-            store_grad<BF16, ADD, 8>(a.grad, current, col, left, a.scale, sum);
+        if ((begun == 0 && first_long) || (to == end && last_long)) {
+            float* p = a.part + (piece * 2 + (begun == 0 ? 0 : 1)) * a.part_ld + at;
+            if (skip == 0 && here == 8) {
+                *reinterpret_cast<float4*>(p) = make_float4(sum[0], sum[1], sum[2], sum[3]);
+                *reinterpret_cast<float4*>(p + 4) = make_float4(sum[4], sum[5], sum[6], sum[7]);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (k >= skip && k < here) p[k] = sum[k];
+            }
         } else {
-            float4* p = reinterpret_cast<float4*>(a.part + (piece * 2 + (from == 0 ? 0 : 1)) * a.part_ld + col);
-            p[0] = make_float4(sum[0], sum[1], sum[2], sum[3]);
-            p[1] = make_float4(sum[4], sum[5], sum[6], sum[7]);
+            store_grad<BF16, ADD, 8>(a.grad, current, at, skip, here, a.scale, sum);
         }
     };
-    for (int i = 0; i < count; i += 8) {
-        float v[8][8];
+    constexpr int kBatch = 16;
+    for (int i = from; i < end; i += kBatch) {
+        u32x4_any raw[kBatch];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            // past the piece: its last token once more, not added
-            const int at = i + j < count ? i + j : count - 1;
-            const int64_t t = (uint32_t)__builtin_amdgcn_readlane((int)token, at);
-            if (left > 0) load8<true>(a.dy, t * a.lddy + col, left, v[j]);
+        for (int j = 0; j < kBatch; ++j) {
+            // past the end: the last token once more, not added
+            const int e = i + j < end ? i + j : end - 1;
+            const uint16_t* p = a.dy + (int64_t)(uint32_t)__builtin_amdgcn_readlane((int)token, e) * a.lddy + at;
+            if (!NARROW) {
+                raw[j] = *reinterpret_cast<const u32x4_any*>(p);
+            } else {
+                uint32_t w[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) w[k] = k < here ? p[k] : 0;
+                raw[j] = u32x4_any{w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16};
+            }
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            if (i + j >= count) break;
+        for (int j = 0; j < kBatch; ++j) {
+            if (i + j >= end) break;
             const uint32_t now = (uint32_t)__builtin_amdgcn_readlane((int)id, i + j);
             if (now != current) {
                 finish(i + j);
-                current = now, from = i + j;
+                current = now, begun = i + j;
 #pragma unroll
                 for (int k = 0; k < 8; ++k) sum[k] = 0.0f;
             }
-            if (now == kNone) return;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) sum[k] += v[j][k];
+            for (int k = 0; k < 4; ++k) {
+                sum[2 * k] += bf16_value(raw[j][k] & 0xFFFFu);
+                sum[2 * k + 1] += __uint_as_float(raw[j][k] & 0xFFFF0000u);
+            }
         }
     }
-    finish(count);
+    finish(end);
 }
 
-// The rows that begin in one of 16 pieces and go on past its end: a wave adds
-// every fourth of a row's sums, 4 columns to a lane, and the four waves' sums
-// are added in order.
+// The long rows that begin in one of 16 pieces: a wave adds every fourth of a
+// row's sums, 4 columns to a lane, and the four waves' sums are added in order.
 template <bool BF16, bool ADD> __global__ __launch_bounds__(256) void k_grad_join(GradArgs a, int64_t col_groups) {
     __shared__ float4 lds[4][64];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t block = group_index(), pg = block / col_groups;
     const int64_t col = (block - pg * col_groups) * kJoinCols + lane * 4, left = a.cols - col;
     const int64_t mine = pg * kJoinPieces + lane;
-    uint32_t last = kNone;
-    bool owner = false, whole = false;
-    if (lane < kJoinPieces && mine < a.pieces - 1) {
-        const int64_t begin = mine * kPiece, end = begin + kPiece;  // not the last piece: it is full, and nothing follows that
-        last = id_of(a.keys[end - 1]);
-        const bool goes_on = last != kNone && id_of(a.keys[end]) == last;
-        whole = id_of(a.keys[begin]) == last;
-        owner = goes_on && !(whole && begin > 0 && id_of(a.keys[begin - 1]) == last);
-    }
-    uint64_t todo = __builtin_amdgcn_ballot_w64(owner);
-    const uint64_t whole_mask = __builtin_amdgcn_ballot_w64(whole);
+    const uint32_t slot = lane < kJoinPieces && mine < a.pieces ? a.long_begins[mine] : 0;
+    uint64_t todo = __builtin_amdgcn_ballot_w64(slot != 0);
     while (todo) {
-        const int at = __builtin_ctzll(todo);
+        const int which = __builtin_ctzll(todo);
         todo &= todo - 1;
-        const uint32_t id = (uint32_t)__builtin_amdgcn_readlane((int)last, at);
-        const int64_t piece = pg * kJoinPieces + at;
+        const int64_t piece = pg * kJoinPieces + which;
+        const uint32_t id = id_of(a.keys[piece * kPiece + kPiece - 1]);  // the last of its piece, which is full
         // the pieces behind it that begin with this row
         int64_t more = 0;
         for (;;) {
@@ -257,8 +317,9 @@ template <bool BF16, bool ADD> __global__ __launch_bounds__(256) void k_grad_joi
         }
         float sum[4] = {};
         if (left > 0) {
-            const float* own = a.part + (piece * 2 + ((whole_mask >> at) & 1 ? 0 : 1)) * a.part_ld + col;
+            const float* own = a.part + (piece * 2 + __builtin_amdgcn_readlane((int)slot, which) - 1) * a.part_ld + col;
             const float* next = a.part + (piece + 1) * 2 * a.part_ld + col;
+#pragma unroll 4
             for (int64_t k = wave; k <= more; k += 4) {
                 const float4 v = *reinterpret_cast<const float4*>(k == 0 ? own : next + (k - 1) * 2 * a.part_ld);
                 sum[0] += v.x, sum[1] += v.y, sum[2] += v.z, sum[3] += v.w;
@@ -272,7 +333,7 @@ template <bool BF16, bool ADD> __global__ __launch_bounds__(256) void k_grad_joi
                 const float4 v = lds[w][lane];
                 sum[0] += v.x, sum[1] += v.y, sum[2] += v.z, sum[3] += v.w;
             }
-            store_grad<BF16, ADD, 4>(a.grad, id, col, left, a.scale, sum);
+            store_grad<BF16, ADD, 4>(a.grad, id, col, 0, left, a.scale, sum);
         }
     }
 }
@@ -281,10 +342,12 @@ size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
 int64_t parts_of(int64_t n, int64_t part) { return (n + part - 1) / part; }
 
 template <bool BF16, bool ADD> void launch_sums(const GradArgs& a, hipStream_t st) {
-    k_grad_pieces<BF16, ADD><<<grid_of(parts_of(a.pieces * a.slabs, 4)), dim3(256), 0, st>>>(a);
-    if (a.pieces > 1) {
+    const dim3 g = grid_of(parts_of(a.pieces * a.slabs, 4)), b(256);
+    if (a.cols < 8) k_grad_pieces<BF16, ADD, true><<<g, b, 0, st>>>(a);
+    else k_grad_pieces<BF16, ADD, false><<<g, b, 0, st>>>(a);
+    if (a.n > kShort) {
         const int64_t cg = parts_of(a.cols, kJoinCols);
-        k_grad_join<BF16, ADD><<<grid_of(parts_of(a.pieces - 1, kJoinPieces) * cg), dim3(256), 0, st>>>(a, cg);
+        k_grad_join<BF16, ADD><<<grid_of(parts_of(a.pieces, kJoinPieces) * cg), dim3(256), 0, st>>>(a, cg);
     }
 }
 
@@ -310,11 +373,19 @@ hipError_t launch_embedding(const Ids& ids, const Dense& table, const MxMat& mx,
     return hipGetLastError();
 }
 
+// The parts of a gradient's workspace: keys twice, the pieces' flags, the long rows' sums.
+struct GradWorkspace {
+    size_t keys, flags, part;
+    GradWorkspace(int64_t tokens, int64_t cols) {
+        const int64_t pieces = parts_of(tokens, kPiece);
+        keys = round256(sizeof(uint64_t) * (size_t)tokens);
+        flags = round256(sizeof(uint32_t) * (size_t)pieces);
+        part = tokens > kShort ? sizeof(float) * (size_t)(pieces * 2 * parts_of(cols, 8) * 8) : 0;
+    }
+};
 size_t embedding_grad_workspace(int64_t tokens, int64_t cols) {
-    if (tokens == 0) return 0;
-    const size_t keys = round256(sizeof(uint64_t) * (size_t)tokens);
-    const size_t part = sizeof(float) * (size_t)(parts_of(tokens, kPiece) * 2 * parts_of(cols, 8) * 8);
-    return 2 * keys + (tokens > kPiece ? part : 0);
+    const GradWorkspace w(tokens, cols);
+    return tokens == 0 ? 0 : 2 * w.keys + w.flags + w.part;
 }
 
 hipError_t launch_embedding_grad(const Ids& ids, const Dense& dy, float scale, int64_t rows, int64_t cols,
@@ -324,21 +395,23 @@ hipError_t launch_embedding_grad(const Ids& ids, const Dense& dy, float scale, i
     if (!add) {
         const int64_t unit = grad.dtype == Q4MX_BF16 ? 2 : 4;
         const bool flat = grad.ld == cols || rows == 1;
-        fill.p = grad.p;
-        fill.rows = flat ? 1 : rows;
+        fill.p = static_cast<char*>(grad.p);
         fill.row_bytes = (flat ? rows * cols : cols) * unit;
         fill.pitch = grad.ld * unit;
-        fill.row_blocks = parts_of(fill.row_bytes, kFillBytes);
-        fill.blocks = fill.rows * fill.row_blocks;
+        fill.row_pieces = parts_of(fill.row_bytes, 16);
+        fill.pieces = (flat ? 1 : rows) * fill.row_pieces;
+        fill.blocks = parts_of(fill.pieces, kFillPieces);
     }
-    uint64_t* keys = static_cast<uint64_t*>(ws);
-    uint64_t* other = reinterpret_cast<uint64_t*>(static_cast<char*>(ws) + round256(sizeof(uint64_t) * (size_t)n));
-    k_sort_tiles<<<grid_of(tiles + fill.blocks), dim3(256), 0, st>>>(ids, rows, keys, tiles, fill);
+    const GradWorkspace w(n, cols);
+    char* p = static_cast<char*>(ws);
+    uint64_t *keys = reinterpret_cast<uint64_t*>(p), *other = reinterpret_cast<uint64_t*>(p + w.keys);
+    k_sort_tiles<<<grid_of(tiles + fill.blocks, kSortTile), dim3(kSortTile), 0, st>>>(ids, rows, keys, tiles, fill);
     if (n == 0) return hipGetLastError();
     GradArgs a = {};
-    a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + 2 * round256(sizeof(uint64_t) * (size_t)n));
+    a.long_begins = reinterpret_cast<uint32_t*>(p + 2 * w.keys);
+    a.part = reinterpret_cast<float*>(p + 2 * w.keys + w.flags);
     for (int64_t run = kSortTile; run < n; run *= kMergeRuns) {
-        k_merge_runs<<<grid_of(parts_of(n, 256)), dim3(256), 0, st>>>(keys, other, n, run);
+        k_merge_runs<<<grid_of(parts_of(n, 16)), dim3(256), 0, st>>>(keys, other, n, run);
         uint64_t* t = keys;
         keys = other, other = t;
     }
