@@ -50,36 +50,37 @@ __global__ __launch_bounds__(256) void k_embedding(Ids ids, Dense table, MxMat m
 //      at 7.9 TB/s where reads and writes together reach 5.1;
 //   2. up to 16 sorted runs at a time are merged: an element's place is the
 //      number of smaller ones in all of them;
-//   3. a wave takes the rows that begin in a piece of 16 sorted tokens, 512
+//   3. a wave takes the rows that begin in a piece of 8 or 16 sorted tokens, 512
 //      columns of them.  A row of up to 32 tokens is summed whole, past the
 //      piece's end where it has to; of a longer one every piece that it touches
 //      leaves an FP32 sum in the workspace;
 //   4. those are joined, in the order of the pieces.
 // Keys are (id << 32) | position; a token that counts for no row has the id
 // kNone and lies behind all others.
-constexpr int kSortTile = 1024, kMergeRuns = 16, kPiece = 16, kShort = 32, kSlab = 512;
+constexpr int kSortTile = 1024, kMergeRuns = 16, kShort = 32, kSlab = 512;
+constexpr int kPiece = 16, kSmallPiece = 8;  // sorted tokens (see piece_of)
 constexpr int kJoinCols = 256, kJoinPieces = 16;
 constexpr uint32_t kNone = 0x80000000u;   // above every id; one more is a number too
-constexpr int kFillPieces = 8 * kSortTile;  // 16 bytes of zeros each, of a work-group
 
 __device__ __forceinline__ uint32_t id_of(uint64_t key) { return (uint32_t)(key >> 32); }
 
-// Zeros into part `block` of grad: 16-byte pieces, the last of a row shorter.
+// Zeros into 16-byte pieces of grad, the last of a row shorter.
 struct Fill {
     char* p;
     int64_t row_bytes, pitch;  // one row if the rows follow each other
-    int64_t pieces, row_pieces;
-    int64_t blocks;
+    int64_t row_pieces, end;   // of all pieces, up to `end`
 };
-__device__ __forceinline__ void fill_zero(const Fill& f, int64_t block) {
-    const int64_t first = block * kFillPieces, row = first / f.row_pieces;
+constexpr int kFillRounds = 8;                       // pieces of a thread
+constexpr int64_t kMergeFill = (int64_t(32) << 20) / 16;  // beside a merge: what is written while it waits for its loads
+template <int THREADS> __device__ __forceinline__ void fill_zero(const Fill& f, int64_t first) {
+    const int64_t row = first / f.row_pieces;
     const uint32_t at = (uint32_t)(first - row * f.row_pieces);
 #pragma unroll
-    for (int k = 0; k < kFillPieces; k += kSortTile) {
-        if (first + k + threadIdx.x >= f.pieces) return;
-        int64_t r = 0, i = first + k + threadIdx.x;
-        if (f.pieces != f.row_pieces) {
-            const uint32_t local = at + k + threadIdx.x, rows = local / (uint32_t)f.row_pieces;
+    for (int k = 0; k < kFillRounds; ++k) {
+        int64_t r = 0, i = first + k * THREADS + threadIdx.x;
+        if (i >= f.end) return;
+        if (f.pitch != 0) {
+            const uint32_t local = at + k * THREADS + threadIdx.x, rows = local / (uint32_t)f.row_pieces;
             r = row + rows, i = local - rows * (uint32_t)f.row_pieces;
         }
         char* p = f.p + r * f.pitch + i * 16;
@@ -92,18 +93,37 @@ __device__ __forceinline__ void fill_zero(const Fill& f, int64_t block) {
     }
 }
 
+// The number of the 2^LOG sorted ids from `run` on that are below `bound`.
+template <int LOG> __device__ __forceinline__ int count_below(const uint32_t* run, uint32_t bound) {
+    int pos = 0;
+#pragma unroll
+    for (int step = 1 << (LOG - 1); step > 0; step /= 2)
+        if (run[pos + step - 1] < bound) pos += step;
+    return pos + (run[pos] < bound ? 1 : 0);
+}
+
+// A thread's id of one of four neighbouring sorted runs of 2^LOG: its place
+// among all of them.  Equal ids keep the order of the runs.
+template <int LOG> __device__ __forceinline__ int place_in_four(const uint32_t* four, int at, uint32_t id) {
+    const int own = at >> LOG;
+    int place = at & ((1 << LOG) - 1);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const int below = count_below<LOG>(four + (r << LOG), id + (r < own ? 1u : 0u));
+        if (r != own) place += below;
+    }
+    return place;
+}
+
 // A wave ranks its 64 ids by comparing each with each (equal ones by their
-// position), which leaves 16 sorted runs in shared memory; then a key's place
-// is its place in its own run and the numbers of ids before it in the others,
-// found by 16 binary searches side by side.
+// position); four such runs, and then four of 256, become one by binary
+// searches in shared memory.  (A bitonic sort's 55 exchanges took 11.8 us, 15
+// searches of 64 at once 7.2.)
 __global__ __launch_bounds__(kSortTile) void k_sort_tiles(Ids ids, int64_t rows, uint64_t* keys, int64_t tiles,
                                                            Fill fill) {
-    __shared__ uint32_t run_id[kSortTile], run_token[kSortTile];
+    __shared__ uint32_t run_id[2][kSortTile], run_token[2][kSortTile];
     const int64_t tile = group_index();
-    if (tile >= tiles) {
-        if (tile - tiles < fill.blocks) fill_zero(fill, tile - tiles);
-        return;
-    }
+    if (tile >= tiles) return fill_zero<kSortTile>(fill, (tile - tiles) * (kSortTile * kFillRounds));
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int64_t t = tile * kSortTile + tid;
     uint32_t id = kNone;
@@ -117,32 +137,31 @@ __global__ __launch_bounds__(kSortTile) void k_sort_tiles(Ids ids, int64_t rows,
         const uint32_t other = (uint32_t)__builtin_amdgcn_readlane((int)id, j);
         rank += other < id + (j < lane ? 1u : 0u) ? 1 : 0;
     }
-    run_id[wave * 64 + rank] = id;
-    run_token[wave * 64 + rank] = (uint32_t)t;
+    run_id[0][wave * 64 + rank] = id;
+    run_token[0][wave * 64 + rank] = (uint32_t)t;
     __syncthreads();
-    id = run_id[tid];
-    int place = lane;
-    int pos[16];
-#pragma unroll
-    for (int r = 0; r < 16; ++r) pos[r] = 0;
-#pragma unroll
-    for (int step = 32; step > 0; step /= 2)
-#pragma unroll
-        for (int r = 0; r < 16; ++r)
-            if (run_id[r * 64 + pos[r] + step - 1] < id + (r < wave ? 1u : 0u)) pos[r] += step;
-#pragma unroll
-    for (int r = 0; r < 16; ++r) {
-        const int found = pos[r] + (run_id[r * 64 + pos[r]] < id + (r < wave ? 1u : 0u) ? 1 : 0);
-        if (r != wave) place += found;
+    id = run_id[0][tid];
+    uint32_t token = run_token[0][tid];
+    int place = (tid & ~255) + place_in_four<6>(run_id[0] + (tid & ~255), tid & 255, id);
+    if (ids.n > 256) {
+        run_id[1][place] = id;
+        run_token[1][place] = token;
+        __syncthreads();
+        id = run_id[1][tid], token = run_token[1][tid];
+        place = place_in_four<8>(run_id[1], tid, id);
     }
     // past the last token: ids of kNone from the end of the tile, so they are the last
-    if (tile * kSortTile + place < ids.n) keys[tile * kSortTile + place] = (uint64_t)id << 32 | run_token[tid];
+    if (tile * kSortTile + place < ids.n) keys[tile * kSortTile + place] = (uint64_t)id << 32 | token;
 }
 
 // Runs of `run` keys, the last one shorter: each kMergeRuns neighbours become
-// one.  16 lanes to a key, a run to each.
-__global__ __launch_bounds__(256) void k_merge_runs(const uint64_t* src, uint64_t* dst, int64_t n, int64_t run) {
-    const int64_t i = (int64_t)group_index() * 16 + (threadIdx.x >> 4);
+// one.  16 lanes to a key, a run to each.  (A thread to a key took 32 us for
+// 16384 keys, this 5.8: 11 loads that wait for each other in place of 165.)
+__global__ __launch_bounds__(256) void k_merge_runs(const uint64_t* src, uint64_t* dst, int64_t n, int64_t run,
+                                                     Fill fill, int64_t fill_from) {
+    const int64_t groups = (n + 15) / 16, block = group_index();
+    if (block >= groups) return fill_zero<256>(fill, fill_from + (block - groups) * (256 * kFillRounds));
+    const int64_t i = block * 16 + (threadIdx.x >> 4);
     if (i >= n) return;
     const uint64_t key = src[i];
     const int64_t group = i / (run * kMergeRuns) * (run * kMergeRuns);
@@ -188,6 +207,7 @@ __device__ __forceinline__ void store_grad(const Dense& grad, int64_t row, int64
 struct GradArgs {
     const uint64_t* keys;
     int64_t n, pieces, slabs;
+    int piece;  // tokens of one
     const uint16_t* dy;
     int64_t lddy, cols, part_ld;
     float* part;     // [pieces][2][part_ld]: of a long row that the piece begins with, and of one that begins behind that
@@ -203,13 +223,13 @@ template <bool BF16, bool ADD, bool NARROW> __global__ __launch_bounds__(256) vo
     const int64_t unit = (int64_t)group_index() * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t piece = unit / a.slabs, slab = unit - piece * a.slabs;
     if (piece >= a.pieces) return;
-    const int64_t begin = piece * kPiece;
-    // the piece and the 48 tokens behind it; the 32 before it
+    const int64_t begin = piece * a.piece;
+    // the piece and what is behind it, 64 tokens; the 32 before it
     const uint64_t key = begin + lane < a.n ? a.keys[begin + lane] : ~uint64_t(0);
     const uint32_t id = id_of(key), token = (uint32_t)key;
     const uint32_t before = lane < kShort && begin - kShort + lane >= 0 ? id_of(a.keys[begin - kShort + lane]) : ~0u;
     const int real = __builtin_popcountll(__builtin_amdgcn_ballot_w64(id < kNone));
-    const int count = real < kPiece ? real : kPiece;
+    const int count = real < a.piece ? real : a.piece;
     int from = 0, end = 0;
     bool first_long = false, last_long = false;
     if (count > 0) {
@@ -224,7 +244,7 @@ template <bool BF16, bool ADD, bool NARROW> __global__ __launch_bounds__(256) vo
         const uint64_t mask = __builtin_amdgcn_ballot_w64(id == last);
         const int start = __builtin_ctzll(mask), length = __builtin_popcountll(mask);
         last_long = (start > 0 || !first_long) && length > kShort;  // begins here, and more than 32 follow
-        end = last_long || (start == 0 && first_long) ? (start + length < kPiece ? start + length : kPiece) : start + length;
+        end = last_long || (start == 0 && first_long) ? (start + length < a.piece ? start + length : a.piece) : start + length;
         if (slab == 0 && lane == 0) a.long_begins[piece] = last_long ? (start == 0 ? 1 : 2) : 0;
     } else {
         if (slab == 0 && lane == 0) a.long_begins[piece] = 0;
@@ -261,7 +281,7 @@ template <bool BF16, bool ADD, bool NARROW> __global__ __launch_bounds__(256) vo
             const int e = i + j < end ? i + j : end - 1;
             const uint16_t* p = a.dy + (int64_t)(uint32_t)__builtin_amdgcn_readlane((int)token, e) * a.lddy + at;
             if (!NARROW) {
-                raw[j] = *reinterpret_cast<const u32x4_any*>(p);
+                raw[j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_any*>(p));
             } else {
                 uint32_t w[8];
 #pragma unroll
@@ -303,12 +323,12 @@ template <bool BF16, bool ADD> __global__ __launch_bounds__(256) void k_grad_joi
         const int which = __builtin_ctzll(todo);
         todo &= todo - 1;
         const int64_t piece = pg * kJoinPieces + which;
-        const uint32_t id = id_of(a.keys[piece * kPiece + kPiece - 1]);  // the last of its piece, which is full
+        const uint32_t id = id_of(a.keys[piece * a.piece + a.piece - 1]);  // the last of its piece, which is full
         // the pieces behind it that begin with this row
         int64_t more = 0;
         for (;;) {
             const int64_t q = piece + 1 + more + lane;
-            const uint64_t other = __builtin_amdgcn_ballot_w64(!(q < a.pieces && id_of(a.keys[q * kPiece]) == id));
+            const uint64_t other = __builtin_amdgcn_ballot_w64(!(q < a.pieces && id_of(a.keys[q * a.piece]) == id));
             if (other) {
                 more += __builtin_ctzll(other);
                 break;
@@ -373,11 +393,15 @@ hipError_t launch_embedding(const Ids& ids, const Dense& table, const MxMat& mx,
     return hipGetLastError();
 }
 
+// Few tokens leave compute units idle and a wave's time is its steps': shorter
+// pieces (301 tokens: PLACEHOLDER); for many, fewer sums of long rows count.
+int piece_of(int64_t tokens) { return tokens <= 2048 ? kSmallPiece : kPiece; }
+
 // The parts of a gradient's workspace: keys twice, the pieces' flags, the long rows' sums.
 struct GradWorkspace {
     size_t keys, flags, part;
     GradWorkspace(int64_t tokens, int64_t cols) {
-        const int64_t pieces = parts_of(tokens, kPiece);
+        const int64_t pieces = parts_of(tokens, piece_of(tokens));
         keys = round256(sizeof(uint64_t) * (size_t)tokens);
         flags = round256(sizeof(uint32_t) * (size_t)pieces);
         part = tokens > kShort ? sizeof(float) * (size_t)(pieces * 2 * parts_of(cols, 8) * 8) : 0;
@@ -392,30 +416,38 @@ hipError_t launch_embedding_grad(const Ids& ids, const Dense& dy, float scale, i
                                  const Dense& grad, bool add, void* ws, hipStream_t st) {
     const int64_t n = ids.n, tiles = parts_of(n, kSortTile);
     Fill fill = {};
+    fill.row_pieces = 1;
+    int64_t split = 0, rest = 0;  // zeros up to `split` beside the sort, the rest beside the first merge
     if (!add) {
         const int64_t unit = grad.dtype == Q4MX_BF16 ? 2 : 4;
         const bool flat = grad.ld == cols || rows == 1;
         fill.p = static_cast<char*>(grad.p);
         fill.row_bytes = (flat ? rows * cols : cols) * unit;
-        fill.pitch = grad.ld * unit;
+        fill.pitch = flat ? 0 : grad.ld * unit;
         fill.row_pieces = parts_of(fill.row_bytes, 16);
-        fill.pieces = (flat ? 1 : rows) * fill.row_pieces;
-        fill.blocks = parts_of(fill.pieces, kFillPieces);
+        fill.end = (flat ? 1 : rows) * fill.row_pieces;
+        if (n > kSortTile) rest = fill.end / 2 < kMergeFill ? fill.end / 2 : kMergeFill;
+        split = fill.end - rest;
     }
     const GradWorkspace w(n, cols);
     char* p = static_cast<char*>(ws);
     uint64_t *keys = reinterpret_cast<uint64_t*>(p), *other = reinterpret_cast<uint64_t*>(p + w.keys);
-    k_sort_tiles<<<grid_of(tiles + fill.blocks, kSortTile), dim3(kSortTile), 0, st>>>(ids, rows, keys, tiles, fill);
+    Fill begun = fill;
+    begun.end = split;
+    k_sort_tiles<<<grid_of(tiles + parts_of(split, kSortTile * kFillRounds), kSortTile), dim3(kSortTile), 0, st>>>(
+        ids, rows, keys, tiles, begun);
     if (n == 0) return hipGetLastError();
     GradArgs a = {};
     a.long_begins = reinterpret_cast<uint32_t*>(p + 2 * w.keys);
     a.part = reinterpret_cast<float*>(p + 2 * w.keys + w.flags);
     for (int64_t run = kSortTile; run < n; run *= kMergeRuns) {
-        k_merge_runs<<<grid_of(parts_of(n, 16)), dim3(256), 0, st>>>(keys, other, n, run);
+        k_merge_runs<<<grid_of(parts_of(n, 16) + parts_of(rest, 256 * kFillRounds)), dim3(256), 0, st>>>(
+            keys, other, n, run, fill, split);
+        rest = 0, fill.end = 0;
         uint64_t* t = keys;
         keys = other, other = t;
     }
-    a.keys = keys, a.n = n, a.pieces = parts_of(n, kPiece), a.slabs = parts_of(cols, kSlab);
+    a.keys = keys, a.n = n, a.piece = piece_of(n), a.pieces = parts_of(n, a.piece), a.slabs = parts_of(cols, kSlab);
     a.dy = static_cast<const uint16_t*>(dy.p), a.lddy = dy.ld;
     a.cols = cols, a.part_ld = parts_of(cols, 8) * 8;
     a.scale = scale, a.grad = grad;

@@ -11,21 +11,25 @@
 // pair up the same way, with the angle 0.
 //
 // The angles of a token are those of all its heads, and FP64: a work-group
-// forms the cosines and sines of its tokens once, in shared memory.
+// forms the cosines and sines of its tokens once, in shared memory.  Its four
+// waves then walk the rows, q's first; the loads of a wave's next rows are on
+// their way while it computes, those of its first ones while the angles are
+// formed.
 #include "q4_mx_dev.h"
 #include "q4_nn.h"
 
 namespace q4 {
 namespace {
 
-constexpr int kTokens = 16, kAngles = 2048;  // most tokens and angles of a work-group
+constexpr int kTokens = 32, kAngles = 2048;  // most tokens and angles of a work-group
 constexpr int kMaxGroups = 1024;             // of a backward pass: each leaves one sum of the gains' gradients
 
 struct HeadsArgs {
     q4nn_heads v[6];  // q, k, dq, dk, q_out, k_out (backward: dq_in, dk_in)
     const void *positions, *gain[2];
     const double* frequencies;
-    int64_t position_batch, position_token, total, per_batch, blocks;
+    int64_t position_batch, position_token;
+    int64_t per_batch, batch_blocks, blocks;  // tokens and work-groups' parts of a batch, and all parts
     int heads[2];
     uint32_t magic[2];  // ceil(2^32 / heads)
     int dim, half, pairs, log_lanes, tokens;
@@ -71,30 +75,6 @@ __device__ __forceinline__ float row_sum(float x, int log_lanes) {
     return x;
 }
 
-// VEC elements of a dense BF16 or FP32 run.
-template <int VEC, bool BF16> __device__ __forceinline__ void load_vec(const void* p, int64_t i, float* v) {
-    if (VEC == 8) {
-        load8<BF16>(p, i, 8, v);
-    } else if (VEC == 4 && BF16) {
-        const u32x2_any q = *reinterpret_cast<const u32x2_any*>(static_cast<const uint16_t*>(p) + i);
-        v[0] = bf16_value(q[0] & 0xFFFFu), v[1] = __uint_as_float(q[0] & 0xFFFF0000u);
-        v[2] = bf16_value(q[1] & 0xFFFFu), v[3] = __uint_as_float(q[1] & 0xFFFF0000u);
-    } else {
-#pragma unroll
-        for (int k = 0; k < VEC; ++k) v[k] = load1<BF16>(p, i + k);
-    }
-}
-template <int VEC> __device__ __forceinline__ void store_vec(uint16_t* p, int64_t i, const float* v) {
-    if (VEC == 8) {
-        store8<true>(p, i, 8, v);
-    } else if (VEC == 4) {
-        *reinterpret_cast<u32x2_any*>(p + i) = u32x2_any{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
-    } else {
-#pragma unroll
-        for (int k = 0; k < VEC; ++k) p[i + k] = bf16_bits(v[k]);
-    }
-}
-
 // Where a lane's VEC pairs from pair u on lie: two vectors at e[0] and e[1].
 // INTER: pairs are neighbours.  Else the halves of the rotary part, behind it
 // the halves of the rest.
@@ -106,178 +86,236 @@ template <int VEC, bool INTER> struct Place {
         else e[0] = u + a.half, e[1] = u + a.pairs;
     }
 };
-// The pairs' first and second elements of two vectors, and back.
-template <int VEC, bool INTER> __device__ __forceinline__ void split_pairs(const float* v, float* p, float* s) {
+
+// A lane's pairs of a row as they lie in memory: VEC words, the two vectors one
+// behind the other.
+template <int VEC> struct Words {
+    uint32_t w[VEC];
+};
+template <int VEC> __device__ __forceinline__ Words<VEC> load_words(const uint16_t* p, const int* e) {
+    Words<VEC> r;
+    if (VEC == 8) {
+        const u32x4_any a = *reinterpret_cast<const u32x4_any*>(p + e[0]), b = *reinterpret_cast<const u32x4_any*>(p + e[1]);
 #pragma unroll
-    for (int k = 0; k < VEC; ++k) p[k] = v[INTER ? 2 * k : k], s[k] = v[INTER ? 2 * k + 1 : VEC + k];
+        for (int k = 0; k < 4; ++k) r.w[k] = a[k], r.w[(4 + k) % VEC] = b[k];
+    } else if (VEC == 4) {
+        const u32x2_any a = *reinterpret_cast<const u32x2_any*>(p + e[0]), b = *reinterpret_cast<const u32x2_any*>(p + e[1]);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) r.w[k] = a[k], r.w[(2 + k) % VEC] = b[k];
+    } else {
+        r.w[0] = (uint32_t)p[e[0]] | (uint32_t)p[e[1]] << 16;
+    }
+    return r;
 }
-template <int VEC, bool INTER> __device__ __forceinline__ void join_pairs(const float* p, const float* s, float* v) {
+template <int VEC> __device__ __forceinline__ void store_words(uint16_t* p, const int* e, const Words<VEC>& r) {
+    if (VEC == 8) {
+        *reinterpret_cast<u32x4_any*>(p + e[0]) = u32x4_any{r.w[0], r.w[1 % VEC], r.w[2 % VEC], r.w[3 % VEC]};
+        *reinterpret_cast<u32x4_any*>(p + e[1]) = u32x4_any{r.w[4 % VEC], r.w[5 % VEC], r.w[6 % VEC], r.w[7 % VEC]};
+    } else if (VEC == 4) {
+        *reinterpret_cast<u32x2_any*>(p + e[0]) = u32x2_any{r.w[0], r.w[1 % VEC]};
+        *reinterpret_cast<u32x2_any*>(p + e[1]) = u32x2_any{r.w[2 % VEC], r.w[3 % VEC]};
+    } else {
+        p[e[0]] = (uint16_t)r.w[0], p[e[1]] = (uint16_t)(r.w[0] >> 16);
+    }
+}
+// The pairs' first and second elements, and back.
+template <int VEC, bool INTER> __device__ __forceinline__ void split_pairs(const Words<VEC>& r, float* p, float* s) {
+    const auto lo = [](uint32_t w) { return __uint_as_float(w << 16); };
+    const auto hi = [](uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); };
 #pragma unroll
-    for (int k = 0; k < VEC; ++k) v[INTER ? 2 * k : k] = p[k], v[INTER ? 2 * k + 1 : VEC + k] = s[k];
+    for (int k = 0; k < VEC; ++k) {
+        if (INTER || VEC == 1) {
+            p[k] = lo(r.w[k]), s[k] = hi(r.w[k]);
+        } else {
+            p[k] = k & 1 ? hi(r.w[k / 2]) : lo(r.w[k / 2]);
+            s[k] = k & 1 ? hi(r.w[VEC / 2 + k / 2]) : lo(r.w[VEC / 2 + k / 2]);
+        }
+    }
+}
+template <int VEC, bool INTER> __device__ __forceinline__ Words<VEC> join_pairs(const float* p, const float* s) {
+    Words<VEC> r;
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) {
+        if (INTER || VEC == 1) r.w[k] = bf16_pair(p[k], s[k]);
+        else if (k < VEC / 2) r.w[k] = bf16_pair(p[2 * k], p[(2 * k + 1) % VEC]);
+        else r.w[k] = bf16_pair(s[2 * k - VEC], s[(2 * k + 1) % VEC]);
+    }
+    return r;
 }
 
-// The rows of `which` (0: q, 1: k) of a work-group's tokens; K vectors of
-// pairs to a lane.  acc: the gain's gradient, pairs' first elements and second.
+// K vectors of pairs to a lane (one, but for heads of odd sizes above 128).
 template <int VEC, int K, bool INTER, bool BACK>
-__device__ __forceinline__ void rows_of(const HeadsArgs& a, int which, int tokens, const float2* angles,
-                                        const int64_t (*at)[6], float (*acc)[2 * VEC]) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, lanes = 1 << a.log_lanes;
-    const int sub = lane & (lanes - 1), per_wave = 64 >> a.log_lanes;
-    const int heads = a.heads[which], rows = tokens * heads;
-    if (rows == 0) return;
-    const q4nn_heads &in = a.v[which], &grad = a.v[2 + which], &out = a.v[4 + which];
-    float gp[K][VEC], gs[K][VEC];
-#pragma unroll
-    for (int c = 0; c < K; ++c) {
-        const int u = (c * lanes + sub) * VEC;
-        if (u >= a.pairs) break;
-        const Place<VEC, INTER> e(a, u);
-        float v[2 * VEC];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            if (a.gain_bf16) load_vec<VEC, true>(a.gain[which], e.e[h], v + h * VEC);
-            else load_vec<VEC, false>(a.gain[which], e.e[h], v + h * VEC);
-        }
-        split_pairs<VEC, INTER>(v, gp[c], gs[c]);
+__global__ __launch_bounds__(256, K == 1 ? 4 : 1) void k_heads(HeadsArgs a) {
+    extern __shared__ float4 shared[];
+    // gains [2][dim], backward: sums [4 waves][2][dim]; angles
+    float* gains = reinterpret_cast<float*>(shared);
+    float* sums = gains + 2 * a.dim;
+    float2* angles = reinterpret_cast<float2*>(sums + (BACK ? 8 * a.dim : 0));
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lanes = 1 << a.log_lanes;
+    const int sub = lane & (lanes - 1), mine = lane >> a.log_lanes, per_wave = 64 >> a.log_lanes;
+    for (int i = threadIdx.x; i < 2 * a.dim; i += 256) {
+        const int w = i >= a.dim, at = i - (w ? a.dim : 0);
+        gains[i] = a.heads[w] == 0 ? 0.0f : a.gain_bf16 ? load1<true>(a.gain[w], at) : load1<false>(a.gain[w], at);
     }
-    // q's rows go to the first waves first, k's to the last
-    for (int r = (which ? 3 - wave : wave) * per_wave + (lane >> a.log_lanes); r < rows; r += 4 * per_wave) {
-        // r / heads: the reciprocal is less than heads 2^-32 of itself too large, and r < 16 * 4096: r heads < 2^32
-        const int tok = heads == 1 ? r : (int)__umulhi((uint32_t)r, a.magic[which]), head = r - tok * heads;
-        const uint16_t* x = in.p + at[tok][which] + head * in.head;
-        const uint16_t* dy = BACK ? grad.p + at[tok][2 + which] + head * grad.head : nullptr;
-        uint16_t* y = out.p + at[tok][4 + which] + head * out.head;
-        float xp[K][VEC], xs[K][VEC], dp[K][VEC], ds[K][VEC], sum = 0.0f;
+    if (BACK)
+        for (int i = threadIdx.x; i < 8 * a.dim; i += 256) sums[i] = 0.0f;
+
+    for (int64_t block = group_index(); block < a.blocks; block += (int64_t)gridDim.x * gridDim.y) {
+        const int64_t b = block / a.batch_blocks, t0 = (block - b * a.batch_blocks) * a.tokens;
+        const int tokens = (int)(a.per_batch - t0 < a.tokens ? a.per_batch - t0 : a.tokens);
+        const int rows_q = tokens * a.heads[0], rows_k = tokens * a.heads[1];
+        const int steps_q = (rows_q + 4 * per_wave - 1) / (4 * per_wave);
+        const int steps = steps_q + (rows_k + 4 * per_wave - 1) / (4 * per_wave);
+        // Step i of a wave: its rows' tensor, and this lane's row.  q's rows go to the first waves first, k's to the last.
+        const auto row_of = [&](int i) {
+            return i < steps_q ? (i * 4 + wave) * per_wave + mine : ((i - steps_q) * 4 + 3 - wave) * per_wave + mine;
+        };
+        // r / heads: the reciprocal is less than heads 2^-32 of itself too large, and r < 32 * 4096 + 256, heads <= 4096
+        const auto token_of = [&](int r, int w) {
+            return a.heads[w] == 1 ? r : (int)__umulhi((uint32_t)r, a.magic[w]);
+        };
+        const auto place_of = [&](const q4nn_heads& v, int tok, int head) {
+            return v.p + (b * v.batch + t0 * v.token) + (tok * v.token + head * v.head);
+        };
+        struct Loaded {
+            Words<VEC> x[K], dy[BACK ? K : 1];
+        };
+        const auto load_step = [&](int i) {
+            Loaded l = {};
+            const int w = i < steps_q ? 0 : 1, r = row_of(i);
+            if (r < (w ? rows_k : rows_q)) {
+                const int tok = token_of(r, w), head = r - tok * a.heads[w];
+                const uint16_t* x = place_of(a.v[w], tok, head);
+                const uint16_t* dy = BACK ? place_of(a.v[2 + w], tok, head) : nullptr;
 #pragma unroll
-        for (int c = 0; c < K; ++c) {
-            const int u = (c * lanes + sub) * VEC;
-#pragma unroll
-            for (int k = 0; k < VEC; ++k) xp[c][k] = xs[c][k] = dp[c][k] = ds[c][k] = 0.0f;
-            if (u >= a.pairs) continue;
-            const Place<VEC, INTER> e(a, u);
-            float v[2 * VEC];
-            load_vec<VEC, true>(x, e.e[0], v);
-            load_vec<VEC, true>(x, e.e[1], v + VEC);
-            split_pairs<VEC, INTER>(v, xp[c], xs[c]);
-            if (BACK) {
-                load_vec<VEC, true>(dy, e.e[0], v);
-                load_vec<VEC, true>(dy, e.e[1], v + VEC);
-                split_pairs<VEC, INTER>(v, dp[c], ds[c]);
-            }
-#pragma unroll
-            for (int k = 0; k < VEC; ++k) sum = __builtin_fmaf(xp[c][k], xp[c][k], __builtin_fmaf(xs[c][k], xs[c][k], sum));
-        }
-        const float inv = __builtin_amdgcn_rsqf(__builtin_fmaf(row_sum(sum, a.log_lanes), a.inv_dim, a.eps));
-        float along = 0.0f;
-#pragma unroll
-        for (int c = 0; c < K; ++c) {
-            const int u = (c * lanes + sub) * VEC;
-            if (u >= a.pairs) continue;
-            const float2* t = angles + tok * a.pairs + u;
-            float p[VEC], s[VEC];
-#pragma unroll
-            for (int k = 0; k < VEC; ++k) {
-                const float2 w = t[k];
-                xp[c][k] *= inv, xs[c][k] *= inv;  // n
-                if (!BACK) {
-                    const float yp = xp[c][k] * gp[c][k], ys = xs[c][k] * gs[c][k];
-                    p[k] = __builtin_fmaf(yp, w.x, -(ys * w.y));
-                    s[k] = __builtin_fmaf(ys, w.x, yp * w.y);
-                } else {
-                    const float up = __builtin_fmaf(dp[c][k], w.x, ds[c][k] * w.y);  // turned back
-                    const float us = __builtin_fmaf(ds[c][k], w.x, -(dp[c][k] * w.y));
-                    acc[c][k] = __builtin_fmaf(up, xp[c][k], acc[c][k]);
-                    acc[c][VEC + k] = __builtin_fmaf(us, xs[c][k], acc[c][VEC + k]);
-                    dp[c][k] = up * gp[c][k], ds[c][k] = us * gs[c][k];
-                    along = __builtin_fmaf(dp[c][k], xp[c][k], __builtin_fmaf(ds[c][k], xs[c][k], along));
+                for (int c = 0; c < K; ++c) {
+                    const int u = (c * lanes + sub) * VEC;
+                    if (u >= a.pairs) continue;
+                    const Place<VEC, INTER> e(a, u);
+                    l.x[c] = load_words<VEC>(x, e.e);
+                    if (BACK) l.dy[c] = load_words<VEC>(dy, e.e);
                 }
             }
-            if (!BACK) {
-                const Place<VEC, INTER> e(a, u);
-                float v[2 * VEC];
-                join_pairs<VEC, INTER>(p, s, v);
-                store_vec<VEC>(y, e.e[0], v);
-                store_vec<VEC>(y, e.e[1], v + VEC);
+            return l;
+        };
+        Loaded now = load_step(0);
+        __syncthreads();  // the block before is done with the angles
+        for (int i = threadIdx.x; i < tokens * a.pairs; i += 256) {
+            const int tok = i / a.pairs, u = i - tok * a.pairs;
+            float2 w = make_float2(1.0f, 0.0f);
+            if (u < a.half) {
+                const int64_t at = b * a.position_batch + (t0 + tok) * a.position_token;
+                const double position = a.positions_wide ? (double)static_cast<const int64_t*>(a.positions)[at]
+                                                         : (double)static_cast<const int32_t*>(a.positions)[at];
+                w = cos_sin(position * a.frequencies[u]);
             }
+            angles[i] = w;
         }
-        if (!BACK) continue;
-        const float mean = row_sum(along, a.log_lanes) * a.inv_dim;
-#pragma unroll
-        for (int c = 0; c < K; ++c) {
-            const int u = (c * lanes + sub) * VEC;
-            if (u >= a.pairs) continue;
-            float p[VEC], s[VEC], v[2 * VEC];
-#pragma unroll
-            for (int k = 0; k < VEC; ++k) {
-                p[k] = inv * __builtin_fmaf(-xp[c][k], mean, dp[c][k]);
-                s[k] = inv * __builtin_fmaf(-xs[c][k], mean, ds[c][k]);
-            }
-            const Place<VEC, INTER> e(a, u);
-            join_pairs<VEC, INTER>(p, s, v);
-            store_vec<VEC>(y, e.e[0], v);
-            store_vec<VEC>(y, e.e[1], v + VEC);
-        }
-    }
-}
-
-template <int VEC, int K, bool INTER, bool BACK> __global__ __launch_bounds__(256) void k_heads(HeadsArgs a) {
-    __shared__ float2 angles[kAngles];
-    __shared__ int64_t at[kTokens][6];
-    __shared__ double position[kTokens];
-    float acc[2][K][2 * VEC];
-#pragma unroll
-    for (int w = 0; w < 2; ++w)
+        __syncthreads();
+        float acc[K][2 * VEC];  // of the gain's gradient: pairs' first elements and second
 #pragma unroll
         for (int c = 0; c < K; ++c)
 #pragma unroll
-            for (int k = 0; k < 2 * VEC; ++k) acc[w][c][k] = 0.0f;
-    for (int64_t block = group_index(); block < a.blocks; block += (int64_t)gridDim.x * gridDim.y) {
-        const int64_t first = block * a.tokens;
-        const int tokens = (int)(a.total - first < a.tokens ? a.total - first : a.tokens);
-        if (BACK) __syncthreads();  // the block before is done with the angles
-        if ((int)threadIdx.x < tokens) {
-            const int64_t n = first + threadIdx.x, b = a.total == a.per_batch ? 0 : n / a.per_batch, t = n - b * a.per_batch;
+            for (int k = 0; k < 2 * VEC; ++k) acc[c][k] = 0.0f;
+        for (int i = 0; i < steps; ++i) {
+            const int w = i < steps_q ? 0 : 1, r = row_of(i);
+            Loaded next;
+            if (i + 1 < steps) next = load_step(i + 1);
+            if (r < (w ? rows_k : rows_q)) {
+                const int tok = token_of(r, w), head = r - tok * a.heads[w];
+                float xp[K][VEC], xs[K][VEC], dp[K][VEC], ds[K][VEC], sum = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 6; ++i) at[threadIdx.x][i] = b * a.v[i].batch + t * a.v[i].token;
-            const int64_t i = b * a.position_batch + t * a.position_token;
-            position[threadIdx.x] = a.positions_wide ? (double)static_cast<const int64_t*>(a.positions)[i]
-                                                     : (double)static_cast<const int32_t*>(a.positions)[i];
+                for (int c = 0; c < K; ++c) {
+                    split_pairs<VEC, INTER>(now.x[c], xp[c], xs[c]);  // zeros past the row
+                    if (BACK) split_pairs<VEC, INTER>(now.dy[c], dp[c], ds[c]);
+#pragma unroll
+                    for (int k = 0; k < VEC; ++k)
+                        sum = __builtin_fmaf(xp[c][k], xp[c][k], __builtin_fmaf(xs[c][k], xs[c][k], sum));
+                }
+                const float inv =
+                    __builtin_amdgcn_rsqf(__builtin_fmaf(row_sum(sum, a.log_lanes), a.inv_dim, a.eps));
+                uint16_t* y = place_of(a.v[4 + w], tok, head);
+                float along = 0.0f;
+#pragma unroll
+                for (int c = 0; c < K; ++c) {
+                    const int u = (c * lanes + sub) * VEC;
+                    if (u >= a.pairs) continue;
+                    const Place<VEC, INTER> e(a, u);
+                    const float2* turn = angles + tok * a.pairs + u;
+                    const float *g0 = gains + w * a.dim + e.e[0], *g1 = gains + w * a.dim + e.e[1];
+                    float p[VEC], s[VEC];
+#pragma unroll
+                    for (int k = 0; k < VEC; ++k) {
+                        const float2 t = turn[k];
+                        const float gp = INTER && VEC > 1 ? (2 * k < VEC ? g0[2 * k] : g1[2 * k - VEC]) : g0[k];
+                        const float gs = INTER && VEC > 1 ? (2 * k < VEC ? g0[2 * k + 1] : g1[2 * k + 1 - VEC]) : g1[k];
+                        xp[c][k] *= inv, xs[c][k] *= inv;  // n
+                        if (!BACK) {
+                            const float yp = xp[c][k] * gp, ys = xs[c][k] * gs;
+                            p[k] = __builtin_fmaf(yp, t.x, -(ys * t.y));
+                            s[k] = __builtin_fmaf(ys, t.x, yp * t.y);
+                        } else {
+                            const float up = __builtin_fmaf(dp[c][k], t.x, ds[c][k] * t.y);  // turned back
+                            const float us = __builtin_fmaf(ds[c][k], t.x, -(dp[c][k] * t.y));
+                            acc[c][k] = __builtin_fmaf(up, xp[c][k], acc[c][k]);
+                            acc[c][VEC + k] = __builtin_fmaf(us, xs[c][k], acc[c][VEC + k]);
+                            dp[c][k] = up * gp, ds[c][k] = us * gs;
+                            along = __builtin_fmaf(dp[c][k], xp[c][k], __builtin_fmaf(ds[c][k], xs[c][k], along));
+                        }
+                    }
+                    if (!BACK) store_words<VEC>(y, e.e, join_pairs<VEC, INTER>(p, s));
+                }
+                if (BACK) {
+                    const float mean = row_sum(along, a.log_lanes) * a.inv_dim;
+#pragma unroll
+                    for (int c = 0; c < K; ++c) {
+                        const int u = (c * lanes + sub) * VEC;
+                        if (u >= a.pairs) continue;
+                        float p[VEC], s[VEC];
+#pragma unroll
+                        for (int k = 0; k < VEC; ++k) {
+                            p[k] = inv * __builtin_fmaf(-xp[c][k], mean, dp[c][k]);
+                            s[k] = inv * __builtin_fmaf(-xs[c][k], mean, ds[c][k]);
+                        }
+                        store_words<VEC>(y, Place<VEC, INTER>(a, u).e, join_pairs<VEC, INTER>(p, s));
+                    }
+                }
+            }
+            if (BACK && (i + 1 == steps_q || i + 1 == steps)) {
+                // all of a tensor's rows: the sums over the wave's rows, added to the wave's own
+#pragma unroll
+                for (int c = 0; c < K; ++c) {
+                    const int u = (c * lanes + sub) * VEC;
+#pragma unroll
+                    for (int k = 0; k < 2 * VEC; ++k)
+                        for (int m = lanes; m < 64; m *= 2) acc[c][k] += __shfl_xor(acc[c][k], m);
+                    if (u < a.pairs && lane < lanes) {
+                        const Place<VEC, INTER> e(a, u);
+                        float *p0 = sums + (wave * 2 + w) * a.dim + e.e[0], *p1 = sums + (wave * 2 + w) * a.dim + e.e[1];
+#pragma unroll
+                        for (int k = 0; k < VEC; ++k) {
+                            // INTER: elements 2k and 2k + 1 of the two vectors
+                            if (INTER && VEC > 1) {
+                                (2 * k < VEC ? p0[2 * k] : p1[2 * k - VEC]) += acc[c][k];
+                                (2 * k < VEC ? p0[2 * k + 1] : p1[2 * k + 1 - VEC]) += acc[c][VEC + k];
+                            } else {
+                                p0[k] += acc[c][k], p1[k] += acc[c][VEC + k];
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int k = 0; k < 2 * VEC; ++k) acc[c][k] = 0.0f;
+                }
+            }
+            now = next;
         }
-        __syncthreads();
-        for (int i = threadIdx.x; i < tokens * a.pairs; i += 256) {
-            const int tok = i / a.pairs, u = i - tok * a.pairs;
-            angles[i] = u < a.half ? cos_sin(position[tok] * a.frequencies[u]) : make_float2(1.0f, 0.0f);
-        }
-        __syncthreads();
-        rows_of<VEC, K, INTER, BACK>(a, 0, tokens, angles, at, acc[0]);
-        rows_of<VEC, K, INTER, BACK>(a, 1, tokens, angles, at, acc[1]);
         if (!BACK) return;
     }
     if (!BACK) return;
-    // the work-group's sums: over the rows of a wave, then over the waves
-    float* lds = reinterpret_cast<float*>(angles);  // [4][dim]
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, lanes = 1 << a.log_lanes;
+    __syncthreads();
     float* part = a.part + (int64_t)group_index() * 2 * a.dim;
-#pragma unroll
-    for (int w = 0; w < 2; ++w) {
-        __syncthreads();
-#pragma unroll
-        for (int c = 0; c < K; ++c) {
-            const int u = (c * lanes + (lane & (lanes - 1))) * VEC;
-#pragma unroll
-            for (int k = 0; k < 2 * VEC; ++k)
-                for (int m = lanes; m < 64; m *= 2) acc[w][c][k] += __shfl_xor(acc[w][c][k], m);
-            if (u >= a.pairs || lane >= lanes) continue;
-            const Place<VEC, INTER> e(a, u);
-            float v[2 * VEC];
-            join_pairs<VEC, INTER>(acc[w][c], acc[w][c] + VEC, v);
-#pragma unroll
-            for (int k = 0; k < VEC; ++k) lds[wave * a.dim + e.e[0] + k] = v[k], lds[wave * a.dim + e.e[1] + k] = v[VEC + k];
-        }
-        __syncthreads();
-        for (int i = threadIdx.x; i < a.dim; i += 256)
-            part[w * a.dim + i] = (lds[i] + lds[a.dim + i]) + (lds[2 * a.dim + i] + lds[3 * a.dim + i]);
-    }
+    for (int i = threadIdx.x; i < 2 * a.dim; i += 256)
+        part[i] = (sums[i] + sums[2 * a.dim + i]) + (sums[4 * a.dim + i] + sums[6 * a.dim + i]);
 }
 
 // The gains' gradients from the work-groups' sums: 16 of the 2 dim columns to a
@@ -303,37 +341,59 @@ __global__ __launch_bounds__(1024) void k_gain_grads(const float* part, int64_t 
     else static_cast<float*>(p)[at] = sum;
 }
 
+// The call with its tokens in as few batches as their strides allow: one where
+// the batches follow each other, or have a token each.
+q4nn_rope flat_batches(const q4nn_rope& r, q4nn_heads* const* v, int n) {
+    q4nn_rope f = r;
+    bool follow = r.position_batch == r.tokens * r.position_token;
+    for (int i = 0; i < n; ++i) follow = follow && v[i]->batch == r.tokens * v[i]->token;
+    if (r.batches <= 1 || (!follow && r.tokens > 1)) return f;
+    if (r.tokens == 1) {
+        for (int i = 0; i < n; ++i) v[i]->token = v[i]->batch;
+        f.position_token = r.position_batch;
+    }
+    f.tokens = r.batches * r.tokens, f.batches = 1;
+    return f;
+}
+
 // Pairs to a lane and lanes to a row: 8 (or 4) pairs where both the rotary
 // part and the rest are made of whole vectors, else single ones.
 struct Shape {
-    int vec, log_lanes, tokens;
+    int vec, log_lanes;
 };
 Shape shape_of(const q4nn_rope& r) {
     const int pairs = r.dim / 2, half = r.rotary / 2;
-    Shape s = {1, 0, 1};
+    Shape s = {1, 0};
     for (int v : {8, 4})
         if (s.vec == 1 && pairs % v == 0 && (r.interleaved || half % v == 0) && pairs <= 64 * v) s.vec = v;
     while ((1 << s.log_lanes) * s.vec < pairs && s.log_lanes < 6) ++s.log_lanes;
-    // tokens to a work-group: until its four waves are full of rows of q and of k, while many work-groups are left
-    const int rows = 4 * (64 >> s.log_lanes);
-    int heads = r.q_heads < r.k_heads ? r.q_heads : r.k_heads;
-    if (heads == 0) heads = r.q_heads + r.k_heads;
-    const int64_t total = r.batches * r.tokens;
-    while (s.tokens < kTokens && s.tokens * heads < rows && 2 * s.tokens * pairs <= kAngles &&
-           total / (2 * s.tokens) >= 1024)
-        s.tokens *= 2;
     return s;
 }
 
-HeadsArgs args_of(const q4nn_rope& r, const Shape& s) {
+// Tokens to a work-group's part.  Forward: until its four waves are full of
+// rows of q and of k, while many work-groups are left.  Backward: as many as
+// leave the parts that the chip holds at once.
+int tokens_of(const q4nn_rope& r, const Shape& s, bool back) {
+    const int rows = 4 * (64 >> s.log_lanes), pairs = r.dim / 2;
+    int heads = r.q_heads < r.k_heads ? r.q_heads : r.k_heads, tokens = 1;
+    if (heads == 0) heads = r.q_heads + r.k_heads;
+    while (2 * tokens <= kTokens && 2 * tokens * pairs <= kAngles &&
+           (back ? r.batches * ((r.tokens + tokens - 1) / tokens) > kMaxGroups
+                 : tokens * heads < rows && r.batches * (r.tokens / (2 * tokens)) >= 1024))
+        tokens *= 2;
+    return tokens;
+}
+
+HeadsArgs args_of(const q4nn_rope& r, const Shape& s, bool back) {
     HeadsArgs a = {};
     a.positions = r.positions, a.gain[0] = r.q_gain, a.gain[1] = r.k_gain, a.frequencies = r.frequencies;
     a.position_batch = r.position_batch, a.position_token = r.position_token;
-    a.per_batch = r.tokens, a.total = r.batches * r.tokens, a.blocks = (a.total + s.tokens - 1) / s.tokens;
+    a.tokens = tokens_of(r, s, back);
+    a.per_batch = r.tokens, a.batch_blocks = (r.tokens + a.tokens - 1) / a.tokens, a.blocks = r.batches * a.batch_blocks;
     a.heads[0] = r.q_heads, a.heads[1] = r.k_heads;
     for (int i = 0; i < 2; ++i)
         if (a.heads[i] > 1) a.magic[i] = (uint32_t)(((uint64_t(1) << 32) + a.heads[i] - 1) / a.heads[i]);
-    a.dim = r.dim, a.half = r.rotary / 2, a.pairs = r.dim / 2, a.log_lanes = s.log_lanes, a.tokens = s.tokens;
+    a.dim = r.dim, a.half = r.rotary / 2, a.pairs = r.dim / 2, a.log_lanes = s.log_lanes;
     a.positions_wide = r.position_type == Q4NN_I64, a.gain_bf16 = r.gain_dtype == Q4MX_BF16;
     a.eps = r.eps, a.inv_dim = 1.0f / (float)r.dim;
     return a;
@@ -341,8 +401,10 @@ HeadsArgs args_of(const q4nn_rope& r, const Shape& s) {
 
 template <bool BACK> void launch_rows(const q4nn_rope& r, const Shape& s, const HeadsArgs& a, int64_t groups, hipStream_t st) {
     const dim3 g = grid_of(groups), b(256);
-#define Q4_HEADS(V, K) \
-    (r.interleaved ? k_heads<V, K, true, BACK><<<g, b, 0, st>>>(a) : k_heads<V, K, false, BACK><<<g, b, 0, st>>>(a))
+    const size_t lds = (size_t)(BACK ? 10 : 2) * a.dim * sizeof(float) + (size_t)a.tokens * a.pairs * sizeof(float2);
+#define Q4_HEADS(V, K)                                               \
+    (r.interleaved ? k_heads<V, K, true, BACK><<<g, b, lds, st>>>(a) \
+                   : k_heads<V, K, false, BACK><<<g, b, lds, st>>>(a))
     if (s.vec == 8) Q4_HEADS(8, 1);
     else if (s.vec == 4) Q4_HEADS(4, 1);
     else if (a.pairs <= 64) Q4_HEADS(1, 1);
@@ -350,39 +412,46 @@ template <bool BACK> void launch_rows(const q4nn_rope& r, const Shape& s, const 
 #undef Q4_HEADS
 }
 
-int64_t groups_of(const HeadsArgs& a) { return a.blocks < kMaxGroups ? a.blocks : kMaxGroups; }
-
 }  // namespace
 
+// The most work-groups that any strides lead to.
 size_t head_norm_rope_workspace(const q4nn_rope& r) {
-    return (size_t)groups_of(args_of(r, shape_of(r))) * 2 * r.dim * sizeof(float);
+    const int64_t total = r.batches * r.tokens;
+    return (size_t)(total < kMaxGroups ? total : kMaxGroups) * 2 * r.dim * sizeof(float);
 }
 
-hipError_t launch_head_norm_rope(const q4nn_rope& r, const q4nn_heads& q, const q4nn_heads& k, const q4nn_heads& qo,
+hipError_t launch_head_norm_rope(const q4nn_rope& rope, const q4nn_heads& q, const q4nn_heads& k, const q4nn_heads& qo,
                                  const q4nn_heads& ko, hipStream_t st) {
+    q4nn_heads v[4] = {q, k, qo, ko}, *const at[4] = {v, v + 1, v + 2, v + 3};
+    const q4nn_rope r = flat_batches(rope, at, 4);
     const Shape s = shape_of(r);
-    HeadsArgs a = args_of(r, s);
-    a.v[0] = q, a.v[1] = k, a.v[4] = qo, a.v[5] = ko;
+    HeadsArgs a = args_of(r, s, false);
+    a.v[0] = v[0], a.v[1] = v[1], a.v[4] = v[2], a.v[5] = v[3];
     launch_rows<false>(r, s, a, a.blocks, st);
     return hipGetLastError();
 }
 
-hipError_t launch_head_norm_rope_backward(const q4nn_rope& r, const q4nn_heads& q, const q4nn_heads& k,
+hipError_t launch_head_norm_rope_backward(const q4nn_rope& rope, const q4nn_heads& q, const q4nn_heads& k,
                                           const q4nn_heads& dq, const q4nn_heads& dk, const q4nn_heads& dq_in,
                                           const q4nn_heads& dk_in, void* gq, void* gk, int dtype, bool add, void* ws,
                                           hipStream_t st) {
-    const Shape s = shape_of(r);
-    HeadsArgs a = args_of(r, s);
-    a.v[0] = q, a.v[1] = k, a.v[2] = dq, a.v[3] = dk, a.v[4] = dq_in, a.v[5] = dk_in;
-    a.part = static_cast<float*>(ws);
-    const bool some = a.total > 0 && r.q_heads + r.k_heads > 0;
-    const int64_t groups = some ? groups_of(a) : 0;
-    if (some) launch_rows<true>(r, s, a, groups, st);
+    q4nn_heads v[6] = {q, k, dq, dk, dq_in, dk_in}, *const at[6] = {v, v + 1, v + 2, v + 3, v + 4, v + 5};
+    const q4nn_rope r = flat_batches(rope, at, 6);
+    int64_t groups = 0;
+    float* part = static_cast<float*>(ws);
+    if (r.batches * r.tokens > 0 && r.q_heads + r.k_heads > 0) {
+        const Shape s = shape_of(r);
+        HeadsArgs a = args_of(r, s, true);
+        for (int i = 0; i < 6; ++i) a.v[i] = v[i];
+        a.part = part;
+        groups = a.blocks < kMaxGroups ? a.blocks : kMaxGroups;
+        launch_rows<true>(r, s, a, groups, st);
+    }
     const dim3 g((unsigned)((2 * r.dim + 15) / 16)), b(1024);
-    if (dtype == Q4MX_BF16 && add) k_gain_grads<true, true><<<g, b, 0, st>>>(a.part, groups, r.dim, gq, gk);
-    else if (dtype == Q4MX_BF16) k_gain_grads<true, false><<<g, b, 0, st>>>(a.part, groups, r.dim, gq, gk);
-    else if (add) k_gain_grads<false, true><<<g, b, 0, st>>>(a.part, groups, r.dim, gq, gk);
-    else k_gain_grads<false, false><<<g, b, 0, st>>>(a.part, groups, r.dim, gq, gk);
+    if (dtype == Q4MX_BF16 && add) k_gain_grads<true, true><<<g, b, 0, st>>>(part, groups, r.dim, gq, gk);
+    else if (dtype == Q4MX_BF16) k_gain_grads<true, false><<<g, b, 0, st>>>(part, groups, r.dim, gq, gk);
+    else if (add) k_gain_grads<false, true><<<g, b, 0, st>>>(part, groups, r.dim, gq, gk);
+    else k_gain_grads<false, false><<<g, b, 0, st>>>(part, groups, r.dim, gq, gk);
     return hipGetLastError();
 }
 
