@@ -10,32 +10,37 @@
 // are interleaved), so the rotation needs no exchange.  Elements past `rotary`
 // pair up the same way, with the angle 0.
 //
-// The angles of a token are those of all its heads, and FP64: a work-group
-// forms the cosines and sines of its tokens once, in shared memory.  Its four
-// waves then walk the rows, q's first; the loads of a wave's next rows are on
-// their way while it computes, those of its first ones while the angles are
-// formed.
+// A work-group takes some tokens' rows of q, or of k.  The angles of a token
+// are those of all its rows, and FP64: a work-group forms the cosines and sines
+// of its tokens once, in shared memory, while its first rows are being loaded.
+// Arithmetic is not far behind memory (an instruction is 4 cycles of a wave), so
+// a lane steps from row to row by additions, and rows whose lanes are no power
+// of two (5 for a head of 80) are packed without idle lanes.
 #include "q4_mx_dev.h"
 #include "q4_nn.h"
 
 namespace q4 {
 namespace {
 
-constexpr int kTokens = 32, kAngles = 2048;  // most tokens and angles of a work-group
-constexpr int kMaxGroups = 1024;             // of a backward pass: each leaves one sum of the gains' gradients
+constexpr int kTokens = 64, kAngles = 2048;  // most tokens and angles of a work-group
+constexpr int kGroups = 1000;                // of a backward pass the chip holds at once: 4 to a compute unit, a few to spare
 
+// One of q and k.
+struct Tensor {
+    q4nn_heads in, grad, out;  // grad: backward only
+    const void* gain;
+    int64_t batch_groups, groups;  // work-groups of a batch, and all
+    int heads, tokens;             // tokens: of a work-group
+    float* part;                   // [groups][dim]: sums of the gain's gradient
+};
 struct HeadsArgs {
-    q4nn_heads v[6];  // q, k, dq, dk, q_out, k_out (backward: dq_in, dk_in)
-    const void *positions, *gain[2];
+    Tensor t[2];
+    const void* positions;
     const double* frequencies;
-    int64_t position_batch, position_token;
-    int64_t per_batch, batch_blocks, blocks;  // tokens and work-groups' parts of a batch, and all parts
-    int heads[2];
-    uint32_t magic[2];  // ceil(2^32 / heads)
-    int dim, half, pairs, log_lanes, tokens;
+    int64_t position_batch, position_token, per_batch;  // per_batch: tokens
+    int dim, half, pairs, lanes, log_pairs;  // lanes: of a row; 2^log_pairs >= pairs, or 256
     bool positions_wide, gain_bf16;
     float eps, inv_dim;
-    float* part;  // [work-groups][2][dim]
 };
 
 // Cosine and sine of `a` radians.  FP64 brings the angle to a quarter turn and
@@ -61,18 +66,36 @@ __device__ __forceinline__ float2 cos_sin(double a) {
     return make_float2((n == 1 || n == 2) ? -cc : cc, n >= 2 ? -ss : ss);
 }
 
-// Sum over the 2^log_lanes neighbouring lanes of a row.
-__device__ __forceinline__ float row_sum(float x, int log_lanes) {
+// Sum over the neighbouring lanes of a row, of which lane `first` is the
+// first: the same in each of them.
+__device__ __forceinline__ float row_sum(float x, int lanes, int first) {
+    if ((lanes & (lanes - 1)) != 0) {
+        float sum = 0.0f;
+        for (int k = 0; k < lanes; ++k)
+            sum += __int_as_float(__builtin_amdgcn_ds_bpermute((first + k) * 4, __float_as_int(x)));
+        return sum;
+    }
 #define Q4_ADD_DPP(ctrl) \
     x += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), ctrl, 0xF, 0xF, true))
-    if (log_lanes > 0) Q4_ADD_DPP(0xB1);   // lanes 1 0 3 2
-    if (log_lanes > 1) Q4_ADD_DPP(0x4E);   // lanes 2 3 0 1
-    if (log_lanes > 2) Q4_ADD_DPP(0x141);  // the other quad of 8
-    if (log_lanes > 3) Q4_ADD_DPP(0x140);  // the other 8 of 16
+    if (lanes > 1) Q4_ADD_DPP(0xB1);   // lanes 1 0 3 2
+    if (lanes > 2) Q4_ADD_DPP(0x4E);   // lanes 2 3 0 1
+    if (lanes > 4) Q4_ADD_DPP(0x141);  // the other quad of 8
+    if (lanes > 8) Q4_ADD_DPP(0x140);  // the other 8 of 16
 #undef Q4_ADD_DPP
-    if (log_lanes > 4) x += __shfl_xor(x, 16);
-    if (log_lanes > 5) x += __shfl_xor(x, 32);
+    if (lanes > 16) x += __shfl_xor(x, 16);
+    if (lanes > 32) x += __shfl_xor(x, 32);
     return x;
+}
+
+// Two FP32 as BF16 in a word, to nearest even.
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    union {
+        bf16x2 b;
+        uint32_t u;
+    } t;
+    t.b = __builtin_convertvector((f32x2{lo, hi}), bf16x2);
+    return t.u;
 }
 
 // Where a lane's VEC pairs from pair u on lie: two vectors at e[0] and e[1].
@@ -136,9 +159,9 @@ template <int VEC, bool INTER> __device__ __forceinline__ Words<VEC> join_pairs(
     Words<VEC> r;
 #pragma unroll
     for (int k = 0; k < VEC; ++k) {
-        if (INTER || VEC == 1) r.w[k] = bf16_pair(p[k], s[k]);
-        else if (k < VEC / 2) r.w[k] = bf16_pair(p[2 * k], p[(2 * k + 1) % VEC]);
-        else r.w[k] = bf16_pair(s[2 * k - VEC], s[(2 * k + 1) % VEC]);
+        if (INTER || VEC == 1) r.w[k] = pack2(p[k], s[k]);
+        else if (k < VEC / 2) r.w[k] = pack2(p[2 * k], p[(2 * k + 1) % VEC]);
+        else r.w[k] = pack2(s[2 * k - VEC], s[(2 * k + 1) % VEC]);
     }
     return r;
 }
@@ -146,199 +169,211 @@ template <int VEC, bool INTER> __device__ __forceinline__ Words<VEC> join_pairs(
 // K vectors of pairs to a lane (one, but for heads of odd sizes above 128).
 template <int VEC, int K, bool INTER, bool BACK>
 __global__ __launch_bounds__(256, K == 1 ? 4 : 1) void k_heads(HeadsArgs a) {
+    // angles [tokens][K][VEC][lanes] (of pair (c lanes + sub) VEC + k: lanes read neighbours); backward, after
+    // that: sums of the gain's gradient [4 waves][dim]
     extern __shared__ float4 shared[];
-    // gains [2][dim], backward: sums [4 waves][2][dim]; angles
-    float* gains = reinterpret_cast<float*>(shared);
-    float* sums = gains + 2 * a.dim;
-    float2* angles = reinterpret_cast<float2*>(sums + (BACK ? 8 * a.dim : 0));
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lanes = 1 << a.log_lanes;
-    const int sub = lane & (lanes - 1), mine = lane >> a.log_lanes, per_wave = 64 >> a.log_lanes;
-    for (int i = threadIdx.x; i < 2 * a.dim; i += 256) {
-        const int w = i >= a.dim, at = i - (w ? a.dim : 0);
-        gains[i] = a.heads[w] == 0 ? 0.0f : a.gain_bf16 ? load1<true>(a.gain[w], at) : load1<false>(a.gain[w], at);
-    }
-    if (BACK)
-        for (int i = threadIdx.x; i < 8 * a.dim; i += 256) sums[i] = 0.0f;
+    float2* const angles = reinterpret_cast<float2*>(shared);
+    int64_t group = group_index();
+    const bool second = group >= a.t[0].groups;
+    const Tensor& w = a.t[second];
+    if (second) group -= a.t[0].groups;
+    if (group >= w.groups) return;
+    const int64_t b = group / w.batch_groups, t0 = (group - b * w.batch_groups) * w.tokens;
+    const int tokens = (int)(a.per_batch - t0 < w.tokens ? a.per_batch - t0 : w.tokens);
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int per_wave = 64 / a.lanes, mine = lane / a.lanes, sub = lane - mine * a.lanes, stride = 4 * per_wave;
+    const int token_size = K * VEC * a.lanes, rows = tokens * w.heads;
 
-    for (int64_t block = group_index(); block < a.blocks; block += (int64_t)gridDim.x * gridDim.y) {
-        const int64_t b = block / a.batch_blocks, t0 = (block - b * a.batch_blocks) * a.tokens;
-        const int tokens = (int)(a.per_batch - t0 < a.tokens ? a.per_batch - t0 : a.tokens);
-        const int rows_q = tokens * a.heads[0], rows_k = tokens * a.heads[1];
-        const int steps_q = (rows_q + 4 * per_wave - 1) / (4 * per_wave);
-        const int steps = steps_q + (rows_k + 4 * per_wave - 1) / (4 * per_wave);
-        // Step i of a wave: its rows' tensor, and this lane's row.  q's rows go to the first waves first, k's to the last.
-        const auto row_of = [&](int i) {
-            return i < steps_q ? (i * 4 + wave) * per_wave + mine : ((i - steps_q) * 4 + 3 - wave) * per_wave + mine;
-        };
-        // r / heads: the reciprocal is less than heads 2^-32 of itself too large, and r < 32 * 4096 + 256, heads <= 4096
-        const auto token_of = [&](int r, int w) {
-            return a.heads[w] == 1 ? r : (int)__umulhi((uint32_t)r, a.magic[w]);
-        };
-        const auto place_of = [&](const q4nn_heads& v, int tok, int head) {
-            return v.p + (b * v.batch + t0 * v.token) + (tok * v.token + head * v.head);
-        };
-        struct Loaded {
-            Words<VEC> x[K], dy[BACK ? K : 1];
-        };
-        const auto load_step = [&](int i) {
-            Loaded l = {};
-            const int w = i < steps_q ? 0 : 1, r = row_of(i);
-            if (r < (w ? rows_k : rows_q)) {
-                const int tok = token_of(r, w), head = r - tok * a.heads[w];
-                const uint16_t* x = place_of(a.v[w], tok, head);
-                const uint16_t* dy = BACK ? place_of(a.v[2 + w], tok, head) : nullptr;
+    // A lane's rows are `stride` apart: that many heads on, or a token and some less.
+    int row = mine < per_wave ? wave * per_wave + mine : rows;
+    const int step_tokens = stride / w.heads, step_heads = stride - step_tokens * w.heads;
+    const int start = row < rows ? row : 0;  // a lane without a row computes on the first, and stores nothing
+    int tok = start / w.heads, head = start - tok * w.heads;
+    const auto first_of = [&](const q4nn_heads& v) { return v.p + (b * v.batch + (t0 + tok) * v.token + head * v.head); };
+    const uint16_t *x_at = first_of(w.in), *dy_at = BACK ? first_of(w.grad) : nullptr;
+    uint16_t* y_at = first_of(w.out);
+    const auto step_of = [&](const q4nn_heads& v) { return step_tokens * v.token + step_heads * v.head; };
+    const auto wrap_of = [&](const q4nn_heads& v) { return v.token - w.heads * v.head; };
+    const int64_t x_step = step_of(w.in), y_step = step_of(w.out), dy_step = BACK ? step_of(w.grad) : 0;
+    const int64_t x_past = x_step + wrap_of(w.in), y_past = y_step + wrap_of(w.out);
+    const int64_t dy_past = BACK ? dy_step + wrap_of(w.grad) : 0;
+
+    Words<VEC> x[K] = {}, dy[K] = {};  // zeros stay where a lane's pairs are past the row's
+    const auto load = [&] {
 #pragma unroll
-                for (int c = 0; c < K; ++c) {
-                    const int u = (c * lanes + sub) * VEC;
-                    if (u >= a.pairs) continue;
-                    const Place<VEC, INTER> e(a, u);
-                    l.x[c] = load_words<VEC>(x, e.e);
-                    if (BACK) l.dy[c] = load_words<VEC>(dy, e.e);
+        for (int c = 0; c < K; ++c) {
+            const int u = (c * a.lanes + sub) * VEC;
+            if (u >= a.pairs) continue;
+            const Place<VEC, INTER> e(a, u);
+            x[c] = load_words<VEC>(x_at, e.e);
+            if (BACK) dy[c] = load_words<VEC>(dy_at, e.e);
+        }
+    };
+    load();
+    float gp[K][VEC], gs[K][VEC];
+#pragma unroll
+    for (int c = 0; c < K; ++c) {
+        const int u = (c * a.lanes + sub) * VEC;
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) gp[c][k] = gs[c][k] = 0.0f;
+        if (u >= a.pairs) continue;
+        const Place<VEC, INTER> e(a, u);
+        if (a.gain_bf16) {
+            split_pairs<VEC, INTER>(load_words<VEC>(static_cast<const uint16_t*>(w.gain), e.e), gp[c], gs[c]);
+        } else {
+            const float* g = static_cast<const float*>(w.gain);
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) {
+                gp[c][k] = INTER ? (2 * k < VEC ? g[e.e[0] + 2 * k] : g[e.e[1] + 2 * k - VEC]) : g[e.e[0] + k];
+                gs[c][k] = INTER ? (2 * k + 1 < VEC ? g[e.e[0] + 2 * k + 1] : g[e.e[1] + 2 * k + 1 - VEC]) : g[e.e[1] + k];
+            }
+        }
+    }
+    // a thread forms the angles of one pair (or every 256th) for every so many tokens
+    for (int u = threadIdx.x & ((1 << a.log_pairs) - 1); u < K * VEC * a.lanes; u += 256) {
+        const int cl = u / VEC, c = K == 1 ? 0 : cl / a.lanes;
+        const int at = (c * VEC + u % VEC) * a.lanes + cl - c * a.lanes;
+        const double frequency = u < a.half ? a.frequencies[u] : 0.0;
+        for (int t = threadIdx.x >> a.log_pairs; t < tokens; t += 256 >> a.log_pairs) {
+            const int64_t p = b * a.position_batch + (t0 + t) * a.position_token;
+            const double position = a.positions_wide ? (double)static_cast<const int64_t*>(a.positions)[p]
+                                                     : (double)static_cast<const int32_t*>(a.positions)[p];
+            angles[t * token_size + at] = u < a.half ? cos_sin(position * frequency) : make_float2(1.0f, 0.0f);
+        }
+    }
+    __syncthreads();
+
+    float acc[K][2 * VEC];  // of the gain's gradient: pairs' first elements and second
+#pragma unroll
+    for (int c = 0; c < K; ++c)
+#pragma unroll
+        for (int k = 0; k < 2 * VEC; ++k) acc[c][k] = 0.0f;
+    const float2* turns = angles + tok * token_size + sub;
+    while (row < rows) {
+        float xp[K][VEC], xs[K][VEC], dp[K][VEC], ds[K][VEC], sum = 0.0f;
+#pragma unroll
+        for (int c = 0; c < K; ++c) {
+            split_pairs<VEC, INTER>(x[c], xp[c], xs[c]);
+            if (BACK) split_pairs<VEC, INTER>(dy[c], dp[c], ds[c]);
+#pragma unroll
+            for (int k = 0; k < VEC; ++k)
+                sum = __builtin_fmaf(xp[c][k], xp[c][k], __builtin_fmaf(xs[c][k], xs[c][k], sum));
+        }
+        const float inv =
+            __builtin_amdgcn_rsqf(__builtin_fmaf(row_sum(sum, a.lanes, lane - sub), a.inv_dim, a.eps));
+        float along = 0.0f;
+#pragma unroll
+        for (int c = 0; c < K; ++c) {
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) {
+                const float2 t = turns[(c * VEC + k) * a.lanes];
+                xp[c][k] *= inv, xs[c][k] *= inv;  // n
+                if (!BACK) {
+                    const float yp = xp[c][k] * gp[c][k], ys = xs[c][k] * gs[c][k];
+                    xp[c][k] = __builtin_fmaf(yp, t.x, -(ys * t.y));
+                    xs[c][k] = __builtin_fmaf(ys, t.x, yp * t.y);
+                } else {
+                    const float up = __builtin_fmaf(dp[c][k], t.x, ds[c][k] * t.y);  // turned back
+                    const float us = __builtin_fmaf(ds[c][k], t.x, -(dp[c][k] * t.y));
+                    acc[c][k] = __builtin_fmaf(up, xp[c][k], acc[c][k]);
+                    acc[c][VEC + k] = __builtin_fmaf(us, xs[c][k], acc[c][VEC + k]);
+                    dp[c][k] = up * gp[c][k], ds[c][k] = us * gs[c][k];
+                    along = __builtin_fmaf(dp[c][k], xp[c][k], __builtin_fmaf(ds[c][k], xs[c][k], along));
                 }
             }
-            return l;
-        };
-        Loaded now = load_step(0);
-        __syncthreads();  // the block before is done with the angles
-        for (int i = threadIdx.x; i < tokens * a.pairs; i += 256) {
-            const int tok = i / a.pairs, u = i - tok * a.pairs;
-            float2 w = make_float2(1.0f, 0.0f);
-            if (u < a.half) {
-                const int64_t at = b * a.position_batch + (t0 + tok) * a.position_token;
-                const double position = a.positions_wide ? (double)static_cast<const int64_t*>(a.positions)[at]
-                                                         : (double)static_cast<const int32_t*>(a.positions)[at];
-                w = cos_sin(position * a.frequencies[u]);
-            }
-            angles[i] = w;
         }
-        __syncthreads();
-        float acc[K][2 * VEC];  // of the gain's gradient: pairs' first elements and second
+        if (BACK) {
+            const float mean = row_sum(along, a.lanes, lane - sub) * a.inv_dim;
+#pragma unroll
+            for (int c = 0; c < K; ++c)
+#pragma unroll
+                for (int k = 0; k < VEC; ++k) {
+                    xp[c][k] = inv * __builtin_fmaf(-xp[c][k], mean, dp[c][k]);
+                    xs[c][k] = inv * __builtin_fmaf(-xs[c][k], mean, ds[c][k]);
+                }
+        }
+        uint16_t* const y = y_at;
+        // the next row
+        row += stride, head += step_heads;
+        const bool past = head >= w.heads;
+        head -= past ? w.heads : 0;
+        turns += (step_tokens + (past ? 1 : 0)) * token_size;
+        x_at += past ? x_past : x_step, y_at += past ? y_past : y_step;
+        if (BACK) dy_at += past ? dy_past : dy_step;
+        if (row < rows) load();
+#pragma unroll
+        for (int c = 0; c < K; ++c) {
+            const int u = (c * a.lanes + sub) * VEC;
+            if (u >= a.pairs) continue;
+            store_words<VEC>(y, Place<VEC, INTER>(a, u).e, join_pairs<VEC, INTER>(xp[c], xs[c]));
+        }
+    }
+    if (!BACK) return;
+
+    // the sums over a wave's rows, then over the waves
+    float* const sums = reinterpret_cast<float*>(angles + w.tokens * token_size);
+    if ((a.lanes & (a.lanes - 1)) == 0) {
+        for (int m = a.lanes; m < 64; m *= 2)
+#pragma unroll
+            for (int c = 0; c < K; ++c)
+#pragma unroll
+                for (int k = 0; k < 2 * VEC; ++k) acc[c][k] += __shfl_xor(acc[c][k], m);
+    } else {
+        float own[K][2 * VEC];
 #pragma unroll
         for (int c = 0; c < K; ++c)
 #pragma unroll
-            for (int k = 0; k < 2 * VEC; ++k) acc[c][k] = 0.0f;
-        for (int i = 0; i < steps; ++i) {
-            const int w = i < steps_q ? 0 : 1, r = row_of(i);
-            Loaded next;
-            if (i + 1 < steps) next = load_step(i + 1);
-            if (r < (w ? rows_k : rows_q)) {
-                const int tok = token_of(r, w), head = r - tok * a.heads[w];
-                float xp[K][VEC], xs[K][VEC], dp[K][VEC], ds[K][VEC], sum = 0.0f;
+            for (int k = 0; k < 2 * VEC; ++k) own[c][k] = acc[c][k];
+        for (int m = 1; m < per_wave; ++m)
 #pragma unroll
-                for (int c = 0; c < K; ++c) {
-                    split_pairs<VEC, INTER>(now.x[c], xp[c], xs[c]);  // zeros past the row
-                    if (BACK) split_pairs<VEC, INTER>(now.dy[c], dp[c], ds[c]);
+            for (int c = 0; c < K; ++c)
 #pragma unroll
-                    for (int k = 0; k < VEC; ++k)
-                        sum = __builtin_fmaf(xp[c][k], xp[c][k], __builtin_fmaf(xs[c][k], xs[c][k], sum));
-                }
-                const float inv =
-                    __builtin_amdgcn_rsqf(__builtin_fmaf(row_sum(sum, a.log_lanes), a.inv_dim, a.eps));
-                uint16_t* y = place_of(a.v[4 + w], tok, head);
-                float along = 0.0f;
-#pragma unroll
-                for (int c = 0; c < K; ++c) {
-                    const int u = (c * lanes + sub) * VEC;
-                    if (u >= a.pairs) continue;
-                    const Place<VEC, INTER> e(a, u);
-                    const float2* turn = angles + tok * a.pairs + u;
-                    const float *g0 = gains + w * a.dim + e.e[0], *g1 = gains + w * a.dim + e.e[1];
-                    float p[VEC], s[VEC];
-#pragma unroll
-                    for (int k = 0; k < VEC; ++k) {
-                        const float2 t = turn[k];
-                        const float gp = INTER && VEC > 1 ? (2 * k < VEC ? g0[2 * k] : g1[2 * k - VEC]) : g0[k];
-                        const float gs = INTER && VEC > 1 ? (2 * k < VEC ? g0[2 * k + 1] : g1[2 * k + 1 - VEC]) : g1[k];
-                        xp[c][k] *= inv, xs[c][k] *= inv;  // n
-                        if (!BACK) {
-                            const float yp = xp[c][k] * gp, ys = xs[c][k] * gs;
-                            p[k] = __builtin_fmaf(yp, t.x, -(ys * t.y));
-                            s[k] = __builtin_fmaf(ys, t.x, yp * t.y);
-                        } else {
-                            const float up = __builtin_fmaf(dp[c][k], t.x, ds[c][k] * t.y);  // turned back
-                            const float us = __builtin_fmaf(ds[c][k], t.x, -(dp[c][k] * t.y));
-                            acc[c][k] = __builtin_fmaf(up, xp[c][k], acc[c][k]);
-                            acc[c][VEC + k] = __builtin_fmaf(us, xs[c][k], acc[c][VEC + k]);
-                            dp[c][k] = up * gp, ds[c][k] = us * gs;
-                            along = __builtin_fmaf(dp[c][k], xp[c][k], __builtin_fmaf(ds[c][k], xs[c][k], along));
-                        }
-                    }
-                    if (!BACK) store_words<VEC>(y, e.e, join_pairs<VEC, INTER>(p, s));
-                }
-                if (BACK) {
-                    const float mean = row_sum(along, a.log_lanes) * a.inv_dim;
-#pragma unroll
-                    for (int c = 0; c < K; ++c) {
-                        const int u = (c * lanes + sub) * VEC;
-                        if (u >= a.pairs) continue;
-                        float p[VEC], s[VEC];
-#pragma unroll
-                        for (int k = 0; k < VEC; ++k) {
-                            p[k] = inv * __builtin_fmaf(-xp[c][k], mean, dp[c][k]);
-                            s[k] = inv * __builtin_fmaf(-xs[c][k], mean, ds[c][k]);
-                        }
-                        store_words<VEC>(y, Place<VEC, INTER>(a, u).e, join_pairs<VEC, INTER>(p, s));
-                    }
-                }
-            }
-            if (BACK && (i + 1 == steps_q || i + 1 == steps)) {
-                // all of a tensor's rows: the sums over the wave's rows, added to the wave's own
-#pragma unroll
-                for (int c = 0; c < K; ++c) {
-                    const int u = (c * lanes + sub) * VEC;
-#pragma unroll
-                    for (int k = 0; k < 2 * VEC; ++k)
-                        for (int m = lanes; m < 64; m *= 2) acc[c][k] += __shfl_xor(acc[c][k], m);
-                    if (u < a.pairs && lane < lanes) {
-                        const Place<VEC, INTER> e(a, u);
-                        float *p0 = sums + (wave * 2 + w) * a.dim + e.e[0], *p1 = sums + (wave * 2 + w) * a.dim + e.e[1];
-#pragma unroll
-                        for (int k = 0; k < VEC; ++k) {
-                            // INTER: elements 2k and 2k + 1 of the two vectors
-                            if (INTER && VEC > 1) {
-                                (2 * k < VEC ? p0[2 * k] : p1[2 * k - VEC]) += acc[c][k];
-                                (2 * k < VEC ? p0[2 * k + 1] : p1[2 * k + 1 - VEC]) += acc[c][VEC + k];
-                            } else {
-                                p0[k] += acc[c][k], p1[k] += acc[c][VEC + k];
-                            }
-                        }
-                    }
-#pragma unroll
-                    for (int k = 0; k < 2 * VEC; ++k) acc[c][k] = 0.0f;
-                }
-            }
-            now = next;
-        }
-        if (!BACK) return;
+                for (int k = 0; k < 2 * VEC; ++k)
+                    acc[c][k] += __int_as_float(
+                        __builtin_amdgcn_ds_bpermute((sub + m * a.lanes) * 4, __float_as_int(own[c][k])));
     }
-    if (!BACK) return;
+#pragma unroll
+    for (int c = 0; c < K; ++c) {
+        const int u = (c * a.lanes + sub) * VEC;
+        if (u >= a.pairs || lane >= a.lanes) continue;
+        const Place<VEC, INTER> e(a, u);
+#pragma unroll
+        for (int k = 0; k < 2 * VEC; ++k) {
+            const int p = k < VEC ? k : k - VEC;  // pair u + p
+            sums[wave * a.dim + (INTER ? 2 * (u + p) + (k >= VEC) : e.e[k >= VEC] + p)] = acc[c][k];
+        }
+    }
     __syncthreads();
-    float* part = a.part + (int64_t)group_index() * 2 * a.dim;
-    for (int i = threadIdx.x; i < 2 * a.dim; i += 256)
-        part[i] = (sums[i] + sums[2 * a.dim + i]) + (sums[4 * a.dim + i] + sums[6 * a.dim + i]);
+    for (int i = threadIdx.x; i < a.dim; i += 256)
+        w.part[group * a.dim + i] = (sums[i] + sums[a.dim + i]) + (sums[2 * a.dim + i] + sums[3 * a.dim + i]);
 }
 
-// The gains' gradients from the work-groups' sums: 16 of the 2 dim columns to a
+// The gains' gradients from the work-groups' sums: 16 columns of q's or k's to a
 // work-group, a 64th of the sums to a thread.
-template <bool BF16, bool ADD>
-__global__ __launch_bounds__(1024) void k_gain_grads(const float* part, int64_t groups, int dim, void* gq, void* gk) {
+struct GainSums {
+    const float* part[2];
+    int64_t groups[2];
+    void* grad[2];
+};
+template <bool BF16, bool ADD> __global__ __launch_bounds__(1024) void k_gain_grads(GainSums a, int dim) {
     __shared__ float lds[64][17];
-    const int i = blockIdx.x * 16 + (threadIdx.x & 15), slice = threadIdx.x >> 4;
+    const int blocks = (dim + 15) / 16, w = (int)blockIdx.x >= blocks;
+    const int col = threadIdx.x & 15, i = ((int)blockIdx.x - w * blocks) * 16 + col, slice = threadIdx.x >> 4;
     float sum = 0.0f;
-    if (i < 2 * dim)
-        for (int64_t g = slice; g < groups; g += 64) sum += part[g * 2 * dim + i];
-    lds[slice][threadIdx.x & 15] = sum;
+    if (i < dim) {
+#pragma unroll 8
+        for (int64_t g = slice; g < a.groups[w]; g += 64) sum += a.part[w][g * dim + i];
+    }
+    lds[slice][col] = sum;
     for (int s = 32; s > 0; s /= 2) {
         __syncthreads();
-        if (slice < s) lds[slice][threadIdx.x & 15] += lds[slice + s][threadIdx.x & 15];
+        if (slice < s) lds[slice][col] += lds[slice + s][col];
     }
-    if (slice != 0 || i >= 2 * dim) return;
-    sum = lds[0][threadIdx.x];
-    void* p = i < dim ? gq : gk;
-    const int at = i < dim ? i : i - dim;
-    if (ADD) sum += load1<BF16>(p, at);
-    if (BF16) static_cast<uint16_t*>(p)[at] = bf16_bits(sum);
-    else static_cast<float*>(p)[at] = sum;
+    if (slice != 0 || i >= dim) return;
+    sum = lds[0][col];
+    if (ADD) sum += load1<BF16>(a.grad[w], i);
+    if (BF16) static_cast<uint16_t*>(a.grad[w])[i] = bf16_bits(sum);
+    else static_cast<float*>(a.grad[w])[i] = sum;
 }
 
 // The call with its tokens in as few batches as their strides allow: one where
@@ -357,51 +392,63 @@ q4nn_rope flat_batches(const q4nn_rope& r, q4nn_heads* const* v, int n) {
 }
 
 // Pairs to a lane and lanes to a row: 8 (or 4) pairs where both the rotary
-// part and the rest are made of whole vectors, else single ones.
+// part and the rest are made of whole vectors, else single ones.  Rows of up to
+// 16 lanes lie side by side as they are where a wave takes more of them so
+// (heads of 80: 12 in place of 8; PLACEHOLDER), else padded to a power of two.
 struct Shape {
-    int vec, log_lanes;
+    int vec, lanes;
 };
 Shape shape_of(const q4nn_rope& r) {
     const int pairs = r.dim / 2, half = r.rotary / 2;
-    Shape s = {1, 0};
+    Shape s = {1, 1};
     for (int v : {8, 4})
         if (s.vec == 1 && pairs % v == 0 && (r.interleaved || half % v == 0) && pairs <= 64 * v) s.vec = v;
-    while ((1 << s.log_lanes) * s.vec < pairs && s.log_lanes < 6) ++s.log_lanes;
+    while (s.lanes * s.vec < pairs && s.lanes < 64) s.lanes *= 2;
+    const int tight = pairs / s.vec;
+    if (tight <= 16 && 64 / tight > 64 / s.lanes) s.lanes = tight;
     return s;
 }
 
-// Tokens to a work-group's part.  Forward: until its four waves are full of
-// rows of q and of k, while many work-groups are left.  Backward: as many as
-// leave the parts that the chip holds at once.
-int tokens_of(const q4nn_rope& r, const Shape& s, bool back) {
-    const int rows = 4 * (64 >> s.log_lanes), pairs = r.dim / 2;
-    int heads = r.q_heads < r.k_heads ? r.q_heads : r.k_heads, tokens = 1;
-    if (heads == 0) heads = r.q_heads + r.k_heads;
-    while (2 * tokens <= kTokens && 2 * tokens * pairs <= kAngles &&
-           (back ? r.batches * ((r.tokens + tokens - 1) / tokens) > kMaxGroups
-                 : tokens * heads < rows && r.batches * (r.tokens / (2 * tokens)) >= 1024))
-        tokens *= 2;
-    return tokens;
+// Angles of a token in shared memory: a lane's whole vectors of them.
+int angles_of(const q4nn_rope& r, const Shape& s) { return s.vec * s.lanes * (s.vec == 1 && r.dim > 128 ? 8 : 1); }
+
+// Tokens to a work-group, `heads` rows each: forward two steps of its waves,
+// while there are work-groups for all compute units; backward as many rows as
+// leave the work-groups that the chip holds at once, since each ends in a sum
+// over its waves.
+int tokens_of(const q4nn_rope& r, const Shape& s, int heads, bool back) {
+    const int64_t step = 4 * (64 / s.lanes), rows = r.batches * r.tokens * (r.q_heads + r.k_heads);
+    int64_t tokens = 1;
+    if (heads > 0 && back) tokens = (rows / kGroups + heads) / heads;
+    else if (heads > 0) tokens = (rows / kGroups < step ? rows / kGroups : rows / kGroups < 2 * step ? step : 2 * step) / heads;
+    if (tokens > kTokens) tokens = kTokens;
+    if (tokens > kAngles / angles_of(r, s)) tokens = kAngles / angles_of(r, s);
+    return tokens < 1 ? 1 : (int)tokens;
 }
 
 HeadsArgs args_of(const q4nn_rope& r, const Shape& s, bool back) {
     HeadsArgs a = {};
-    a.positions = r.positions, a.gain[0] = r.q_gain, a.gain[1] = r.k_gain, a.frequencies = r.frequencies;
+    a.positions = r.positions, a.frequencies = r.frequencies;
     a.position_batch = r.position_batch, a.position_token = r.position_token;
-    a.tokens = tokens_of(r, s, back);
-    a.per_batch = r.tokens, a.batch_blocks = (r.tokens + a.tokens - 1) / a.tokens, a.blocks = r.batches * a.batch_blocks;
-    a.heads[0] = r.q_heads, a.heads[1] = r.k_heads;
-    for (int i = 0; i < 2; ++i)
-        if (a.heads[i] > 1) a.magic[i] = (uint32_t)(((uint64_t(1) << 32) + a.heads[i] - 1) / a.heads[i]);
-    a.dim = r.dim, a.half = r.rotary / 2, a.pairs = r.dim / 2, a.log_lanes = s.log_lanes;
+    a.per_batch = r.tokens;
+    for (int i = 0; i < 2; ++i) {
+        Tensor& t = a.t[i];
+        t.heads = i ? r.k_heads : r.q_heads, t.gain = i ? r.k_gain : r.q_gain;
+        t.tokens = tokens_of(r, s, t.heads, back);
+        t.batch_groups = (r.tokens + t.tokens - 1) / t.tokens;
+        t.groups = t.heads > 0 ? r.batches * t.batch_groups : 0;
+    }
+    a.dim = r.dim, a.half = r.rotary / 2, a.pairs = r.dim / 2, a.lanes = s.lanes;
+    while (a.log_pairs < 8 && (1 << a.log_pairs) < angles_of(r, s)) ++a.log_pairs;
     a.positions_wide = r.position_type == Q4NN_I64, a.gain_bf16 = r.gain_dtype == Q4MX_BF16;
     a.eps = r.eps, a.inv_dim = 1.0f / (float)r.dim;
     return a;
 }
 
-template <bool BACK> void launch_rows(const q4nn_rope& r, const Shape& s, const HeadsArgs& a, int64_t groups, hipStream_t st) {
-    const dim3 g = grid_of(groups), b(256);
-    const size_t lds = (size_t)(BACK ? 10 : 2) * a.dim * sizeof(float) + (size_t)a.tokens * a.pairs * sizeof(float2);
+template <bool BACK> void launch_rows(const q4nn_rope& r, const Shape& s, const HeadsArgs& a, hipStream_t st) {
+    const dim3 g = grid_of(a.t[0].groups + a.t[1].groups), b(256);
+    const int tokens = a.t[0].tokens > a.t[1].tokens ? a.t[0].tokens : a.t[1].tokens;
+    const size_t lds = (BACK ? 4 * sizeof(float) * a.dim : 0) + sizeof(float2) * tokens * angles_of(r, s);
 #define Q4_HEADS(V, K)                                               \
     (r.interleaved ? k_heads<V, K, true, BACK><<<g, b, lds, st>>>(a) \
                    : k_heads<V, K, false, BACK><<<g, b, lds, st>>>(a))
@@ -416,8 +463,13 @@ template <bool BACK> void launch_rows(const q4nn_rope& r, const Shape& s, const 
 
 // The most work-groups that any strides lead to.
 size_t head_norm_rope_workspace(const q4nn_rope& r) {
-    const int64_t total = r.batches * r.tokens;
-    return (size_t)(total < kMaxGroups ? total : kMaxGroups) * 2 * r.dim * sizeof(float);
+    const Shape s = shape_of(r);
+    q4nn_rope flat = r;
+    flat.tokens = r.batches * r.tokens, flat.batches = 1;
+    const HeadsArgs a = args_of(r, s, true), f = args_of(flat, s, true);
+    const int64_t q = a.t[0].groups > f.t[0].groups ? a.t[0].groups : f.t[0].groups;
+    const int64_t k = a.t[1].groups > f.t[1].groups ? a.t[1].groups : f.t[1].groups;
+    return (size_t)(q + k) * r.dim * sizeof(float);
 }
 
 hipError_t launch_head_norm_rope(const q4nn_rope& rope, const q4nn_heads& q, const q4nn_heads& k, const q4nn_heads& qo,
@@ -426,8 +478,8 @@ hipError_t launch_head_norm_rope(const q4nn_rope& rope, const q4nn_heads& q, con
     const q4nn_rope r = flat_batches(rope, at, 4);
     const Shape s = shape_of(r);
     HeadsArgs a = args_of(r, s, false);
-    a.v[0] = v[0], a.v[1] = v[1], a.v[4] = v[2], a.v[5] = v[3];
-    launch_rows<false>(r, s, a, a.blocks, st);
+    for (int i = 0; i < 2; ++i) a.t[i].in = v[i], a.t[i].out = v[2 + i];
+    launch_rows<false>(r, s, a, st);
     return hipGetLastError();
 }
 
@@ -437,21 +489,25 @@ hipError_t launch_head_norm_rope_backward(const q4nn_rope& rope, const q4nn_head
                                           hipStream_t st) {
     q4nn_heads v[6] = {q, k, dq, dk, dq_in, dk_in}, *const at[6] = {v, v + 1, v + 2, v + 3, v + 4, v + 5};
     const q4nn_rope r = flat_batches(rope, at, 6);
-    int64_t groups = 0;
-    float* part = static_cast<float*>(ws);
+    GainSums g = {};
+    g.grad[0] = gq, g.grad[1] = gk;
     if (r.batches * r.tokens > 0 && r.q_heads + r.k_heads > 0) {
         const Shape s = shape_of(r);
         HeadsArgs a = args_of(r, s, true);
-        for (int i = 0; i < 6; ++i) a.v[i] = v[i];
-        a.part = part;
-        groups = a.blocks < kMaxGroups ? a.blocks : kMaxGroups;
-        launch_rows<true>(r, s, a, groups, st);
+        float* part = static_cast<float*>(ws);
+        for (int i = 0; i < 2; ++i) {
+            Tensor& t = a.t[i];
+            t.in = v[i], t.grad = v[2 + i], t.out = v[4 + i], t.part = part;
+            g.part[i] = part, g.groups[i] = t.groups;
+            part += t.groups * r.dim;
+        }
+        launch_rows<true>(r, s, a, st);
     }
-    const dim3 g((unsigned)((2 * r.dim + 15) / 16)), b(1024);
-    if (dtype == Q4MX_BF16 && add) k_gain_grads<true, true><<<g, b, 0, st>>>(part, groups, r.dim, gq, gk);
-    else if (dtype == Q4MX_BF16) k_gain_grads<true, false><<<g, b, 0, st>>>(part, groups, r.dim, gq, gk);
-    else if (add) k_gain_grads<false, true><<<g, b, 0, st>>>(part, groups, r.dim, gq, gk);
-    else k_gain_grads<false, false><<<g, b, 0, st>>>(part, groups, r.dim, gq, gk);
+    const dim3 n((unsigned)(2 * ((r.dim + 15) / 16))), b(1024);
+    if (dtype == Q4MX_BF16 && add) k_gain_grads<true, true><<<n, b, 0, st>>>(g, r.dim);
+    else if (dtype == Q4MX_BF16) k_gain_grads<true, false><<<n, b, 0, st>>>(g, r.dim);
+    else if (add) k_gain_grads<false, true><<<n, b, 0, st>>>(g, r.dim);
+    else k_gain_grads<false, false><<<n, b, 0, st>>>(g, r.dim);
     return hipGetLastError();
 }
 
