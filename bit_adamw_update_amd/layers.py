@@ -124,7 +124,7 @@ def _heads(name, t, like=None):
 
 
 def _vector(name, t, n, dtypes=_BOTH):
-    if not isinstance(t, torch.Tensor) or tuple(t.shape) != (n,) or (n > 1 and t.stride(0) != 1):
+    if not isinstance(t, torch.Tensor) or t.shape != (n,) or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous tensor of {n} elements")
     if t.dtype not in dtypes:
         raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, not {t.dtype}")
@@ -142,26 +142,37 @@ def _pair(name, v):
 
 def _rope(q, k, q_gain, k_gain, positions, frequencies, eps, interleaved):
     """The packed q4nn_rope of a call."""
-    if q.shape[:-2] != k.shape[:-2] or q.shape[-1] != k.shape[-1]:
-        raise ValueError(f"q {tuple(q.shape)} and k {tuple(k.shape)} differ in more than their heads")
-    *lead, dim = q.shape[:-2] + q.shape[-1:]
+    shape, k_shape = q.shape, k.shape
+    *lead, q_heads, dim = shape
+    if k_shape[:-2] != shape[:-2] or k_shape[-1] != dim:
+        raise ValueError(f"q {tuple(shape)} and k {tuple(k_shape)} differ in more than their heads")
     _vector("q_gain", q_gain, dim)
-    _vector("k_gain", k_gain, dim, (q_gain.dtype,))
+    gain_dtype = q_gain.dtype
+    _vector("k_gain", k_gain, dim, (gain_dtype,))
     position_type = _ints("positions", positions)
-    shape, stride = tuple(positions.shape), positions.stride()
-    if shape == tuple(lead):
-        step, batch_step = stride[-1] if shape[-1] > 1 else 0, stride[0] if len(shape) == 2 and shape[0] > 1 else 0
-    elif shape == tuple(lead[1:]):   # of every batch
-        step, batch_step = stride[0] if shape[0] > 1 else 0, 0
+    at, step = list(positions.shape), positions.stride()
+    if at == lead:
+        batch_step = step[0] if len(at) == 2 and at[0] > 1 else 0
+    elif len(lead) == 2 and at == lead[1:]:   # of every batch
+        batch_step = 0
     else:
-        raise ValueError(f"positions must have shape {tuple(lead)}, not {shape}")
+        raise ValueError(f"positions must have shape {tuple(lead)}, not {tuple(at)}")
     if not isinstance(frequencies, torch.Tensor) or frequencies.dim() != 1:
         raise ValueError("frequencies must be a 1-D tensor")
-    _vector("frequencies", frequencies, frequencies.shape[0], (torch.float64,))
-    return _PACK_ROPE(lead[0] if len(lead) == 2 else 1, lead[-1], q.shape[-2], k.shape[-2], dim,
-                      2 * frequencies.shape[0], int(interleaved), _DTYPES[q_gain.dtype], position_type, eps,
-                      q_gain.data_ptr(), k_gain.data_ptr(), positions.data_ptr(), batch_step, step,
+    pairs = frequencies.shape[0]
+    _vector("frequencies", frequencies, pairs, (torch.float64,))
+    return _PACK_ROPE(lead[0] if len(lead) == 2 else 1, lead[-1], q_heads, k_shape[-2], dim, 2 * pairs,
+                      1 if interleaved else 0, _DTYPES[gain_dtype], position_type, eps, q_gain.data_ptr(),
+                      k_gain.data_ptr(), positions.data_ptr(), batch_step, step[-1] if at[-1] > 1 else 0,
                       frequencies.data_ptr())
+
+
+def _new_heads(like):
+    """An uninitialized result of like's shape, and its description."""
+    t = torch.empty_like(like, memory_format=torch.contiguous_format)
+    heads, dim = t.shape[-2:]
+    row = heads * dim
+    return t, _PACK_HEADS(t.data_ptr(), row * t.shape[-3], row, dim)
 
 
 def head_norm_rope(q, k, q_gain, k_gain, positions, frequencies, eps: float = 1e-6, interleaved: bool = False,
@@ -185,8 +196,7 @@ def head_norm_rope(q, k, q_gain, k_gain, positions, frequencies, eps: float = 1e
         return _entered(device, stream, (q, k, q_gain, k_gain, positions, frequencies, out), head_norm_rope, q, k,
                         q_gain, k_gain, positions, frequencies, eps, interleaved, out)
     if out is None:
-        qo, ko = (torch.empty(t.shape, dtype=torch.bfloat16, device=device) for t in (q, k))
-        pqo, pko = _heads("out[0]", qo), _heads("out[1]", ko)
+        (qo, pqo), (ko, pko) = _new_heads(q), _new_heads(k)
     api.q4nn_head_norm_rope(rope, pq, pk, pqo, pko, _raw(device))
     return qo, ko
 
@@ -219,8 +229,7 @@ def head_norm_rope_backward(q, k, q_gain, k_gain, positions, frequencies, dq, dk
         return _entered(device, stream, tuple(held), head_norm_rope_backward, q, k, q_gain, k_gain, positions,
                         frequencies, dq, dk, eps, interleaved, out, gain_grads, accumulate, dtype)
     if out is None:
-        qo, ko = (torch.empty(t.shape, dtype=torch.bfloat16, device=device) for t in (q, k))
-        pqo, pko = _heads("out[0]", qo), _heads("out[1]", ko)
+        (qo, pqo), (ko, pko) = _new_heads(q), _new_heads(k)
     if gain_grads is None:
         gq, gk = (torch.empty(q.shape[-1], dtype=dtype, device=device) for _ in range(2))
     need = api.q4nn_head_norm_rope_backward_workspace_bytes(rope)
@@ -256,7 +265,10 @@ def dropout(x, p: float, seed: int, step, layer: int, residual=None, offset: int
         return _entered(device, stream, (x, residual, out, step if on_gpu else None), dropout, x, p, seed, step, layer,
                         residual, offset, out)
     rows, cols = x.shape
-    out, code, ldo = _result(out, (rows, cols), x.dtype, device)
+    if out is None:
+        out, code, ldo = torch.empty_like(x, memory_format=torch.contiguous_format), _DTYPES[x.dtype], max(1, cols)
+    else:
+        out, code, ldo = _result(out, (rows, cols), x.dtype, device)
     if on_gpu:
         at, step = step.data_ptr(), 0
     api.q4nn_dropout(p, seed, step, at, layer, offset, x.data_ptr(), ldx, None if residual is None else

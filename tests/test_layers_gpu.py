@@ -600,7 +600,7 @@ def test_refusals():
                        (lambda: layers.embedding_grad(ids, dy, 5, out=dy), "shape"),
                        (lambda: rope(k=h[:3]), "differ"), (lambda: rope(q=h[..., ::2]), "consecutive"),
                        (lambda: rope(g=one[:7]), "8 elements"), (lambda: rope(g=one.to(BF)), "float32|bfloat16"),
-                       (lambda: rope(p=ids[:3]), "positions"), (lambda: rope(p=ids.float()), "int32"),
+                       (lambda: rope(p=ids[:3]), "positions"), (lambda: rope(p=ids[0]), "positions"), (lambda: rope(p=ids.float()), "int32"),
                        (lambda: rope(fr=f.float()), "float64"), (lambda: rope(out=h), "pair"),
                        (lambda: rope(out=(h, h[:, :1])), "shape"),
                        (lambda: rope(g=one.clone().requires_grad_()), "gradient"),
