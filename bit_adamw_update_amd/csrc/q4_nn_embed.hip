@@ -47,9 +47,10 @@ __global__ __launch_bounds__(256) void k_embedding(Ids ids, Dense table, MxMat m
 //   1. tiles of 1024 tokens are sorted in shared memory, and the gradient is
 //      filled with zeros by the work-groups behind them: the sort is over long
 //      before the fill of a large vocabulary's table is, and writes alone run
-//      at 7.9 TB/s where reads and writes together reach 5.1;
+//      at 6.6 to 7.9 TB/s where reads and writes together reach 5.1;
 //   2. up to 16 sorted runs at a time are merged: an element's place is the
-//      number of smaller ones in all of them;
+//      number of smaller ones in all of them (unless the first step placed it
+//      already);
 //   3. a wave takes the rows that begin in a piece of 8 or 16 sorted tokens, 512
 //      columns of them.  A row of up to 32 tokens is summed whole, past the
 //      piece's end where it has to; of a longer one every piece that it touches
@@ -58,6 +59,10 @@ __global__ __launch_bounds__(256) void k_embedding(Ids ids, Dense table, MxMat m
 // Keys are (id << 32) | position; a token that counts for no row has the id
 // kNone and lies behind all others.
 constexpr int kSortTile = 1024, kMergeRuns = 16, kShort = 32, kSlab = 512;
+// A sort that needs no merges (RANKED below) where the fill beside it takes
+// longer: kHides bytes of zeros a tile, 1.5 us (8192 tokens into 151936 x 1024:
+// 70.6 us, with merges 75.0; into 1000 x 64, with 16384 tokens: 40.3 and 26.2).
+constexpr int64_t kRanked = 65536, kHides = 12 << 20;
 constexpr int kPiece = 16, kSmallPiece = 8;  // sorted tokens (see piece_of)
 constexpr int kJoinCols = 256, kJoinPieces = 16;
 constexpr uint32_t kNone = 0x80000000u;   // above every id; one more is a number too
@@ -70,8 +75,7 @@ struct Fill {
     int64_t row_bytes, pitch;  // one row if the rows follow each other
     int64_t row_pieces, end;   // of all pieces, up to `end`
 };
-constexpr int kFillRounds = 8;                       // pieces of a thread
-constexpr int64_t kMergeFill = (int64_t(32) << 20) / 16;  // beside a merge: what is written while it waits for its loads
+constexpr int kFillRounds = 8;  // pieces of a thread
 template <int THREADS> __device__ __forceinline__ void fill_zero(const Fill& f, int64_t first) {
     const int64_t row = first / f.row_pieces;
     const uint32_t at = (uint32_t)(first - row * f.row_pieces);
@@ -119,18 +123,23 @@ template <int LOG> __device__ __forceinline__ int place_in_four(const uint32_t* 
 // position); four such runs, and then four of 256, become one by binary
 // searches in shared memory.  (A bitonic sort's 55 exchanges took 11.8 us, 15
 // searches of 64 at once 7.2.)
+//
+// RANKED: a tile finds its places among all tokens by itself.  It looks every
+// other tile's ids up in its own sorted ones and counts them there: what is
+// counted up to an element lies before it.  That takes 1.5 us for each of the
+// others (shared memory's rate), and saves the merges' launches.
+template <bool RANKED>
 __global__ __launch_bounds__(kSortTile) void k_sort_tiles(Ids ids, int64_t rows, uint64_t* keys, int64_t tiles,
                                                            Fill fill) {
-    __shared__ uint32_t run_id[2][kSortTile], run_token[2][kSortTile];
+    __shared__ uint32_t run_id[2][kSortTile], run_token[2][kSortTile], counted[RANKED ? kSortTile + 1 : 1], of_wave[16];
     const int64_t tile = group_index();
     if (tile >= tiles) return fill_zero<kSortTile>(fill, (tile - tiles) * (kSortTile * kFillRounds));
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int64_t t = tile * kSortTile + tid;
-    uint32_t id = kNone;
-    if (t < ids.n) {
-        const int64_t v = load_id(ids, t);
-        if (v >= 0 && v < rows) id = (uint32_t)v;
-    }
+    const auto id_at = [&](int64_t t) {
+        const int64_t v = t < ids.n ? load_id(ids, t) : -1;
+        return v >= 0 && v < rows ? (uint32_t)v : kNone;
+    };
+    uint32_t id = id_at(tile * kSortTile + tid);
     int rank = 0;
 #pragma unroll
     for (int j = 0; j < 64; ++j) {
@@ -138,7 +147,7 @@ __global__ __launch_bounds__(kSortTile) void k_sort_tiles(Ids ids, int64_t rows,
         rank += other < id + (j < lane ? 1u : 0u) ? 1 : 0;
     }
     run_id[0][wave * 64 + rank] = id;
-    run_token[0][wave * 64 + rank] = (uint32_t)t;
+    run_token[0][wave * 64 + rank] = (uint32_t)(tile * kSortTile + tid);
     __syncthreads();
     id = run_id[0][tid];
     uint32_t token = run_token[0][tid];
@@ -150,18 +159,57 @@ __global__ __launch_bounds__(kSortTile) void k_sort_tiles(Ids ids, int64_t rows,
         id = run_id[1][tid], token = run_token[1][tid];
         place = place_in_four<8>(run_id[1], tid, id);
     }
-    // past the last token: ids of kNone from the end of the tile, so they are the last
-    if (tile * kSortTile + place < ids.n) keys[tile * kSortTile + place] = (uint64_t)id << 32 | token;
+    int64_t before = tile * kSortTile;
+    if (RANKED) {
+        run_id[0][place] = id;
+        counted[tid] = 0;
+        if (tid == 0) counted[kSortTile] = 0;
+        __syncthreads();
+        constexpr int kAtOnce = 4;
+        for (int64_t first = 0; first < tiles; first += kAtOnce) {
+            uint32_t below[kAtOnce];
+            int at[kAtOnce];
+#pragma unroll
+            for (int k = 0; k < kAtOnce; ++k) {
+                // of equal ids, those of a tile before this one come first
+                below[k] = id_at((first + k) * kSortTile + tid) + (first + k < tile ? 0u : 1u);
+                at[k] = 0;
+            }
+            // side by side: a step of one waits for shared memory
+#pragma unroll
+            for (int step = kSortTile / 2; step > 0; step /= 2)
+#pragma unroll
+                for (int k = 0; k < kAtOnce; ++k) at[k] += run_id[0][at[k] + step - 1] < below[k] ? step : 0;
+#pragma unroll
+            for (int k = 0; k < kAtOnce; ++k) at[k] += run_id[0][at[k]] < below[k] ? 1 : 0;
+#pragma unroll
+            for (int k = 0; k < kAtOnce; ++k)
+                if (first + k != tile && (first + k) * kSortTile + tid < ids.n) atomicAdd(&counted[at[k]], 1u);
+        }
+        __syncthreads();
+        // the running sums of `counted`
+        int sum = (int)counted[tid];
+#pragma unroll
+        for (int m = 1; m < 64; m *= 2) {
+            const int up = __shfl_up(sum, m);
+            if (lane >= m) sum += up;
+        }
+        if (lane == 63) of_wave[wave] = (uint32_t)sum;
+        __syncthreads();
+        for (int w = 0; w < wave; ++w) sum += (int)of_wave[w];
+        counted[tid] = (uint32_t)sum;
+        __syncthreads();
+        before = counted[place];
+    }
+    // past the last token: ids of kNone from the end of the last tile, the last of all
+    if (token < ids.n) keys[before + place] = (uint64_t)id << 32 | token;
 }
 
 // Runs of `run` keys, the last one shorter: each kMergeRuns neighbours become
 // one.  16 lanes to a key, a run to each.  (A thread to a key took 32 us for
 // 16384 keys, this 5.8: 11 loads that wait for each other in place of 165.)
-__global__ __launch_bounds__(256) void k_merge_runs(const uint64_t* src, uint64_t* dst, int64_t n, int64_t run,
-                                                     Fill fill, int64_t fill_from) {
-    const int64_t groups = (n + 15) / 16, block = group_index();
-    if (block >= groups) return fill_zero<256>(fill, fill_from + (block - groups) * (256 * kFillRounds));
-    const int64_t i = block * 16 + (threadIdx.x >> 4);
+__global__ __launch_bounds__(256) void k_merge_runs(const uint64_t* src, uint64_t* dst, int64_t n, int64_t run) {
+    const int64_t i = (int64_t)group_index() * 16 + (threadIdx.x >> 4);
     if (i >= n) return;
     const uint64_t key = src[i];
     const int64_t group = i / (run * kMergeRuns) * (run * kMergeRuns);
@@ -417,7 +465,6 @@ hipError_t launch_embedding_grad(const Ids& ids, const Dense& dy, float scale, i
     const int64_t n = ids.n, tiles = parts_of(n, kSortTile);
     Fill fill = {};
     fill.row_pieces = 1;
-    int64_t split = 0, rest = 0;  // zeros up to `split` beside the sort, the rest beside the first merge
     if (!add) {
         const int64_t unit = grad.dtype == Q4MX_BF16 ? 2 : 4;
         const bool flat = grad.ld == cols || rows == 1;
@@ -426,24 +473,20 @@ hipError_t launch_embedding_grad(const Ids& ids, const Dense& dy, float scale, i
         fill.pitch = flat ? 0 : grad.ld * unit;
         fill.row_pieces = parts_of(fill.row_bytes, 16);
         fill.end = (flat ? 1 : rows) * fill.row_pieces;
-        if (n > kSortTile) rest = fill.end / 2 < kMergeFill ? fill.end / 2 : kMergeFill;
-        split = fill.end - rest;
     }
     const GradWorkspace w(n, cols);
     char* p = static_cast<char*>(ws);
     uint64_t *keys = reinterpret_cast<uint64_t*>(p), *other = reinterpret_cast<uint64_t*>(p + w.keys);
-    Fill begun = fill;
-    begun.end = split;
-    k_sort_tiles<<<grid_of(tiles + parts_of(split, kSortTile * kFillRounds), kSortTile), dim3(kSortTile), 0, st>>>(
-        ids, rows, keys, tiles, begun);
+    const bool ranked = tiles > 1 && n <= kRanked && fill.end * 16 >= tiles * kHides;
+    const dim3 g = grid_of(tiles + parts_of(fill.end, kSortTile * kFillRounds), kSortTile), b(kSortTile);
+    if (ranked) k_sort_tiles<true><<<g, b, 0, st>>>(ids, rows, keys, tiles, fill);
+    else k_sort_tiles<false><<<g, b, 0, st>>>(ids, rows, keys, tiles, fill);
     if (n == 0) return hipGetLastError();
     GradArgs a = {};
     a.long_begins = reinterpret_cast<uint32_t*>(p + 2 * w.keys);
     a.part = reinterpret_cast<float*>(p + 2 * w.keys + w.flags);
-    for (int64_t run = kSortTile; run < n; run *= kMergeRuns) {
-        k_merge_runs<<<grid_of(parts_of(n, 16) + parts_of(rest, 256 * kFillRounds)), dim3(256), 0, st>>>(
-            keys, other, n, run, fill, split);
-        rest = 0, fill.end = 0;
+    for (int64_t run = kSortTile; run < n && !ranked; run *= kMergeRuns) {
+        k_merge_runs<<<grid_of(parts_of(n, 16)), dim3(256), 0, st>>>(keys, other, n, run);
         uint64_t* t = keys;
         keys = other, other = t;
     }

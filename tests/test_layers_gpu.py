@@ -667,3 +667,23 @@ def test_a_layers_ends_between_masters_and_gradients():
     _check_grad(ids, dx0, rows, math.sqrt(d), BF, out=grad)
     start = grad.clone()
     _check_grad(ids, dx0, rows, math.sqrt(d), BF, start, out=grad, accumulate=True)   # a second micro-batch's
+
+
+# ---- sorting without merges: tokens of several tiles beside the fill of a large table ----------
+
+@pytest.mark.parametrize("how", ["same", "text", "falling", "none", "padded"])
+@pytest.mark.parametrize("tokens,rows,cols", [(1025, 40000, 320), (3000, 60000, 320), (5000, 100000, 320), (16384, 320000, 320)])
+def test_embedding_grad_of_large_tables(tokens, rows, cols, how):
+    _say("large table", tokens, rows, cols, how)
+    ids, dy = _drawn(how, tokens, rows, tokens).to(DEV), _normal(tokens, cols, seed=3).to(DEV)
+    got = layers.embedding_grad(ids, dy, rows, scale=0.5)
+    # added to zeros, which sorts with merges and sums in the same order
+    want = torch.zeros(rows, cols, dtype=BF, device=DEV)
+    layers.embedding_grad(ids, dy, rows, scale=0.5, out=want, accumulate=True)
+    assert torch.equal(got, want)
+    real = (ids >= 0) & (ids < rows)
+    seen = torch.unique(ids[real])
+    want, mag, n = ref.embedding_grad(torch.searchsorted(seen, ids[real]), dy[real], len(seen), 0.5)
+    _close(got[seen], want, (n[:, None] + 3) * S24 * mag, BF)
+    got[seen] = 0
+    assert float(got.abs().amax()) == 0
