@@ -51,7 +51,7 @@ __global__ __launch_bounds__(256) void k_embedding(Ids ids, Dense table, MxMat m
 //   2. up to 16 sorted runs at a time are merged: an element's place is the
 //      number of smaller ones in all of them (unless the first step placed it
 //      already);
-//   3. a wave takes the rows that begin in a piece of 8 or 16 sorted tokens, 512
+//   3. a wave takes the rows that begin in a piece of 2 to 32 sorted tokens, 512
 //      columns of them.  A row of up to 32 tokens is summed whole, past the
 //      piece's end where it has to; of a longer one every piece that it touches
 //      leaves an FP32 sum in the workspace;
@@ -63,8 +63,7 @@ constexpr int kSortTile = 1024, kMergeRuns = 16, kShort = 32, kSlab = 512;
 // longer: kHides bytes of zeros a tile, 1.5 us (8192 tokens into 151936 x 1024:
 // 70.6 us, with merges 75.0; into 1000 x 64, with 16384 tokens: 40.3 and 26.2).
 constexpr int64_t kRanked = 65536, kHides = 12 << 20;
-constexpr int kPiece = 16, kSmallPiece = 8;  // sorted tokens (see piece_of)
-constexpr int kJoinCols = 256, kJoinPieces = 16;
+constexpr int kJoinCols = 256, kJoinPieces = 16, kJoinWaves = 8;
 constexpr uint32_t kNone = 0x80000000u;   // above every id; one more is a number too
 
 __device__ __forceinline__ uint32_t id_of(uint64_t key) { return (uint32_t)(key >> 32); }
@@ -229,20 +228,20 @@ __global__ __launch_bounds__(256) void k_merge_runs(const uint64_t* src, uint64_
     if ((threadIdx.x & 15) == 0) dst[group + (uint32_t)smaller] = key;
 }
 
-// scale * sum into N columns of a row from col on, or added to what is there;
-// those before `skip` and from `left` on are another lane's, or do not exist.
-template <bool BF16, bool ADD, int N>
-__device__ __forceinline__ void store_grad(const Dense& grad, int64_t row, int64_t col, int skip, int64_t left,
-                                           float scale, const float* sum) {
-    const int64_t at = row * grad.ld + col;
-    if (N == 8 && skip == 0 && left >= 8) {
-        float v[8];
-        if (ADD) load8<BF16>(grad.p, at, 8, v);
+// scale * sum into 8 columns of a row, or added to what is there.
+template <bool BF16, bool ADD>
+__device__ __forceinline__ void store_grad8(const Dense& grad, int64_t at, float scale, const float* sum) {
+    float v[8];
+    if (ADD) load8<BF16>(grad.p, at, 8, v);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = ADD ? __builtin_fmaf(scale, sum[k], v[k]) : scale * sum[k];
-        store8<BF16>(grad.p, at, 8, v);
-        return;
-    }
+    for (int k = 0; k < 8; ++k) v[k] = ADD ? __builtin_fmaf(scale, sum[k], v[k]) : scale * sum[k];
+    store8<BF16>(grad.p, at, 8, v);
+}
+// The same of N columns, of which those before `skip` and from `left` on are
+// another lane's, or do not exist.
+template <bool BF16, bool ADD, int N>
+__device__ __forceinline__ void store_grad_some(const Dense& grad, int64_t at, int skip, int64_t left, float scale,
+                                                const float* sum) {
 #pragma unroll
     for (int k = 0; k < N; ++k) {
         if (k < skip || k >= left) continue;
@@ -264,9 +263,12 @@ struct GradArgs {
     Dense grad;
 };
 
-// NARROW: fewer than 8 columns.  Else a lane whose 8 columns pass the end takes
-// the last 8, and stores those that are its own.
-template <bool BF16, bool ADD, bool NARROW> __global__ __launch_bounds__(256) void k_grad_pieces(GradArgs a) {
+// WHOLE: whole vectors of 8 columns, whose code is a third of the others'
+// (the loop below holds a row's end 16 times, and has to fit the instruction
+// cache).  RAGGED: a lane whose 8 columns pass the end takes the last 8, and
+// stores those that are its own.  NARROW: fewer than 8 columns.
+enum Columns { WHOLE, RAGGED, NARROW };
+template <bool BF16, bool ADD, int COLS> __global__ __launch_bounds__(256) void k_grad_pieces(GradArgs a) {
     const int lane = threadIdx.x & 63;
     const int64_t unit = (int64_t)group_index() * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t piece = unit / a.slabs, slab = unit - piece * a.slabs;
@@ -299,25 +301,29 @@ template <bool BF16, bool ADD, bool NARROW> __global__ __launch_bounds__(256) vo
         return;
     }
     const int64_t col = slab * kSlab + lane * 8, left = a.cols - col;
-    const int64_t at = NARROW ? 0 : left >= 8 ? col : left > 0 ? a.cols - 8 : 0;
-    const int skip = left >= 8 || NARROW ? 0 : left > 0 ? (int)(8 - left) : 8;
-    const int64_t here = NARROW ? (lane == 0 ? a.cols : 0) : 8;  // of the 8 columns from `at` on
+    // Lanes past the columns go along on the first ones and store nothing: all 64 hold a token that is read below.
+    const int64_t at = COLS == NARROW ? 0 : left >= 8 ? col : left > 0 ? a.cols - 8 : 0;
+    const int skip = left >= 8 || COLS == NARROW ? 0 : left > 0 ? (int)(8 - left) : 8;
+    const int64_t here = COLS == NARROW ? (lane == 0 ? a.cols : 0) : 8;  // of the 8 columns from `at` on
+    const bool whole = skip == 0 && here == 8;
     float sum[8] = {};
     uint32_t current = (uint32_t)__builtin_amdgcn_readlane((int)id, from);
     int begun = from;
     auto finish = [&](int to) {
         if ((begun == 0 && first_long) || (to == end && last_long)) {
             float* p = a.part + (piece * 2 + (begun == 0 ? 0 : 1)) * a.part_ld + at;
-            if (skip == 0 && here == 8) {
+            if (whole) {
                 *reinterpret_cast<float4*>(p) = make_float4(sum[0], sum[1], sum[2], sum[3]);
                 *reinterpret_cast<float4*>(p + 4) = make_float4(sum[4], sum[5], sum[6], sum[7]);
-            } else {
+            } else if (COLS != WHOLE) {
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
                     if (k >= skip && k < here) p[k] = sum[k];
             }
-        } else {
-            store_grad<BF16, ADD, 8>(a.grad, current, at, skip, here, a.scale, sum);
+        } else if (whole) {
+            store_grad8<BF16, ADD>(a.grad, current * a.grad.ld + at, a.scale, sum);
+        } else if (COLS != WHOLE) {
+            store_grad_some<BF16, ADD, 8>(a.grad, current * a.grad.ld + at, skip, here, a.scale, sum);
         }
     };
     constexpr int kBatch = 16;
@@ -328,7 +334,7 @@ template <bool BF16, bool ADD, bool NARROW> __global__ __launch_bounds__(256) vo
             // past the end: the last token once more, not added
             const int e = i + j < end ? i + j : end - 1;
             const uint16_t* p = a.dy + (int64_t)(uint32_t)__builtin_amdgcn_readlane((int)token, e) * a.lddy + at;
-            if (!NARROW) {
+            if (COLS != NARROW) {
                 raw[j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_any*>(p));
             } else {
                 uint32_t w[8];
@@ -357,10 +363,10 @@ template <bool BF16, bool ADD, bool NARROW> __global__ __launch_bounds__(256) vo
     finish(end);
 }
 
-// The long rows that begin in one of 16 pieces: a wave adds every fourth of a
-// row's sums, 4 columns to a lane, and the four waves' sums are added in order.
-template <bool BF16, bool ADD> __global__ __launch_bounds__(256) void k_grad_join(GradArgs a, int64_t col_groups) {
-    __shared__ float4 lds[4][64];
+// The long rows that begin in one of 16 pieces: a wave adds every eighth of a
+// row's sums, 4 columns to a lane, and the waves' sums are added in order.
+template <bool BF16, bool ADD> __global__ __launch_bounds__(64 * kJoinWaves) void k_grad_join(GradArgs a, int64_t col_groups) {
+    __shared__ float4 lds[kJoinWaves][64];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t block = group_index(), pg = block / col_groups;
     const int64_t col = (block - pg * col_groups) * kJoinCols + lane * 4, left = a.cols - col;
@@ -384,11 +390,12 @@ template <bool BF16, bool ADD> __global__ __launch_bounds__(256) void k_grad_joi
             more += 64;
         }
         float sum[4] = {};
+        const int own_slot = __builtin_amdgcn_readlane((int)slot, which) - 1;
         if (left > 0) {
-            const float* own = a.part + (piece * 2 + __builtin_amdgcn_readlane((int)slot, which) - 1) * a.part_ld + col;
+            const float* own = a.part + (piece * 2 + own_slot) * a.part_ld + col;
             const float* next = a.part + (piece + 1) * 2 * a.part_ld + col;
-#pragma unroll 4
-            for (int64_t k = wave; k <= more; k += 4) {
+#pragma unroll 8
+            for (int64_t k = wave; k <= more; k += kJoinWaves) {
                 const float4 v = *reinterpret_cast<const float4*>(k == 0 ? own : next + (k - 1) * 2 * a.part_ld);
                 sum[0] += v.x, sum[1] += v.y, sum[2] += v.z, sum[3] += v.w;
             }
@@ -397,11 +404,12 @@ template <bool BF16, bool ADD> __global__ __launch_bounds__(256) void k_grad_joi
         lds[wave][lane] = make_float4(sum[0], sum[1], sum[2], sum[3]);
         __syncthreads();
         if (wave == 0 && left > 0) {
-            for (int w = 1; w < 4; ++w) {
+#pragma unroll
+            for (int w = 1; w < kJoinWaves; ++w) {
                 const float4 v = lds[w][lane];
                 sum[0] += v.x, sum[1] += v.y, sum[2] += v.z, sum[3] += v.w;
             }
-            store_grad<BF16, ADD, 4>(a.grad, id, col, 0, left, a.scale, sum);
+            store_grad_some<BF16, ADD, 4>(a.grad, id * a.grad.ld + col, 0, left, a.scale, sum);
         }
     }
 }
@@ -411,11 +419,12 @@ int64_t parts_of(int64_t n, int64_t part) { return (n + part - 1) / part; }
 
 template <bool BF16, bool ADD> void launch_sums(const GradArgs& a, hipStream_t st) {
     const dim3 g = grid_of(parts_of(a.pieces * a.slabs, 4)), b(256);
-    if (a.cols < 8) k_grad_pieces<BF16, ADD, true><<<g, b, 0, st>>>(a);
-    else k_grad_pieces<BF16, ADD, false><<<g, b, 0, st>>>(a);
+    if (a.cols < 8) k_grad_pieces<BF16, ADD, NARROW><<<g, b, 0, st>>>(a);
+    else if (a.cols % 8 != 0) k_grad_pieces<BF16, ADD, RAGGED><<<g, b, 0, st>>>(a);
+    else k_grad_pieces<BF16, ADD, WHOLE><<<g, b, 0, st>>>(a);
     if (a.n > kShort) {
         const int64_t cg = parts_of(a.cols, kJoinCols);
-        k_grad_join<BF16, ADD><<<grid_of(parts_of(a.pieces, kJoinPieces) * cg), dim3(256), 0, st>>>(a, cg);
+        k_grad_join<BF16, ADD><<<grid_of(parts_of(a.pieces, kJoinPieces) * cg), dim3(64 * kJoinWaves), 0, st>>>(a, cg);
     }
 }
 
@@ -441,15 +450,23 @@ hipError_t launch_embedding(const Ids& ids, const Dense& table, const MxMat& mx,
     return hipGetLastError();
 }
 
-// Few tokens leave compute units idle and a wave's time is its steps': shorter
-// pieces (301 tokens: PLACEHOLDER); for many, fewer sums of long rows count.
-int piece_of(int64_t tokens) { return tokens <= 2048 ? kSmallPiece : kPiece; }
+// Few pieces leave compute units idle and a wave's time is its steps': shorter
+// ones; for many, fewer sums of long rows count: longer ones.  Microseconds of a
+// call with pieces of 2, 4, 8, 16, 32: 301 tokens x 100 columns 12.5, 12.7, 13.7,
+// 15.8, 19.4; 2048 x 768 25.5, 24.4, 24.3, 26.1, 30.7; 4096 x 1024 31.5, 29.2,
+// 28.8, 30.4, 34.2; 16384 x 2560 110, 88, 79, 76.5, 78; 131072 x 512 223, 164,
+// 133, 121, 117.  The wave sees 64 tokens from the piece's first on, so kShort +
+// the piece is at most 64.
+int piece_of(int64_t tokens, int64_t cols) {
+    const int64_t n = tokens * parts_of(cols, kSlab);
+    return n <= 1024 ? 2 : n <= 4096 ? 4 : n <= 16384 ? 8 : n < 131072 ? 16 : 32;
+}
 
 // The parts of a gradient's workspace: keys twice, the pieces' flags, the long rows' sums.
 struct GradWorkspace {
     size_t keys, flags, part;
     GradWorkspace(int64_t tokens, int64_t cols) {
-        const int64_t pieces = parts_of(tokens, piece_of(tokens));
+        const int64_t pieces = parts_of(tokens, piece_of(tokens, cols));
         keys = round256(sizeof(uint64_t) * (size_t)tokens);
         flags = round256(sizeof(uint32_t) * (size_t)pieces);
         part = tokens > kShort ? sizeof(float) * (size_t)(pieces * 2 * parts_of(cols, 8) * 8) : 0;
@@ -490,7 +507,7 @@ hipError_t launch_embedding_grad(const Ids& ids, const Dense& dy, float scale, i
         uint64_t* t = keys;
         keys = other, other = t;
     }
-    a.keys = keys, a.n = n, a.piece = piece_of(n), a.pieces = parts_of(n, a.piece), a.slabs = parts_of(cols, kSlab);
+    a.keys = keys, a.n = n, a.piece = piece_of(n, cols), a.pieces = parts_of(n, a.piece), a.slabs = parts_of(cols, kSlab);
     a.dy = static_cast<const uint16_t*>(dy.p), a.lddy = dy.ld;
     a.cols = cols, a.part_ld = parts_of(cols, 8) * 8;
     a.scale = scale, a.grad = grad;
