@@ -80,6 +80,11 @@ bool shifted(const q4nn_heads* a, const q4nn_heads* b, const q4nn_rope* r) {
            ((r->batches > 1 && a->batch != b->batch) || (r->tokens > 1 && a->token != b->token) || a->head != b->head);
 }
 
+// Whether q's and k's results begin in one place.
+bool one_place(const q4nn_heads* q, const q4nn_heads* k, const q4nn_rope* r) {
+    return q->p == k->p && r->batches * r->tokens > 0 && r->q_heads > 0 && r->k_heads > 0;
+}
+
 q4_status check_rope(const q4nn_rope* r) {
     if (!r) return bad(Q4_ERR_INVALID_ARG, "r is NULL");
     if (r->batches < 0 || r->tokens < 0 || r->batches >= kMaxDim || r->tokens >= kMaxDim ||
@@ -179,6 +184,7 @@ q4_status q4nn_head_norm_rope(const q4nn_rope* r, const q4nn_heads* q, const q4n
     Q4_TRY(check_heads("k_out", k_out, r, r->k_heads, true));
     if (shifted(q_out, q, r) || shifted(k_out, k, r))
         return bad(Q4_ERR_SHAPE, "an output in place of its input must have its strides");
+    if (one_place(q_out, k_out, r)) return bad(Q4_ERR_CONFLICT, "q_out and k_out are one buffer");
     if (empty(r)) return ok();
     Q4_TRY(device());
     return launched(launch_head_norm_rope(*r, *q, *k, *q_out, *k_out, reinterpret_cast<hipStream_t>(stream)),
@@ -207,8 +213,10 @@ q4_status q4nn_head_norm_rope_backward(const q4nn_rope* r, const q4nn_heads* q, 
     Q4_TRY(check_heads("dk_in", dk_in, r, r->k_heads, true));
     if (shifted(dq_in, dq, r) || shifted(dk_in, dk, r))
         return bad(Q4_ERR_SHAPE, "a gradient in place of the result's must have its strides");
+    if (one_place(dq_in, dk_in, r)) return bad(Q4_ERR_CONFLICT, "dq_in and dk_in are one buffer");
     Q4_TRY(check_dense("dq_gain", dq_gain, dtype, 1, r->dim, r->dim));
     Q4_TRY(check_dense("dk_gain", dk_gain, dtype, 1, r->dim, r->dim));
+    if (dq_gain == dk_gain) return bad(Q4_ERR_CONFLICT, "dq_gain and dk_gain are one buffer: add them up afterwards");
     const bool add = (flags & Q4NN_ADD) != 0;
     if (add && empty(r)) return ok();
     Q4_TRY(check_ws(ws, ws_bytes, need));

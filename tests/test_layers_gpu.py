@@ -566,6 +566,35 @@ def test_on_another_stream(which):
         call(*fresh, stream=Other())
 
 
+def test_given_results_on_another_stream():
+    ids, rows = _drawn("text", 500, 90, 1).to(DEV), 90
+    table, dy = _normal(90, 64, seed=2, dtype=F32).to(DEV), _normal(500, 64, seed=3).to(DEV)
+    q, k, gq, gk, pos, f, how = _heads_case(500, 1, 1, 64, 64, True, "split", 4)
+    heads = (q, k, gq.to(DEV), gk.to(DEV), pos.to(DEV), f)
+
+    def outs():
+        e = lambda *s, dt=BF: torch.ones(*s, dtype=dt, device=DEV)   # noqa: E731
+        return [e(500, 64, dt=F32), e(rows, 64, dt=F32), (e(500, 1, 64), e(500, 1, 64)), (e(500, 1, 64), e(500, 1, 64)),
+                (e(64, dt=F32), e(64, dt=F32)), e(500, 64)]
+
+    def run(o, **kw):
+        return [layers.embedding(ids, table, 2.0, o[0], F32, **kw),
+                layers.embedding_grad(ids, dy, rows, 2.0, o[1], True, F32, **kw),
+                layers.head_norm_rope(*heads, 1e-6, True, o[2], **kw),
+                layers.head_norm_rope_backward(*heads, q, k, 1e-6, True, list(o[3]), list(o[4]), True, F32, **kw),
+                layers.dropout(dy, 0.3, 1, 2, 3, dy, 16, o[5], **kw)]
+
+    want = run(outs())
+    side = torch.cuda.Stream()
+    given = outs()
+    side.wait_stream(torch.cuda.current_stream())
+    got = run(given, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    flat = lambda v: [t for x in v for t in (x if isinstance(x, tuple) else (x,))]   # noqa: E731
+    assert all(torch.equal(a, b) for a, b in zip(flat(want), flat(got)))
+    assert got[0] is given[0] and got[2][0] is given[2][0] and got[3][2] is given[4][0] and got[4] is given[5]
+
+
 @pytest.mark.parametrize("which", range(5))
 def test_two_at_once_do_not_meet(which):
     """Two calls on two streams, each with a workspace of its own."""
@@ -617,7 +646,8 @@ def test_refusals():
     for call, status in [(lambda: layers.dropout(t, 1.5, 0, 0, 0), 1), (lambda: layers.dropout(t, 0.5, 0, 0, 0, offset=4), 2),
                          (lambda: layers.embedding(ids, t, scale=math.inf), 1), (lambda: layers.embedding_grad(ids, dy, -1), 2),
                          (lambda: rope(eps=0.0), 1), (lambda: rope(out=(h[:, :1].expand(4, 2, 8), torch.zeros_like(h))), 2),
-                         (lambda: rope(fr=layers.rope_frequencies(10)), 2)]:
+                         (lambda: rope(fr=layers.rope_frequencies(10)), 2), (lambda: rope(out=(h, h)), 4),
+                         (lambda: layers.head_norm_rope_backward(h, h, one, one, ids, f, h, h, gain_grads=(one, one)), 4)]:
         with pytest.raises(api.Q4Error) as e:
             call()
         assert e.value.status == status

@@ -12,7 +12,7 @@ import torch
 import layers_reference as ref
 from bit_adamw_update_amd import api, layers
 
-INVALID, SHAPE, ALIGNMENT, WORKSPACE = 1, 2, 3, 7
+INVALID, SHAPE, ALIGNMENT, CONFLICT, WORKSPACE = 1, 2, 3, 4, 7
 P = 0x10000000   # plausible aligned addresses: refused before any is used
 BIG = 1 << 31
 
@@ -95,7 +95,7 @@ def heads(r=None, q=None, k=None, qo=None, ko=None):
     api.q4nn_head_norm_rope(r or rope(), q or view(4), k or view(2), qo or view(4, p=2 * P), ko or view(2, p=3 * P), 0)
 
 
-def back(r=None, dq=None, dqi=None, dki=None, gq=P, gk=P, dtype=api.MX_BF16, flags=0, ws=P, n=1 << 40):
+def back(r=None, dq=None, dqi=None, dki=None, gq=P, gk=2 * P, dtype=api.MX_BF16, flags=0, ws=P, n=1 << 40):
     api.q4nn_head_norm_rope_backward(r or rope(), view(4), view(2), dq or view(4, p=2 * P), view(2, p=3 * P),
                                      dqi or view(4, p=4 * P), dki or view(2, p=5 * P), gq, gk, dtype, flags, ws, n, 0)
 
@@ -136,6 +136,9 @@ def test_head_operands_are_checked():
     refused(WORKSPACE, str(need), back, n=need - 1)
     refused(INVALID, "flags", back, flags=4)
     refused(INVALID, "dq_gain", back, gq=None)
+    refused(CONFLICT, "one buffer", back, gk=P)
+    refused(CONFLICT, "one buffer", back, dki=view(2, p=4 * P))
+    refused(CONFLICT, "one buffer", heads, ko=view(2, p=2 * P))
     refused(INVALID, "dtype", back, dtype=3)
     refused(ALIGNMENT, "dk_gain", back, gk=P + 1)
     refused(SHAPE, "overlap", back, dki=view(2, p=5 * P, head=0))
