@@ -26,9 +26,9 @@ import struct
 import torch
 
 from . import api
-from .mx import (_BOTH, _DTYPES, MXMatrix, _dense, _elsewhere, _entered, _lost_gradient, _raw, _result, _same_device,
-                 _workspace)
+from .mx import _BOTH, _DTYPES, MXMatrix, _dense, _elsewhere, _entered, _lost_gradient, _raw, _result, _same_device
 
+_CONTIGUOUS = torch.contiguous_format
 _INTS = {torch.int32: api.NN_I32, torch.int64: api.NN_I64}
 _PACK_HEADS = struct.Struct("@Pqqq").pack           # a q4nn_heads
 _PACK_ROPE = struct.Struct("@qqiiiiiiifPPPqqP").pack   # a q4nn_rope
@@ -50,6 +50,22 @@ def _tokens(ids):
     return code
 
 
+def _new(like, rows, cols, dtype):
+    """(an uninitialized result, its dtype code, its row stride); like: a tensor of its device."""
+    if dtype not in _DTYPES:
+        raise ValueError(f"dtype must be torch.float32 or torch.bfloat16, not {dtype}")
+    t = like.new_empty((rows, cols)) if like.dtype == dtype else like.new_empty((rows, cols), dtype=dtype)
+    return t, _DTYPES[dtype], max(1, cols)
+
+
+def _room(like, nbytes):
+    """A workspace, in elements of like's type, and where it is."""
+    if nbytes == 0:
+        return None, None
+    t = like.new_empty(nbytes // like.element_size() + 1)
+    return t, t.data_ptr()
+
+
 def embedding(ids, table, scale: float = 1.0, out=None, dtype=torch.bfloat16, stream=None) -> torch.Tensor:
     """scale * table[ids] [tokens, cols]: table a float32 (a master) or
     bfloat16 tensor [rows, cols] or an MXMatrix.  An id below 0 is padding (a
@@ -65,13 +81,17 @@ def embedding(ids, table, scale: float = 1.0, out=None, dtype=torch.bfloat16, st
     if _elsewhere(device, stream):
         return _entered(device, stream, (ids, table, out), embedding, ids, table, scale, out, dtype)
     tokens = ids.shape[0]
-    out, code, ldo = _result(out, (tokens, cols), dtype, device)
-    if coded:
-        api.q4nn_embedding_mx(ids.data_ptr(), id_type, tokens, table.packed, scale, out.data_ptr(), code, ldo,
-                              _raw(device))
+    if out is None:
+        out, code, ldo = _new(ids if coded else table, tokens, cols, dtype)
     else:
-        api.q4nn_embedding(ids.data_ptr(), id_type, tokens, table.data_ptr(), _DTYPES[table.dtype], rows, cols, ld,
-                           scale, out.data_ptr(), code, ldo, _raw(device))
+        out, code, ldo = _result(out, (tokens, cols), dtype, device)
+    lib = api.load_library()
+    if coded:
+        api._check(lib.q4nn_embedding_mx(ids.data_ptr(), id_type, tokens, table.packed, scale, out.data_ptr(), code, ldo,
+                                         _raw(device)))
+    else:
+        api._check(lib.q4nn_embedding(ids.data_ptr(), id_type, tokens, table.data_ptr(), _DTYPES[table.dtype], rows,
+                                      cols, ld, scale, out.data_ptr(), code, ldo, _raw(device)))
     return out
 
 
@@ -90,9 +110,14 @@ def embedding_grad(ids, dy, rows: int, scale: float = 1.0, out=None, accumulate:
     if _elsewhere(device, stream):
         return _entered(device, stream, (ids, dy, out), embedding_grad, ids, dy, rows, scale, out, accumulate, dtype)
     need = api.q4nn_embedding_grad_workspace_bytes(tokens, rows, cols)
-    out, code, ld = _result(out, (rows, cols), dtype, device)
-    api.q4nn_embedding_grad(ids.data_ptr(), id_type, tokens, dy.data_ptr(), lddy, scale, rows, cols, out.data_ptr(),
-                            code, ld, api.NN_ADD if accumulate else 0, _workspace(need, device), need, _raw(device))
+    if out is None:
+        out, code, ld = _new(dy, rows, cols, dtype)
+    else:
+        out, code, ld = _result(out, (rows, cols), dtype, device)
+    ws, at = _room(dy, need)
+    api._check(api.load_library().q4nn_embedding_grad(
+        ids.data_ptr(), id_type, tokens, dy.data_ptr(), lddy, scale, rows, cols, out.data_ptr(), code, ld,
+        api.NN_ADD if accumulate else 0, at, need, _raw(device)))
     return out
 
 
@@ -107,7 +132,7 @@ def _heads(name, t, like=None):
     """A [tokens, heads, dim] or [batch, tokens, heads, dim] operand for a call."""
     if not isinstance(t, torch.Tensor) or t.dim() not in (3, 4):
         raise ValueError(f"{name} must be a tensor [tokens, heads, dim] or [batch, tokens, heads, dim]")
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise ValueError(f"{name} must be torch.bfloat16, not {t.dtype}")
     if _lost_gradient(t):
         raise ValueError(f"{name} has a gradient, which autograd would lose here; call under torch.no_grad() or detach it")
@@ -169,7 +194,7 @@ def _rope(q, k, q_gain, k_gain, positions, frequencies, eps, interleaved):
 
 def _new_heads(like):
     """An uninitialized result of like's shape, and its description."""
-    t = torch.empty_like(like, memory_format=torch.contiguous_format)
+    t = torch.empty_like(like, memory_format=_CONTIGUOUS)
     heads, dim = t.shape[-2:]
     row = heads * dim
     return t, _PACK_HEADS(t.data_ptr(), row * t.shape[-3], row, dim)
@@ -197,7 +222,7 @@ def head_norm_rope(q, k, q_gain, k_gain, positions, frequencies, eps: float = 1e
                         q_gain, k_gain, positions, frequencies, eps, interleaved, out)
     if out is None:
         (qo, pqo), (ko, pko) = _new_heads(q), _new_heads(k)
-    api.q4nn_head_norm_rope(rope, pq, pk, pqo, pko, _raw(device))
+    api._check(api.load_library().q4nn_head_norm_rope(rope, pq, pk, pqo, pko, _raw(device)))
     return qo, ko
 
 
@@ -231,10 +256,12 @@ def head_norm_rope_backward(q, k, q_gain, k_gain, positions, frequencies, dq, dk
     if out is None:
         (qo, pqo), (ko, pko) = _new_heads(q), _new_heads(k)
     if gain_grads is None:
-        gq, gk = (torch.empty(q.shape[-1], dtype=dtype, device=device) for _ in range(2))
+        gq, gk = (torch.empty_like(t, dtype=dtype) for t in (q_gain, k_gain))
     need = api.q4nn_head_norm_rope_backward_workspace_bytes(rope)
-    api.q4nn_head_norm_rope_backward(rope, pq, pk, pdq, pdk, pqo, pko, gq.data_ptr(), gk.data_ptr(), _DTYPES[gq.dtype],
-                                     api.NN_ADD if accumulate else 0, _workspace(need, device), need, _raw(device))
+    ws, at = _room(q, need)
+    api._check(api.load_library().q4nn_head_norm_rope_backward(
+        rope, pq, pk, pdq, pdk, pqo, pko, gq.data_ptr(), gk.data_ptr(), _DTYPES[gq.dtype],
+        api.NN_ADD if accumulate else 0, at, need, _raw(device)))
     return qo, ko, gq, gk
 
 
@@ -266,11 +293,12 @@ def dropout(x, p: float, seed: int, step, layer: int, residual=None, offset: int
                         residual, offset, out)
     rows, cols = x.shape
     if out is None:
-        out, code, ldo = torch.empty_like(x, memory_format=torch.contiguous_format), _DTYPES[x.dtype], max(1, cols)
+        out, code, ldo = torch.empty_like(x, memory_format=_CONTIGUOUS), _DTYPES[x.dtype], max(1, cols)
     else:
         out, code, ldo = _result(out, (rows, cols), x.dtype, device)
     if on_gpu:
         at, step = step.data_ptr(), 0
-    api.q4nn_dropout(p, seed, step, at, layer, offset, x.data_ptr(), ldx, None if residual is None else
-                     residual.data_ptr(), ldr, rows, cols, out.data_ptr(), ldo, code, _raw(device))
+    api._check(api.load_library().q4nn_dropout(
+        p, seed, step, at, layer, offset, x.data_ptr(), ldx, None if residual is None else residual.data_ptr(), ldr, rows,
+        cols, out.data_ptr(), ldo, code, _raw(device)))
     return out
