@@ -63,7 +63,7 @@ constexpr int kSortTile = 1024, kMergeRuns = 16, kShort = 32, kSlab = 512;
 // longer: kHides bytes of zeros a tile, 1.5 us (8192 tokens into 151936 x 1024:
 // 70.6 us, with merges 75.0; into 1000 x 64, with 16384 tokens: 40.3 and 26.2).
 constexpr int64_t kRanked = 65536, kHides = 12 << 20;
-constexpr int kJoinCols = 256, kJoinPieces = 16, kJoinWaves = 8;
+constexpr int kJoinCols = 256, kJoinPieces = 8, kJoinWaves = 8;
 constexpr uint32_t kNone = 0x80000000u;   // above every id; one more is a number too
 
 __device__ __forceinline__ uint32_t id_of(uint64_t key) { return (uint32_t)(key >> 32); }
@@ -369,24 +369,28 @@ template <bool BF16, bool ADD, int COLS> __global__ __launch_bounds__(256) void 
     finish(end);
 }
 
-// The long rows that begin in one of 16 pieces: a wave adds every eighth of a
+// The long rows that begin in one of 8 pieces: a wave adds every eighth of a
 // row's sums, 4 columns to a lane, and the waves' sums are added in order.
 template <bool BF16, bool ADD> __global__ __launch_bounds__(64 * kJoinWaves) void k_grad_join(GradArgs a, int64_t col_groups) {
     __shared__ float4 lds[kJoinWaves][64];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t block = group_index(), pg = block / col_groups;
     const int64_t col = (block - pg * col_groups) * kJoinCols + lane * 4, left = a.cols - col;
-    const int64_t mine = pg * kJoinPieces + lane;
+    // of 64 pieces from the group's first on: the ids that they begin and end with (its long row's, if one begins there)
+    const int64_t mine = pg * kJoinPieces + lane, first = mine * a.piece, last = first + a.piece - 1;
     const uint32_t slot = lane < kJoinPieces && mine < a.pieces ? a.long_begins[mine] : 0;
+    const uint32_t begins = first < a.n ? id_of(a.keys[first]) : ~0u;
+    const uint32_t ends = id_of(a.keys[last < a.n ? last : a.n - 1]);
     uint64_t todo = __builtin_amdgcn_ballot_w64(slot != 0);
     while (todo) {
         const int which = __builtin_ctzll(todo);
         todo &= todo - 1;
         const int64_t piece = pg * kJoinPieces + which;
-        const uint32_t id = id_of(a.keys[piece * a.piece + a.piece - 1]);  // the last of its piece, which is full
+        const uint32_t id = (uint32_t)__builtin_amdgcn_readlane((int)ends, which);
         // the pieces behind it that begin with this row
-        int64_t more = 0;
-        for (;;) {
+        const uint64_t same = __builtin_amdgcn_ballot_w64(lane > which && begins == id);
+        int64_t more = __builtin_popcountll(same);
+        while (which + 1 + more >= 64) {
             const int64_t q = piece + 1 + more + lane;
             const uint64_t other = __builtin_amdgcn_ballot_w64(!(q < a.pieces && id_of(a.keys[q * a.piece]) == id));
             if (other) {
