@@ -56,6 +56,7 @@ __global__ __launch_bounds__(256) void k_embedding(Ids ids, Dense table, MxMat m
 //      piece's end where it has to; of a longer one every piece that it touches
 //      leaves an FP32 sum in the workspace;
 //   4. those are joined, in the order of the pieces.
+// Up to 1024 tokens take all of that in one launch (k_grad_small).
 // Keys are (id << 32) | position; a token that counts for no row has the id
 // kNone and lies behind all others.
 constexpr int kSortTile = 1024, kMergeRuns = 16, kShort = 32, kSlab = 512;
@@ -118,49 +119,70 @@ template <int LOG> __device__ __forceinline__ int place_in_four(const uint32_t* 
     return place;
 }
 
-// A wave ranks its 64 ids by comparing each with each (equal ones by their
-// position); four such runs, and then four of 256, become one by binary
-// searches in shared memory.  (A bitonic sort's 55 exchanges took 11.8 us, 15
-// searches of 64 at once 7.2.)
-//
-// RANKED: a tile finds its places among all tokens by itself.  It looks every
-// other tile's ids up in its own sorted ones and counts them there: what is
-// counted up to an element lies before it.  That takes 1.5 us for each of the
-// others (shared memory's rate), and saves the merges' launches.
+__device__ __forceinline__ uint32_t valid_id(const Ids& ids, int64_t rows, int64_t t) {
+    const int64_t v = t < ids.n ? load_id(ids, t) : -1;
+    return v >= 0 && v < rows ? (uint32_t)v : kNone;
+}
+
+// A tile of 1024 tokens, the ids of those past the last kNone, sorted by a
+// work-group: a thread's id, token and place.  A wave ranks its 64 ids by
+// comparing each with each (equal ones by their position); four such runs, and
+// then four of 256, become one by binary searches in shared memory.  (A bitonic
+// sort's 55 exchanges took 11.8 us, 15 searches of 64 at once 7.2, this 5.7.)
+struct SortRoom {
+    uint32_t id[2][kSortTile], token[2][kSortTile];
+};
+struct Sorted {
+    uint32_t id, token;
+    int place;
+};
+__device__ __forceinline__ Sorted sort_tile(const Ids& ids, int64_t rows, int64_t tile, SortRoom& room) {
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const uint32_t id = valid_id(ids, rows, tile * kSortTile + tid);
+    // waves, and groups of 256, that lie past the last token hold kNone alone and stay as they are
+    const bool wave_real = tile * kSortTile + (tid & ~63) < ids.n, group_real = tile * kSortTile + (tid & ~255) < ids.n;
+    int rank = lane;
+    if (wave_real) {
+        rank = 0;
+#pragma unroll
+        for (int j = 0; j < 64; ++j) {
+            const uint32_t other = (uint32_t)__builtin_amdgcn_readlane((int)id, j);
+            rank += other < id + (j < lane ? 1u : 0u) ? 1 : 0;
+        }
+    }
+    room.id[0][wave * 64 + rank] = id;
+    room.token[0][wave * 64 + rank] = (uint32_t)(tile * kSortTile + tid);
+    __syncthreads();
+    Sorted s = {room.id[0][tid], room.token[0][tid], tid};
+    if (group_real) s.place = (tid & ~255) + place_in_four<6>(room.id[0] + (tid & ~255), tid & 255, s.id);
+    if (ids.n > 256) {
+        room.id[1][s.place] = s.id;
+        room.token[1][s.place] = s.token;
+        __syncthreads();
+        s = {room.id[1][tid], room.token[1][tid], tid};
+        if (group_real) s.place = place_in_four<8>(room.id[1], tid, s.id);
+    }
+    return s;  // room.id[0] is free where there are more than 256 tokens
+}
+
+// RANKED (more than one tile): a tile finds its places among all tokens by
+// itself.  It looks every other tile's ids up in its own sorted ones and counts
+// them there: what is counted up to an element lies before it.  That takes 1.5
+// us for each of the others (shared memory's rate), and saves the merges'
+// launches.
 template <bool RANKED>
 __global__ __launch_bounds__(kSortTile) void k_sort_tiles(Ids ids, int64_t rows, uint64_t* keys, int64_t tiles,
                                                            Fill fill) {
-    __shared__ uint32_t run_id[2][kSortTile], run_token[2][kSortTile], counted[RANKED ? kSortTile + 1 : 1], of_wave[16];
+    __shared__ SortRoom room;
+    __shared__ uint32_t counted[RANKED ? kSortTile + 1 : 1], of_wave[16];
     const int64_t tile = group_index();
     if (tile >= tiles) return fill_zero<kSortTile>(fill, (tile - tiles) * (kSortTile * kFillRounds));
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const auto id_at = [&](int64_t t) {
-        const int64_t v = t < ids.n ? load_id(ids, t) : -1;
-        return v >= 0 && v < rows ? (uint32_t)v : kNone;
-    };
-    uint32_t id = id_at(tile * kSortTile + tid);
-    int rank = 0;
-#pragma unroll
-    for (int j = 0; j < 64; ++j) {
-        const uint32_t other = (uint32_t)__builtin_amdgcn_readlane((int)id, j);
-        rank += other < id + (j < lane ? 1u : 0u) ? 1 : 0;
-    }
-    run_id[0][wave * 64 + rank] = id;
-    run_token[0][wave * 64 + rank] = (uint32_t)(tile * kSortTile + tid);
-    __syncthreads();
-    id = run_id[0][tid];
-    uint32_t token = run_token[0][tid];
-    int place = (tid & ~255) + place_in_four<6>(run_id[0] + (tid & ~255), tid & 255, id);
-    if (ids.n > 256) {
-        run_id[1][place] = id;
-        run_token[1][place] = token;
-        __syncthreads();
-        id = run_id[1][tid], token = run_token[1][tid];
-        place = place_in_four<8>(run_id[1], tid, id);
-    }
+    const Sorted s = sort_tile(ids, rows, tile, room);
+    uint32_t* const sorted = room.id[0];
     int64_t before = tile * kSortTile;
     if (RANKED) {
-        run_id[0][place] = id;
+        sorted[s.place] = s.id;
         counted[tid] = 0;
         if (tid == 0) counted[kSortTile] = 0;
         __syncthreads();
@@ -171,16 +193,16 @@ __global__ __launch_bounds__(kSortTile) void k_sort_tiles(Ids ids, int64_t rows,
 #pragma unroll
             for (int k = 0; k < kAtOnce; ++k) {
                 // of equal ids, those of a tile before this one come first
-                below[k] = id_at((first + k) * kSortTile + tid) + (first + k < tile ? 0u : 1u);
+                below[k] = valid_id(ids, rows, (first + k) * kSortTile + tid) + (first + k < tile ? 0u : 1u);
                 at[k] = 0;
             }
             // side by side: a step of one waits for shared memory
 #pragma unroll
             for (int step = kSortTile / 2; step > 0; step /= 2)
 #pragma unroll
-                for (int k = 0; k < kAtOnce; ++k) at[k] += run_id[0][at[k] + step - 1] < below[k] ? step : 0;
+                for (int k = 0; k < kAtOnce; ++k) at[k] += sorted[at[k] + step - 1] < below[k] ? step : 0;
 #pragma unroll
-            for (int k = 0; k < kAtOnce; ++k) at[k] += run_id[0][at[k]] < below[k] ? 1 : 0;
+            for (int k = 0; k < kAtOnce; ++k) at[k] += sorted[at[k]] < below[k] ? 1 : 0;
 #pragma unroll
             for (int k = 0; k < kAtOnce; ++k)
                 if (first + k != tile && (first + k) * kSortTile + tid < ids.n) atomicAdd(&counted[at[k]], 1u);
@@ -198,10 +220,10 @@ __global__ __launch_bounds__(kSortTile) void k_sort_tiles(Ids ids, int64_t rows,
         for (int w = 0; w < wave; ++w) sum += (int)of_wave[w];
         counted[tid] = (uint32_t)sum;
         __syncthreads();
-        before = counted[place];
+        before = counted[s.place];
     }
     // past the last token: ids of kNone from the end of the last tile, the last of all
-    if (token < ids.n) keys[before + place] = (uint64_t)id << 32 | token;
+    if (s.token < ids.n) keys[before + s.place] = (uint64_t)s.id << 32 | s.token;
 }
 
 // Runs of `run` keys, the last one shorter: each kMergeRuns neighbours become
@@ -270,10 +292,80 @@ struct GradArgs {
 };
 
 // WHOLE: whole vectors of 8 columns, whose code is a third of the others'
-// (the loop below holds a row's end 16 times, and has to fit the instruction
+// (the walk below holds a row's end 16 times, and has to fit the instruction
 // cache).  RAGGED: a lane whose 8 columns pass the end takes the last 8, and
 // stores those that are its own.  NARROW: fewer than 8 columns.
 enum Columns { WHOLE, RAGGED, NARROW };
+
+// A lane's 8 columns of a slab.  Lanes past the columns go along on the first
+// ones and store nothing: all 64 of a wave hold a token that it reads.
+template <int COLS> struct LaneColumns {
+    int64_t at;    // the first
+    int skip;      // of the 8, that another lane stores
+    int64_t here;  // of the 8, that exist
+    bool whole;
+    __device__ __forceinline__ LaneColumns(int64_t cols, int64_t slab) {
+        const int lane = threadIdx.x & 63;
+        const int64_t col = slab * kSlab + lane * 8, left = cols - col;
+        at = COLS == NARROW ? 0 : left >= 8 ? col : left > 0 ? cols - 8 : 0;
+        skip = left >= 8 || COLS == NARROW ? 0 : left > 0 ? (int)(8 - left) : 8;
+        here = COLS == NARROW ? (lane == 0 ? cols : 0) : 8;
+        whole = skip == 0 && here == 8;
+    }
+};
+template <int COLS> __device__ __forceinline__ u32x4_any load_grad(const uint16_t* p, const LaneColumns<COLS>& c) {
+    if (COLS != NARROW) return __builtin_nontemporal_load(reinterpret_cast<const u32x4_any*>(p));
+    uint32_t w[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) w[k] = k < c.here ? p[k] : 0;
+    return u32x4_any{w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16};
+}
+__device__ __forceinline__ void add8(float* sum, const u32x4_any& raw) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        sum[2 * k] += bf16_value(raw[k] & 0xFFFFu);
+        sum[2 * k + 1] += __uint_as_float(raw[k] & 0xFFFF0000u);
+    }
+}
+template <bool BF16, bool ADD, int COLS>
+__device__ __forceinline__ void store_row(const GradArgs& a, uint32_t id, const LaneColumns<COLS>& c, const float* sum) {
+    if (c.whole) store_grad8<BF16, ADD>(a.grad, id * a.grad.ld + c.at, a.scale, sum);
+    else if (COLS != WHOLE) store_grad_some<BF16, ADD, 8>(a.grad, id * a.grad.ld + c.at, c.skip, c.here, a.scale, sum);
+}
+
+// The tokens of lanes from .. end - 1, by whole rows: row_end(id, first lane,
+// lane behind the last, sums) at each row's end.
+template <int COLS, class RowEnd>
+__device__ __forceinline__ void walk_tokens(const GradArgs& a, uint32_t id, uint32_t token, int from, int end,
+                                            const LaneColumns<COLS>& c, RowEnd row_end) {
+    constexpr int kBatch = 16;
+    float sum[8] = {};
+    uint32_t current = (uint32_t)__builtin_amdgcn_readlane((int)id, from);
+    int begun = from;
+    for (int i = from; i < end; i += kBatch) {
+        u32x4_any raw[kBatch];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            // past the end: the last token once more, not added
+            const int e = i + j < end ? i + j : end - 1;
+            raw[j] = load_grad<COLS>(a.dy + (int64_t)(uint32_t)__builtin_amdgcn_readlane((int)token, e) * a.lddy + c.at, c);
+        }
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            if (i + j >= end) break;
+            const uint32_t now = (uint32_t)__builtin_amdgcn_readlane((int)id, i + j);
+            if (now != current) {
+                row_end(current, begun, i + j, sum);
+                current = now, begun = i + j;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) sum[k] = 0.0f;
+            }
+            add8(sum, raw[j]);
+        }
+    }
+    row_end(current, begun, end, sum);
+}
+
 template <bool BF16, bool ADD, int COLS> __global__ __launch_bounds__(256) void k_grad_pieces(GradArgs a) {
     const int lane = threadIdx.x & 63;
     const int64_t unit = (int64_t)group_index() * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -306,67 +398,22 @@ template <bool BF16, bool ADD, int COLS> __global__ __launch_bounds__(256) void 
         if (slab == 0 && lane == 0) a.long_begins[piece] = 0;
         return;
     }
-    const int64_t col = slab * kSlab + lane * 8, left = a.cols - col;
-    // Lanes past the columns go along on the first ones and store nothing: all 64 hold a token that is read below.
-    const int64_t at = COLS == NARROW ? 0 : left >= 8 ? col : left > 0 ? a.cols - 8 : 0;
-    const int skip = left >= 8 || COLS == NARROW ? 0 : left > 0 ? (int)(8 - left) : 8;
-    const int64_t here = COLS == NARROW ? (lane == 0 ? a.cols : 0) : 8;  // of the 8 columns from `at` on
-    const bool whole = skip == 0 && here == 8;
-    float sum[8] = {};
-    uint32_t current = (uint32_t)__builtin_amdgcn_readlane((int)id, from);
-    int begun = from;
-    auto finish = [&](int to) {
+    const LaneColumns<COLS> c(a.cols, slab);
+    walk_tokens<COLS>(a, id, token, from, end, c, [&](uint32_t row, int begun, int to, const float* sum) {
         if ((begun == 0 && first_long) || (to == end && last_long)) {
-            float* p = a.part + (piece * 2 + (begun == 0 ? 0 : 1)) * a.part_ld + at;
-            if (whole) {
+            float* p = a.part + (piece * 2 + (begun == 0 ? 0 : 1)) * a.part_ld + c.at;
+            if (c.whole) {
                 *reinterpret_cast<float4*>(p) = make_float4(sum[0], sum[1], sum[2], sum[3]);
                 *reinterpret_cast<float4*>(p + 4) = make_float4(sum[4], sum[5], sum[6], sum[7]);
             } else if (COLS != WHOLE) {
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
-                    if (k >= skip && k < here) p[k] = sum[k];
+                    if (k >= c.skip && k < c.here) p[k] = sum[k];
             }
-        } else if (whole) {
-            store_grad8<BF16, ADD>(a.grad, current * a.grad.ld + at, a.scale, sum);
-        } else if (COLS != WHOLE) {
-            store_grad_some<BF16, ADD, 8>(a.grad, current * a.grad.ld + at, skip, here, a.scale, sum);
+        } else {
+            store_row<BF16, ADD, COLS>(a, row, c, sum);
         }
-    };
-    constexpr int kBatch = 16;
-    for (int i = from; i < end; i += kBatch) {
-        u32x4_any raw[kBatch];
-#pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-            // past the end: the last token once more, not added
-            const int e = i + j < end ? i + j : end - 1;
-            const uint16_t* p = a.dy + (int64_t)(uint32_t)__builtin_amdgcn_readlane((int)token, e) * a.lddy + at;
-            if (COLS != NARROW) {
-                raw[j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_any*>(p));
-            } else {
-                uint32_t w[8];
-#pragma unroll
-                for (int k = 0; k < 8; ++k) w[k] = k < here ? p[k] : 0;
-                raw[j] = u32x4_any{w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16};
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-            if (i + j >= end) break;
-            const uint32_t now = (uint32_t)__builtin_amdgcn_readlane((int)id, i + j);
-            if (now != current) {
-                finish(i + j);
-                current = now, begun = i + j;
-#pragma unroll
-                for (int k = 0; k < 8; ++k) sum[k] = 0.0f;
-            }
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                sum[2 * k] += bf16_value(raw[j][k] & 0xFFFFu);
-                sum[2 * k + 1] += __uint_as_float(raw[j][k] & 0xFFFF0000u);
-            }
-        }
-    }
-    finish(end);
+    });
 }
 
 // The long rows that begin in one of 8 pieces: a wave adds every eighth of a
@@ -424,6 +471,117 @@ template <bool BF16, bool ADD> __global__ __launch_bounds__(64 * kJoinWaves) voi
     }
 }
 
+// Up to 1024 tokens in one launch: every work-group sorts them all for itself.
+// The first ones then sum: a wave the short rows that begin in two sorted
+// tokens, and all 16 together the long row that begins in the work-group's 32,
+// if one does (it passes their end, so there is at most one).  All of them fill
+// their share of the rows that no token reads.
+constexpr int kSmallPiece = 2, kSegment = 16 * kSmallPiece;
+static_assert(kSegment <= kShort, "two long rows could begin in one segment");
+struct SmallArgs {
+    Ids ids;
+    int64_t rows, row_bytes, pitch, sum_groups;
+    uint32_t row_pieces;  // 16 bytes each, the last one shorter
+    int group_rows;       // rows of a work-group to fill, at most kSortTile
+};
+template <bool BF16, bool ADD, int COLS> __global__ __launch_bounds__(kSortTile) void k_grad_small(SmallArgs m, GradArgs a) {
+    __shared__ SortRoom room;
+    __shared__ uint32_t id_at[kSortTile], token_at[kSortTile];
+    __shared__ float4 lds[16][64][2];
+    __shared__ int long_begin;
+    __shared__ bool touched[kSortTile];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int64_t group = group_index();
+    {
+        const Sorted s = sort_tile(m.ids, m.rows, 0, room);
+        id_at[s.place] = s.id, token_at[s.place] = s.token;
+    }
+    if (tid == 0) long_begin = -1;
+    __syncthreads();
+    if (group < m.sum_groups) {
+        const int64_t segment = group / a.slabs, slab = group - segment * a.slabs;
+        const LaneColumns<COLS> c(a.cols, slab);
+        const int begin = (int)segment * kSegment + wave * kSmallPiece, at = begin + lane, ahead_of = begin - kShort + lane;
+        const uint32_t id = at < kSortTile ? id_at[at] : ~0u, token = at < kSortTile ? token_at[at] : 0u;
+        const uint32_t before = lane < kShort && ahead_of >= 0 ? id_at[ahead_of] : ~0u;
+        const int real = __builtin_popcountll(__builtin_amdgcn_ballot_w64(id < kNone));
+        const int count = real < kSmallPiece ? real : kSmallPiece;
+        int from = 0, end = 0;
+        if (count > 0) {
+            const uint32_t first = (uint32_t)__builtin_amdgcn_readlane((int)id, 0);
+            const bool begun = __builtin_amdgcn_ballot_w64(before == first) != 0;
+            from = begun ? __builtin_popcountll(__builtin_amdgcn_ballot_w64(id == first)) : 0;
+        }
+        if (from < count) {
+            const uint32_t last = (uint32_t)__builtin_amdgcn_readlane((int)id, count - 1);
+            const uint64_t mask = __builtin_amdgcn_ballot_w64(id == last);
+            const int start = __builtin_ctzll(mask), length = __builtin_popcountll(mask);
+            end = length > kShort ? start : start + length;
+            if (length > kShort && lane == 0) long_begin = begin + start;
+            if (from < end)
+                walk_tokens<COLS>(a, id, token, from, end, c, [&](uint32_t row, int, int, const float* sum) {
+                    store_row<BF16, ADD, COLS>(a, row, c, sum);
+                });
+        }
+        __syncthreads();
+        const int first = long_begin;
+        if (first >= 0) {
+            const uint32_t row = id_at[first];
+            const int stop = count_below<10>(id_at, row + 1);
+            float sum[8] = {};
+            constexpr int kBatch = 8;
+            for (int i = first + wave; i < stop; i += 16 * kBatch) {
+                u32x4_any raw[kBatch];
+#pragma unroll
+                for (int j = 0; j < kBatch; ++j) {
+                    const int e = i + 16 * j < stop ? i + 16 * j : i;
+                    raw[j] = load_grad<COLS>(a.dy + (int64_t)token_at[e] * a.lddy + c.at, c);
+                }
+#pragma unroll
+                for (int j = 0; j < kBatch; ++j)
+                    if (i + 16 * j < stop) add8(sum, raw[j]);
+            }
+            lds[wave][lane][0] = make_float4(sum[0], sum[1], sum[2], sum[3]);
+            lds[wave][lane][1] = make_float4(sum[4], sum[5], sum[6], sum[7]);
+            __syncthreads();
+            if (wave == 0) {
+#pragma unroll
+                for (int w = 1; w < 16; ++w) {
+                    const float4 u = lds[w][lane][0], v = lds[w][lane][1];
+                    sum[0] += u.x, sum[1] += u.y, sum[2] += u.z, sum[3] += u.w;
+                    sum[4] += v.x, sum[5] += v.y, sum[6] += v.z, sum[7] += v.w;
+                }
+                store_row<BF16, ADD, COLS>(a, row, c, sum);
+            }
+        }
+    }
+    if (ADD) return;
+    const int64_t first_row = group * m.group_rows;
+    if (first_row >= m.rows) return;
+    const int n_rows = (int)(m.rows - first_row < m.group_rows ? m.rows - first_row : m.group_rows);
+    if (tid < n_rows) {
+        const uint32_t row = (uint32_t)(first_row + tid);
+        const int place = count_below<10>(id_at, row);
+        touched[tid] = place < kSortTile && id_at[place] == row;
+    }
+    __syncthreads();
+    const uint32_t step_rows = kSortTile / m.row_pieces, step_pieces = kSortTile - step_rows * m.row_pieces;
+    uint32_t row = tid / m.row_pieces, piece = tid - row * m.row_pieces;
+    while (row < (uint32_t)n_rows) {
+        if (!touched[row]) {
+            char* p = static_cast<char*>(a.grad.p) + (first_row + row) * m.pitch + (int64_t)piece * 16;
+            const int64_t size = m.row_bytes - (int64_t)piece * 16;
+            if (size >= 16) {
+                *reinterpret_cast<u32x4_any*>(p) = u32x4_any{0, 0, 0, 0};
+            } else {
+                for (int64_t k = 0; k < size; k += 2) *reinterpret_cast<uint16_t*>(p + k) = 0;
+            }
+        }
+        row += step_rows, piece += step_pieces;
+        if (piece >= m.row_pieces) piece -= m.row_pieces, ++row;
+    }
+}
+
 size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
 int64_t parts_of(int64_t n, int64_t part) { return (n + part - 1) / part; }
 
@@ -436,6 +594,15 @@ template <bool BF16, bool ADD> void launch_sums(const GradArgs& a, hipStream_t s
         const int64_t cg = parts_of(a.cols, kJoinCols);
         k_grad_join<BF16, ADD><<<grid_of(parts_of(a.pieces, kJoinPieces) * cg), dim3(64 * kJoinWaves), 0, st>>>(a, cg);
     }
+}
+
+template <bool BF16, bool ADD> void launch_small(SmallArgs m, const GradArgs& a, hipStream_t st) {
+    m.sum_groups = parts_of(a.n, kSegment) * a.slabs;
+    const int64_t fill = ADD ? 0 : parts_of(m.rows, m.group_rows);
+    const dim3 g = grid_of(fill > m.sum_groups ? fill : m.sum_groups, kSortTile), b(kSortTile);
+    if (a.cols < 8) k_grad_small<BF16, ADD, NARROW><<<g, b, 0, st>>>(m, a);
+    else if (a.cols % 8 != 0) k_grad_small<BF16, ADD, RAGGED><<<g, b, 0, st>>>(m, a);
+    else k_grad_small<BF16, ADD, WHOLE><<<g, b, 0, st>>>(m, a);
 }
 
 }  // namespace
@@ -487,16 +654,45 @@ size_t embedding_grad_workspace(int64_t tokens, int64_t cols) {
     return tokens == 0 ? 0 : 2 * w.keys + w.flags + w.part;
 }
 
+// The form in one launch (k_grad_small): while its work-groups, one to a compute
+// unit, run at once, and the zeros are few enough to wait for the sort in each
+// of them.  Microseconds of a call, outside of a graph, and of the other form:
+// 301 tokens x 100 into 1000 rows 10.1, 14.4; 1024 x 4096 into 500 13.8, 16.4;
+// 1024 x 5120 18.9, 17.8; x 16384 39, 22; 1000 x 1024 into 4000 13.5, 15.6; in a
+// graph 1000 x 256 into 32000 (16 MB) 20.0, 15.8.
+constexpr int64_t kSmallGroups = 256, kSmallFill = 8 << 20, kSmallGroupFill = 32 << 10;
+bool small(int64_t tokens, int64_t cols, int64_t fill_bytes) {
+    return tokens > 0 && tokens <= kSortTile && fill_bytes <= kSmallFill &&
+           parts_of(tokens, kSegment) * parts_of(cols, kSlab) <= kSmallGroups;
+}
+
 hipError_t launch_embedding_grad(const Ids& ids, const Dense& dy, float scale, int64_t rows, int64_t cols,
                                  const Dense& grad, bool add, void* ws, hipStream_t st) {
     const int64_t n = ids.n, tiles = parts_of(n, kSortTile);
+    const int64_t unit = grad.dtype == Q4MX_BF16 ? 2 : 4, row_bytes = cols * unit;
+    const bool bf = grad.dtype == Q4MX_BF16;
+    GradArgs a = {};
+    a.n = n, a.slabs = parts_of(cols, kSlab);
+    a.dy = static_cast<const uint16_t*>(dy.p), a.lddy = dy.ld;
+    a.cols = cols, a.scale = scale, a.grad = grad;
+    if (small(n, cols, add ? 0 : rows * row_bytes)) {
+        SmallArgs m = {};
+        m.ids = ids, m.rows = rows, m.row_bytes = row_bytes, m.pitch = grad.ld * unit;
+        m.row_pieces = (uint32_t)parts_of(row_bytes, 16);
+        const int64_t most = kSmallGroupFill / row_bytes;
+        m.group_rows = most < 1 ? 1 : most > kSortTile ? kSortTile : (int)most;
+        if (bf && add) launch_small<true, true>(m, a, st);
+        else if (bf) launch_small<true, false>(m, a, st);
+        else if (add) launch_small<false, true>(m, a, st);
+        else launch_small<false, false>(m, a, st);
+        return hipGetLastError();
+    }
     Fill fill = {};
     fill.row_pieces = 1;
     if (!add) {
-        const int64_t unit = grad.dtype == Q4MX_BF16 ? 2 : 4;
         const bool flat = grad.ld == cols || rows == 1;
         fill.p = static_cast<char*>(grad.p);
-        fill.row_bytes = (flat ? rows * cols : cols) * unit;
+        fill.row_bytes = flat ? rows * row_bytes : row_bytes;
         fill.pitch = flat ? 0 : grad.ld * unit;
         fill.row_pieces = parts_of(fill.row_bytes, 16);
         fill.end = (flat ? 1 : rows) * fill.row_pieces;
@@ -509,7 +705,6 @@ hipError_t launch_embedding_grad(const Ids& ids, const Dense& dy, float scale, i
     if (ranked) k_sort_tiles<true><<<g, b, 0, st>>>(ids, rows, keys, tiles, fill);
     else k_sort_tiles<false><<<g, b, 0, st>>>(ids, rows, keys, tiles, fill);
     if (n == 0) return hipGetLastError();
-    GradArgs a = {};
     a.long_begins = reinterpret_cast<uint32_t*>(p + 2 * w.keys);
     a.part = reinterpret_cast<float*>(p + 2 * w.keys + w.flags);
     for (int64_t run = kSortTile; run < n && !ranked; run *= kMergeRuns) {
@@ -517,11 +712,7 @@ hipError_t launch_embedding_grad(const Ids& ids, const Dense& dy, float scale, i
         uint64_t* t = keys;
         keys = other, other = t;
     }
-    a.keys = keys, a.n = n, a.piece = piece_of(n, cols), a.pieces = parts_of(n, a.piece), a.slabs = parts_of(cols, kSlab);
-    a.dy = static_cast<const uint16_t*>(dy.p), a.lddy = dy.ld;
-    a.cols = cols, a.part_ld = parts_of(cols, 8) * 8;
-    a.scale = scale, a.grad = grad;
-    const bool bf = grad.dtype == Q4MX_BF16;
+    a.keys = keys, a.piece = piece_of(n, cols), a.pieces = parts_of(n, a.piece), a.part_ld = parts_of(cols, 8) * 8;
     if (bf && add) launch_sums<true, true>(a, st);
     else if (bf) launch_sums<true, false>(a, st);
     else if (add) launch_sums<false, true>(a, st);

@@ -717,3 +717,45 @@ def test_embedding_grad_of_large_tables(tokens, rows, cols, how):
     _close(got[seen], want, (n[:, None] + 3) * S24 * mag, BF)
     got[seen] = 0
     assert float(got.abs().amax()) == 0
+
+
+# ---- more than a tile's tokens, and few tokens of many columns: not the form in one launch ------
+
+@pytest.mark.parametrize("cols", [1, 2, 7, 8, 9, 255, 256, 257, 511, 512, 513, 1030])
+def test_embedding_grad_of_many_tokens_by_columns(cols):
+    for how in ("text", "same", "padded"):
+        ids, dy = _drawn(how, 1500, 40, 6), _normal(1500, cols, seed=7)
+        _check_grad(ids, dy, 40, 1.0, BF)
+        start = _normal(40, cols, seed=8)
+        _check_grad(ids, dy, 40, 0.5, BF, start, out=start.to(DEV), accumulate=True)
+
+
+@pytest.mark.parametrize("tokens", [1, 33, 40, 300, 1024])
+@pytest.mark.parametrize("how", ["same", "text", "padded"])
+def test_embedding_grad_of_wide_rows(tokens, how):
+    ids, dy = _drawn(how, tokens, 30, 6), _normal(tokens, 8200, seed=7)
+    _check_grad(ids, dy, 30, 1.0, BF)
+    start = _normal(30, 8200, seed=8)
+    _check_grad(ids, dy, 30, 0.5, BF, start, out=start.to(DEV), accumulate=True)
+
+
+@pytest.mark.parametrize("gap,shift", [(1, 0), (3, 1), (8, 8)])
+@pytest.mark.parametrize("cols", [5, 96, 101])
+def test_embedding_grad_of_many_tokens_between_strided_rows(cols, gap, shift):
+    ids = _drawn("text", 3000, 900, 8)
+    dy, _ = _strided(_normal(3000, cols, seed=9), gap, shift)
+    for add, dtype in ((False, BF), (True, BF), (False, F32), (True, F32)):
+        out, buf = _strided(torch.ones(900, cols, dtype=dtype), gap, shift)
+        _check_grad(ids, dy, 900, 1.0, dtype, torch.ones(900, cols) if add else None, out=out, accumulate=add)
+        assert _untouched(out, buf)
+
+
+@pytest.mark.parametrize("lengths", [(33, 33, 33), (32, 1, 31, 64, 1, 33), (1, 1000, 23), (40, 60, 80, 100, 5, 5, 5, 500), (31, 34, 2, 200, 32)])
+def test_embedding_grad_of_rows_around_the_lengths_that_are_split(lengths):
+    ids = torch.cat([torch.full((n,), 3 * i + 1) for i, n in enumerate(lengths)])
+    for tokens in (len(ids), 2200):   # either form: padding behind
+        padded = torch.cat((ids, torch.full((tokens - len(ids),), -1)))[torch.randperm(tokens, generator=_gen(9))]
+        dy = _normal(tokens, 72, seed=10)
+        _check_grad(padded, dy, 40, 1.0, F32)
+        start = _normal(40, 72, seed=11)
+        _check_grad(padded, dy, 40, 1.0, BF, start, out=start.to(DEV), accumulate=True)
