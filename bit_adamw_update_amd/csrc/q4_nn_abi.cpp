@@ -80,7 +80,7 @@ bool shifted(const q4nn_heads* a, const q4nn_heads* b, const q4nn_rope* r) {
            ((r->batches > 1 && a->batch != b->batch) || (r->tokens > 1 && a->token != b->token) || a->head != b->head);
 }
 
-// Whether q's and k's results begin in one place.
+// Whether an operand of q and one of k begin in one place.
 bool one_place(const q4nn_heads* q, const q4nn_heads* k, const q4nn_rope* r) {
     return q->p == k->p && r->batches * r->tokens > 0 && r->q_heads > 0 && r->k_heads > 0;
 }
@@ -185,6 +185,8 @@ q4_status q4nn_head_norm_rope(const q4nn_rope* r, const q4nn_heads* q, const q4n
     if (shifted(q_out, q, r) || shifted(k_out, k, r))
         return bad(Q4_ERR_SHAPE, "an output in place of its input must have its strides");
     if (one_place(q_out, k_out, r)) return bad(Q4_ERR_CONFLICT, "q_out and k_out are one buffer");
+    if (one_place(q_out, k, r) || one_place(q, k_out, r))
+        return bad(Q4_ERR_CONFLICT, "an output is in the place of the other tensor's input");
     if (empty(r)) return ok();
     Q4_TRY(device());
     return launched(launch_head_norm_rope(*r, *q, *k, *q_out, *k_out, reinterpret_cast<hipStream_t>(stream)),
@@ -214,6 +216,8 @@ q4_status q4nn_head_norm_rope_backward(const q4nn_rope* r, const q4nn_heads* q, 
     if (shifted(dq_in, dq, r) || shifted(dk_in, dk, r))
         return bad(Q4_ERR_SHAPE, "a gradient in place of the result's must have its strides");
     if (one_place(dq_in, dk_in, r)) return bad(Q4_ERR_CONFLICT, "dq_in and dk_in are one buffer");
+    if (one_place(dq_in, dk, r) || one_place(dq, dk_in, r) || one_place(dq_in, k, r) || one_place(q, dk_in, r))
+        return bad(Q4_ERR_CONFLICT, "a gradient is in the place of the other tensor's operand");
     Q4_TRY(check_dense("dq_gain", dq_gain, dtype, 1, r->dim, r->dim));
     Q4_TRY(check_dense("dk_gain", dk_gain, dtype, 1, r->dim, r->dim));
     if (dq_gain == dk_gain) return bad(Q4_ERR_CONFLICT, "dq_gain and dk_gain are one buffer: add them up afterwards");

@@ -139,6 +139,11 @@ def test_head_operands_are_checked():
     refused(CONFLICT, "one buffer", back, gk=P)
     refused(CONFLICT, "one buffer", back, dki=view(2, p=4 * P))
     refused(CONFLICT, "one buffer", heads, ko=view(2, p=2 * P))
+    refused(CONFLICT, "the other", heads, k=view(2, p=2 * P))
+    refused(CONFLICT, "the other", heads, ko=view(2, p=P))
+    refused(CONFLICT, "the other", back, dqi=view(4, p=3 * P))
+    refused(CONFLICT, "the other", back, dki=view(2, p=2 * P))
+    refused(CONFLICT, "the other", back, dki=view(2, p=P))
     refused(INVALID, "dtype", back, dtype=3)
     refused(ALIGNMENT, "dk_gain", back, gk=P + 1)
     refused(SHAPE, "overlap", back, dki=view(2, p=5 * P, head=0))
