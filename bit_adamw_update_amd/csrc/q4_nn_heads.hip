@@ -2,8 +2,10 @@
 // rotation by position, in one pass, and its gradients (gfx950).
 //
 // A row is one head of one token: dim elements, consecutive.  Memory bounds
-// both directions (4 bytes an element forward, 6 backward), so a row is read
-// once, held in registers by a few lanes, and written once: its sums are
+// both directions, 4 bytes an element forward, 6 backward (8192 tokens x 24 heads
+// of 128: 21 us, 101 MB at 4.8 TB/s, and 31 us, 151 MB at 4.9, with 4 us for the
+// gains' gradients; 16001 x 64 heads of 80 forward: 66 us, 328 MB at 5.0).  So a
+// row is read once, held in registers by a few lanes, and written once: its sums are
 // exchanged between those lanes without shared memory.  The unit of work is a
 // pair of elements that turn together; a lane takes VEC neighbouring pairs in
 // two vectors (the halves' (i, i + rotary/2), or 2 VEC neighbours when pairs
