@@ -47,13 +47,26 @@ struct HeadsArgs {
 
 // Cosine and sine of `a` radians.  FP64 brings the angle to a quarter turn and
 // its remainder within +-1/8 turn, which FP32 holds to half a step; there the
-// Taylor polynomials to x^9 and x^10 are off by less than 2^-29.
+// Taylor polynomials to x^9 and x^10 are off by less than 2^-29.  From 2^40 on
+// the number of quarters is itself rounded, more than half a quarter from 2^52
+// on, so the remainder is reduced once more: 2^72 quarters leave up to 2^20, and
+// pi/2 in two parts, off by 2^-109, still gives them to 2^-33.  That holds every
+// 64-bit position at frequencies up to 2^9; from 2^72 on the angle is NaN.
 __device__ __forceinline__ float2 cos_sin(double a) {
-    const double quarters = a * 0.63661977236758134308;  // 2 / pi
-    const double q = __builtin_rint(quarters);
+    constexpr double kQuarters = 0.63661977236758134308;  // 2 / pi
+    const double q = __builtin_rint(a * kQuarters);
     // the remainder in radians: a multiply-add keeps what the product alone loses of a far angle
-    const double r = __builtin_fma(q, -1.57079632679489661923, a);
-    const float x = (float)__builtin_fma(q, -6.123233995736766036e-17, r), z = x * x;
+    const auto less = [](double x, double quarters) {
+        return __builtin_fma(quarters, -6.123233995736766036e-17, __builtin_fma(quarters, -1.57079632679489661923, x));
+    };
+    double r = less(a, q);
+    int n = (int)(q - 4.0 * __builtin_floor(q * 0.25));  // q mod 4
+    if (__builtin_fabs(a) >= 0x1p40) {
+        const double more = __builtin_rint(r * kQuarters);
+        r = __builtin_fabs(a) < 0x1p72 ? less(r, more) : __builtin_nan("");
+        n = (n + (int)more) & 3;
+    }
+    const float x = (float)r, z = x * x;
     float s = __builtin_fmaf(z, 2.7557319e-6f, -1.9841270e-4f);
     s = __builtin_fmaf(z, s, 8.3333333e-3f);
     s = __builtin_fmaf(z, s, -0.16666667f);
@@ -63,7 +76,6 @@ __device__ __forceinline__ float2 cos_sin(double a) {
     c = __builtin_fmaf(z, c, 4.1666667e-2f);
     c = __builtin_fmaf(z, c, -0.5f);
     c = __builtin_fmaf(z, c, 1.0f);
-    const int n = (int)(q - 4.0 * __builtin_floor(q * 0.25));  // q mod 4
     const float cc = (n & 1) ? s : c, ss = (n & 1) ? c : s;
     return make_float2((n == 1 || n == 2) ? -cc : cc, n >= 2 ? -ss : ss);
 }

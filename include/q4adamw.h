@@ -525,8 +525,10 @@ typedef struct {
  * `rotary` elements of y turned by position: pair i is (y_a, y_b) <-
  * (y_a c - y_b s, y_b c + y_a s), c and s the cosine and sine of position *
  * frequencies[i], where (a, b) = (i, i + rotary/2), or (2i, 2i + 1) with
- * `interleaved`.  Angles are formed and reduced in FP64, the rest is FP32
- * (squares too: a mean past its range normalizes to 0), one rounding. */
+ * `interleaved`.  Angles are formed and reduced in FP64 (any 64-bit position's,
+ * as one product: from 2^72 on, which takes a frequency of 2^9, an angle gives
+ * NaN), the rest is FP32 (squares too: a mean past its range normalizes to 0),
+ * one rounding. */
 typedef struct {
     int64_t batches, tokens;   /* per batch; batches * tokens < 2^31 */
     int32_t q_heads, k_heads;  /* each in [0, 4096] */
