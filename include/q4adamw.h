@@ -507,8 +507,8 @@ q4_status q4nn_embedding_mx(const void* ids, int32_t id_type, int64_t tokens, co
  * of it (0 where no token read it; with Q4NN_ADD such rows are not touched).
  * Tokens outside [0, rows) count for no row.  The tokens are sorted by id and
  * position; a row's gradients are summed in FP32 in an order that follows from
- * the sorted ids and the sizes.  A tensor's BF16 gradient (q4_tensor.grad) is a
- * grad of dtype Q4MX_BF16. */
+ * the sorted ids and the sizes.  grad in the place of dy is refused.  A tensor's
+ * BF16 gradient (q4_tensor.grad) is a grad of dtype Q4MX_BF16. */
 q4_status q4nn_embedding_grad(const void* ids, int32_t id_type, int64_t tokens, const uint16_t* dy, int64_t lddy,
                               float scale, int64_t rows, int64_t cols, void* grad, int32_t dtype, int64_t ldg,
                               int32_t flags, void* ws, size_t ws_bytes, void* stream);

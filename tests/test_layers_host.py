@@ -80,6 +80,16 @@ def test_gradients_of_tables_are_checked():
     assert api.q4nn_embedding_grad_workspace_bytes(5, 0, 5) == 0
 
 
+def test_a_tables_gradient_in_the_place_of_its_operand():
+    # zeros are written before dy is summed, and a row's sum before another row's dy is read
+    for rows, flags in ((40, 0), (40, api.NN_ADD), (100, 0), (7, 0)):
+        refused(CONFLICT, "in the place of dy", grad, rows=rows, out=P, dy=P, flags=flags)
+    # that comes before the workspace, and not where dy has nothing to read
+    refused(WORKSPACE, "NULL", grad, out=2 * P, ws=None)
+    grad(rows=0, out=P, dy=P)
+    grad(tokens=0, out=P, dy=P, flags=api.NN_ADD)
+
+
 def rope(**k):
     d = dict(batches=2, tokens=5, q_heads=4, k_heads=2, dim=64, rotary=64, interleaved=0, gain_dtype=0,
              position_type=1, eps=1e-6, q_gain=P, k_gain=P, positions=P, position_batch=5, position_token=1,
