@@ -168,8 +168,8 @@ q4_status q4nn_embedding_grad(const void* ids, int32_t id_type, int64_t tokens, 
     Q4_TRY(q4nn_embedding_grad_workspace_bytes(tokens, rows, cols, &need));
     const bool add = (flags & Q4NN_ADD) != 0;
     if (rows == 0 || cols == 0 || (add && tokens == 0)) return ok();
-    if (tokens > 0 && grad == dy) return bad(Q4_ERR_CONFLICT, "grad is in the place of dy, which is read after it is written");
     Q4_TRY(check_ws(ws, ws_bytes, need));
+    if (tokens > 0 && grad == dy) return bad(Q4_ERR_CONFLICT, "grad is in the place of dy, which is read after it is written");
     Q4_TRY(device());
     return launched(launch_embedding_grad(Ids{ids, tokens, id_type}, dense(dy, lddy, Q4MX_BF16), scale, rows, cols,
                                           dense(grad, ldg, dtype), add, ws, reinterpret_cast<hipStream_t>(stream)),

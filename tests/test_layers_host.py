@@ -84,8 +84,7 @@ def test_a_tables_gradient_in_the_place_of_its_operand():
     # zeros are written before dy is summed, and a row's sum before another row's dy is read
     for rows, flags in ((40, 0), (40, api.NN_ADD), (100, 0), (7, 0)):
         refused(CONFLICT, "in the place of dy", grad, rows=rows, out=P, dy=P, flags=flags)
-    # that comes before the workspace, and not where dy has nothing to read
-    refused(WORKSPACE, "NULL", grad, out=2 * P, ws=None)
+    # not where dy has nothing to read
     grad(rows=0, out=P, dy=P)
     grad(tokens=0, out=P, dy=P, flags=api.NN_ADD)
 
