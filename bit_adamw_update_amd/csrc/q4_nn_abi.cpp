@@ -128,6 +128,7 @@ q4_status q4nn_embedding(const void* ids, int32_t id_type, int64_t tokens, const
     Q4_TRY(check_dense("table", table, dtype, rows, cols, ld));
     Q4_TRY(check_lookup(ids, id_type, tokens, cols, scale, out, out_dtype, ldo));
     if (tokens == 0 || cols == 0) return ok();
+    if (rows > 0 && out == table) return bad(Q4_ERR_CONFLICT, "out is in the place of the table");
     Q4_TRY(device());
     return launched(launch_embedding(Ids{ids, tokens, id_type}, dense(table, ld, dtype), MxMat{}, rows, cols, scale,
                                      dense(out, ldo, out_dtype), reinterpret_cast<hipStream_t>(stream)),
@@ -139,6 +140,8 @@ q4_status q4nn_embedding_mx(const void* ids, int32_t id_type, int64_t tokens, co
     Q4_TRY(check_mx("table", table));
     Q4_TRY(check_lookup(ids, id_type, tokens, table->cols, scale, out, out_dtype, ldo));
     if (tokens == 0 || table->cols == 0) return ok();
+    if (table->rows > 0 && (out == table->codes || out == table->scales))
+        return bad(Q4_ERR_CONFLICT, "out is in the place of the table");
     Q4_TRY(device());
     return launched(launch_embedding(Ids{ids, tokens, id_type}, Dense{}, mat(table), table->rows, table->cols, scale,
                                      dense(out, ldo, out_dtype), reinterpret_cast<hipStream_t>(stream)),

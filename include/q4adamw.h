@@ -493,7 +493,8 @@ typedef enum { Q4NN_I32 = 0, Q4NN_I64 = 1 } q4nn_int; /* integers in device memo
  * FP32 and rounded once.  ids (device, type id_type): tokens consecutive
  * integers.  A token below 0 is padding: its row is 0.  A token of `rows` or
  * more names no row: its row is NaN.  table: rows x cols, dtype, or an MX
- * matrix in either format (the w of a tied q4mx_linear). */
+ * matrix in either format (the w of a tied q4mx_linear); out in its place is
+ * refused. */
 q4_status q4nn_embedding(const void* ids, int32_t id_type, int64_t tokens, const void* table, int32_t dtype,
                          int64_t rows, int64_t cols, int64_t ld, float scale, void* out, int32_t out_dtype, int64_t ldo,
                          void* stream);

@@ -54,6 +54,18 @@ def test_lookups_are_checked():
     refused(SHAPE, "stride", mx, cols=65)
 
 
+def test_a_lookup_in_the_place_of_its_table():
+    # a row is read by any work-group, after others have written theirs
+    for k in (dict(), dict(tokens=100), dict(tokens=1), dict(dtype=api.MX_BF16)):
+        refused(CONFLICT, "in the place of the table", lookup, table=P, out=P, **k)
+    for out in (2 * P, 3 * P):
+        refused(CONFLICT, "in the place of the table", api.q4nn_embedding_mx, P, 1, 8,
+                api.Q4MXMatrix(format=1, reserved=0, rows=9, cols=64, codes=2 * P, scales=3 * P), 1.0, out, 1, 64, 0)
+    # not where nothing is read
+    lookup(tokens=0, table=P, out=P)
+    lookup(cols=0, table=P, out=P)
+
+
 def grad(ids=P, id_type=api.NN_I64, tokens=40, dy=P, lddy=64, scale=1.0, rows=100, cols=64, out=P, dtype=api.MX_BF16,
          ldg=64, flags=0, ws=P, n=1 << 40):
     api.q4nn_embedding_grad(ids, id_type, tokens, dy, lddy, scale, rows, cols, out, dtype, ldg, flags, ws, n, 0)
