@@ -217,8 +217,8 @@ q4_status q4nn_head_norm_rope_backward(const q4nn_rope* r, const q4nn_heads* q, 
     Q4_TRY(check_heads("dk", dk, r, r->k_heads, false));
     Q4_TRY(check_heads("dq_in", dq_in, r, r->q_heads, true));
     Q4_TRY(check_heads("dk_in", dk_in, r, r->k_heads, true));
-    if (shifted(dq_in, dq, r) || shifted(dk_in, dk, r))
-        return bad(Q4_ERR_SHAPE, "a gradient in place of the result's must have its strides");
+    if (shifted(dq_in, dq, r) || shifted(dk_in, dk, r) || shifted(dq_in, q, r) || shifted(dk_in, k, r))
+        return bad(Q4_ERR_SHAPE, "a gradient in place of the result's or of the input must have its strides");
     if (one_place(dq_in, dk_in, r)) return bad(Q4_ERR_CONFLICT, "dq_in and dk_in are one buffer");
     if (one_place(dq_in, dk, r) || one_place(dq, dk_in, r) || one_place(dq_in, k, r) || one_place(q, dk_in, r))
         return bad(Q4_ERR_CONFLICT, "a gradient is in the place of the other tensor's operand");

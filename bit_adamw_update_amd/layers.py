@@ -231,8 +231,8 @@ def head_norm_rope_backward(q, k, q_gain, k_gain, positions, frequencies, dq, dk
                             dtype=torch.bfloat16, stream=None) -> tuple:
     """(dq, dk, dq_gain, dk_gain): the gradients of head_norm_rope's q, k and
     gains from its inputs and the gradients dq, dk of its results.  out: the
-    tensors of the first two, which may be dq and dk; gain_grads: those of the
-    others (bfloat16 or float32), to which accumulate adds."""
+    tensors of the first two, which may be dq and dk, or q and k; gain_grads:
+    those of the others (bfloat16 or float32), to which accumulate adds."""
     pq, pk, pdq, pdk = _heads("q", q), _heads("k", k), _heads("dq", dq, q), _heads("dk", dk, k)
     rope = _rope(q, k, q_gain, k_gain, positions, frequencies, eps, interleaved)
     held = [q, k, q_gain, k_gain, positions, frequencies, dq, dk]

@@ -551,9 +551,10 @@ q4_status q4nn_head_norm_rope(const q4nn_rope* r, const q4nn_heads* q, const q4n
                               const q4nn_heads* k_out, void* stream);
 
 /* Its gradients from the inputs q and k and the results' gradients dq and dk:
- * those of q and k in dq_in and dk_in (each may be dq or dk, with the same
- * strides), and those of the gains (dim elements, dtype; with Q4NN_ADD added
- * to what they hold).  A q4_tensor's grad is one of dtype Q4MX_BF16. */
+ * those of q and k in dq_in and dk_in (dq_in may be dq or q, dk_in dk or k,
+ * with the same strides), and those of the gains (dim elements, dtype; with
+ * Q4NN_ADD added to what they hold).  A q4_tensor's grad is one of dtype
+ * Q4MX_BF16. */
 q4_status q4nn_head_norm_rope_backward(const q4nn_rope* r, const q4nn_heads* q, const q4nn_heads* k,
                                        const q4nn_heads* dq, const q4nn_heads* dk, const q4nn_heads* dq_in,
                                        const q4nn_heads* dk_in, void* dq_gain, void* dk_gain, int32_t dtype,

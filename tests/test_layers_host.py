@@ -170,6 +170,17 @@ def test_head_operands_are_checked():
     refused(SHAPE, "overlap", back, dki=view(2, p=5 * P, head=0))
 
 
+def test_gradients_in_the_place_of_an_input_have_its_strides():
+    # q's and k's addresses are P: a permuted view of equal extents, and other strides
+    refused(SHAPE, "in place", back, rope(tokens=4), dqi=view(4, p=P, batch=1024, token=64, head=256))
+    refused(SHAPE, "in place", back, dqi=view(4, p=P, token=300, batch=1500))
+    refused(SHAPE, "in place", back, rope(k_heads=0), dqi=view(4, p=P, token=300, batch=1500))
+    refused(SHAPE, "in place", back, rope(q_heads=0), dki=view(2, p=P, token=300, batch=1500))
+    # with its strides it is not: the next thing to refuse is the workspace
+    refused(WORKSPACE, "NULL", back, rope(k_heads=0), dqi=view(4, p=P), ws=None)
+    refused(WORKSPACE, "NULL", back, rope(q_heads=0), dki=view(2, p=P), ws=None)
+
+
 def drop(p=0.1, step_at=None, offset=0, x=P, ldx=64, res=None, ldr=64, rows=10, cols=64, out=2 * P, ldo=64, dtype=1):
     api.q4nn_dropout(p, 1, 1, step_at, 0, offset, x, ldx, res, ldr, rows, cols, out, ldo, dtype, 0)
 
