@@ -7,7 +7,8 @@
 // (the scale uses that p, so the expectation is exact); 32 bits to an element
 // would double the generator's work, which takes half of the VALU's time now.
 // Memory bounds it: 8192 x 2560 in BF16 15 us, 84 MB at 5.6 TB/s, with a residual
-// 21 us, 126 MB at 6.0.
+// 21 us, 126 MB at 6.0.  Rows with a gap between them: 25 where rows that follow
+// each other take 24 (from memory alone), in FP32 47 and 44.
 #include "q4_exact.h"
 #include "q4_mx_dev.h"
 #include "q4_nn.h"

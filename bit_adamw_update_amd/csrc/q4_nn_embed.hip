@@ -13,7 +13,10 @@ __device__ __forceinline__ int64_t load_id(const Ids& ids, int64_t t) {
 // ---- lookup -----------------------------------------------------------------
 // Rows gathered and scaled: memory (16384 tokens x 2560 from FP32 masters: 31 us,
 // 107 MB read and 84 written at 6.1 TB/s, part of it from the last-level cache;
-// one token's row of E2M1: 1.8 us).  A lane takes 8 columns of a token; lanes
+// from BF16, E4M3 and E2M1 23 us, 52, 48 and 34 MB read where the rows that are
+// named have 31, 16 and 8: several XCDs read the same ones, and a row's scales
+// are 4 bytes of a cache line for every 128 columns; one token's row of E2M1: 1.7
+// us).  A lane takes 8 columns of a token; lanes
 // follow the row-major order of the result, so odd widths leave none idle but
 // at a row's end.
 enum TableKind { TABLE_F32, TABLE_BF16, TABLE_MX };
@@ -68,6 +71,9 @@ constexpr int kSortTile = 1024, kMergeRuns = 16, kShort = 32, kSlab = 512;
 // A sort that needs no merges (RANKED below) where the fill beside it takes
 // longer: kHides bytes of zeros a tile, 1.5 us (8192 tokens into 151936 x 1024:
 // 70.6 us, with merges 75.0; into 1000 x 64, with 16384 tokens: 40.3 and 26.2).
+// Beside less, or added to a gradient, it gains nothing for few tiles either, in a
+// graph: 2, 4, 8 tiles into 2000 x 768 20.0, 23.8, 30.9 us, with merges 19.9, 21.6,
+// 24.2; added to it 20.8, 25.3, 32.2 and 20.6, 23.0, 25.5.
 constexpr int64_t kRanked = 65536, kHides = 12 << 20;
 constexpr int kJoinCols = 256, kJoinPieces = 8, kJoinWaves = 8;
 constexpr uint32_t kNone = 0x80000000u;   // above every id; one more is a number too

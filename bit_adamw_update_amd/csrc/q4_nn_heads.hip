@@ -406,10 +406,12 @@ q4nn_rope flat_batches(const q4nn_rope& r, q4nn_heads* const* v, int n) {
 }
 
 // Pairs to a lane and lanes to a row: 8 (or 4) pairs where both the rotary
-// part and the rest are made of whole vectors, else single ones.  Rows of up to
-// 16 lanes lie side by side as they are where a wave takes more of them so
-// (heads of 80: 12 in place of 8, and 66 us in place of 73 for a prompt of 16001
-// tokens x 64 heads), else padded to a power of two.
+// part and the rest are made of whole vectors, else single ones, in accesses of 2
+// bytes (8192 tokens x 24 heads of 72, forward and backward: 18 + 24 us, with 36
+// elements rotated 50 + 57).  Rows of up to 16 lanes lie side by side as they are
+// where a wave takes more of them so (heads of 80: 12 in place of 8, and 66 us in
+// place of 73 for a prompt of 16001 tokens x 64 heads), else padded to a power of
+// two.
 struct Shape {
     int vec, lanes;
 };

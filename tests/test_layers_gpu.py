@@ -719,7 +719,7 @@ def test_embedding_grad_of_large_tables(tokens, rows, cols, how):
     assert float(got.abs().amax()) == 0
 
 
-# ---- more than a tile's tokens, and few tokens of many columns: not the form in one launch ------
+# ---- more than a tile's tokens, and 1024 tokens of many columns: not the form in one launch ------
 
 @pytest.mark.parametrize("cols", [1, 2, 7, 8, 9, 255, 256, 257, 511, 512, 513, 1030])
 def test_embedding_grad_of_many_tokens_by_columns(cols):
