@@ -74,10 +74,12 @@ q4_status check_heads(const char* name, const q4nn_heads* v, const q4nn_rope* r,
     return Q4_OK;
 }
 
-// Whether a in place of b would be read as another element than it is written.
-bool shifted(const q4nn_heads* a, const q4nn_heads* b, const q4nn_rope* r) {
-    return a->p == b->p && a->p &&
-           ((r->batches > 1 && a->batch != b->batch) || (r->tokens > 1 && a->token != b->token) || a->head != b->head);
+// Whether a in place of b would be read as another element than it is written;
+// the stride of a single entry means nothing.
+bool shifted(const q4nn_heads* a, const q4nn_heads* b, const q4nn_rope* r, int32_t heads) {
+    return a->p == b->p && r->batches * r->tokens * heads > 0 &&
+           ((r->batches > 1 && a->batch != b->batch) || (r->tokens > 1 && a->token != b->token) ||
+            (heads > 1 && a->head != b->head));
 }
 
 // Whether an operand of q and one of k begin in one place.
@@ -186,7 +188,7 @@ q4_status q4nn_head_norm_rope(const q4nn_rope* r, const q4nn_heads* q, const q4n
     Q4_TRY(check_heads("k", k, r, r->k_heads, false));
     Q4_TRY(check_heads("q_out", q_out, r, r->q_heads, true));
     Q4_TRY(check_heads("k_out", k_out, r, r->k_heads, true));
-    if (shifted(q_out, q, r) || shifted(k_out, k, r))
+    if (shifted(q_out, q, r, r->q_heads) || shifted(k_out, k, r, r->k_heads))
         return bad(Q4_ERR_SHAPE, "an output in place of its input must have its strides");
     if (one_place(q_out, k_out, r)) return bad(Q4_ERR_CONFLICT, "q_out and k_out are one buffer");
     if (one_place(q_out, k, r) || one_place(q, k_out, r))
@@ -217,7 +219,8 @@ q4_status q4nn_head_norm_rope_backward(const q4nn_rope* r, const q4nn_heads* q, 
     Q4_TRY(check_heads("dk", dk, r, r->k_heads, false));
     Q4_TRY(check_heads("dq_in", dq_in, r, r->q_heads, true));
     Q4_TRY(check_heads("dk_in", dk_in, r, r->k_heads, true));
-    if (shifted(dq_in, dq, r) || shifted(dk_in, dk, r) || shifted(dq_in, q, r) || shifted(dk_in, k, r))
+    if (shifted(dq_in, dq, r, r->q_heads) || shifted(dq_in, q, r, r->q_heads) || shifted(dk_in, dk, r, r->k_heads) ||
+        shifted(dk_in, k, r, r->k_heads))
         return bad(Q4_ERR_SHAPE, "a gradient in place of the result's or of the input must have its strides");
     if (one_place(dq_in, dk_in, r)) return bad(Q4_ERR_CONFLICT, "dq_in and dk_in are one buffer");
     if (one_place(dq_in, dk, r) || one_place(dq, dk_in, r) || one_place(dq_in, k, r) || one_place(q, dk_in, r))

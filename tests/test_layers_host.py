@@ -181,6 +181,18 @@ def test_gradients_in_the_place_of_an_input_have_its_strides():
     refused(WORKSPACE, "NULL", back, rope(q_heads=0), dki=view(2, p=P), ws=None)
 
 
+def test_strides_of_a_single_head_and_of_none_mean_nothing():
+    def one(**k):
+        return view(1, **{**dict(batch=320, token=64, head=64), **k})
+    r = rope(q_heads=1, k_heads=0)
+    for call in (lambda: api.q4nn_head_norm_rope_backward(r, one(), view(2), one(p=2 * P), view(2), one(p=P, head=0), view(2),
+                                                          P, 2 * P, 1, 0, None, 0, 0),
+                 lambda: api.q4nn_head_norm_rope_backward(r, one(), view(2), one(p=2 * P, head=7), view(2), one(p=2 * P),
+                                                          view(2, p=P, token=999), P, 2 * P, 1, 0, None, 0, 0)):
+        refused(WORKSPACE, "NULL", call)   # the next thing to refuse
+    refused(SHAPE, "in place", api.q4nn_head_norm_rope, r, one(token=65), view(2), one(head=1), view(2), 0)
+
+
 def drop(p=0.1, step_at=None, offset=0, x=P, ldx=64, res=None, ldr=64, rows=10, cols=64, out=2 * P, ldo=64, dtype=1):
     api.q4nn_dropout(p, 1, 1, step_at, 0, offset, x, ldx, res, ldr, rows, cols, out, ldo, dtype, 0)
 
